@@ -316,6 +316,136 @@ int mo_svd_entropy(const mo_matrix* mats, int64_t count, int dtype,
                    double* entropy, double* sigma, void* workspace,
                    size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit matrices ("MX4").
+ *
+ * The image of a matrix X [rows, cols] holds each element as a sign and one
+ * of {0, 0.5, 1, 1.5, 2, 3, 4, 6}, times a power of two shared by 32
+ * consecutive elements of a row (block b: columns 32 b .. 32 b + 31; the
+ * last block may be short).  With nb = ceil(cols / 32):
+ *   codes   uint8 [rows][16 nb]: element (r, c) is the low (c even) or high
+ *           (c odd) half of byte c / 2; bit 3 is the sign, bits 2..0 the
+ *           index into the list above.
+ *   scales  uint8 [rows][4 ceil(nb / 4)]: byte b of a row is e + 127 for
+ *           the block's scale 2^e; 255 makes the block NaN.
+ * Padding (codes of columns >= cols, scales of blocks >= nb) is zero.
+ * codes are 16-byte, scales 4-byte aligned.
+ *
+ * Quantisation: a = the block's largest |x|; e = max(floor(log2 a) - 2,
+ * -127) (byte 0 for a = 0); code = x 2^-e rounded to the nearest value of
+ * the list, halfway cases to the even index, saturating at 6.  A block that
+ * holds a NaN or an infinity gets scale byte 255 and zero codes: its values
+ * read back as NaN, and so does every product they enter.
+ * ---------------------------------------------------------------------- */
+typedef struct mo_mx4_image {
+    const void* codes;
+    const void* scales;
+    int64_t     rows;
+    int64_t     cols;
+} mo_mx4_image;
+
+/* One matrix to quantise.  src [rows, cols], rows `ld` elements apart
+ * (ld >= cols), aligned to its element.  codes / scales: the image of src,
+ * or both NULL.  codes_t / scales_t: the image of its transpose [cols,
+ * rows] (blocks run along src's columns), or both NULL.  One of the two is
+ * needed. */
+typedef struct mo_mx4_item {
+    const void* src;
+    void*       codes;
+    void*       scales;
+    void*       codes_t;
+    void*       scales_t;
+    int64_t     rows;
+    int64_t     cols;
+    int64_t     ld;
+} mo_mx4_item;
+
+/* Bytes of an image's two arrays.  1 <= rows, cols < 2^31 and rows * cols
+ * <= 2^40.  Host-only. */
+int mo_mx4_image_size(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
+
+/* Quantises `count` matrices of one dtype (MO_F32 or MO_BF16) on `stream`,
+ * grouped into few launches.  An output may not overlap a source or another
+ * output.  Results do not depend on the grouping. */
+int mo_mx4_quantize(const mo_mx4_item* items, int64_t count, int dtype, void* stream);
+
+/* The values that `count` images stand for: dst[i] contiguous [rows, cols]
+ * in dtype, 16-byte aligned.  Every value is exact in either dtype (those of
+ * 2^128 and more, which only images of another origin hold, become inf). */
+int mo_mx4_dequantize(const mo_mx4_image* images, void* const* dst, int64_t count, int dtype,
+                      void* stream);
+
+/* out[m, n] = sum_k a[m, k] b[n, k] over the values of two images with the
+ * same cols (a [M, K], b [N, K]), + out[m, n] when accumulate != 0.
+ * Products enter fp32 sums on the matrix cores; the result (after the
+ * accumulation) is rounded once to out_dtype (MO_F32 or MO_BF16).  out: rows
+ * ldo elements apart (ldo >= N), aligned to its element; columns N .. ldo - 1
+ * are left as they were.  out may not overlap an image.  Results do not
+ * depend on the run (no atomics).  M, N, K < 2^31. */
+int mo_mx4_matmul(const mo_mx4_image* a, const mo_mx4_image* b, void* out, int out_dtype,
+                  int64_t ldo, int accumulate, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Token log probabilities and distillation.
+ *
+ * logits [rows, vocab] (MO_F32 or MO_BF16), rows `ld` elements apart
+ * (ld >= vocab), aligned to the element; columns vocab .. ld - 1 are never
+ * read.  1 <= vocab < 2^31, 0 <= rows < 2^22.  z = logits / temperature with
+ * a finite temperature > 0.  Statistics are fp32, and their sums run in a
+ * fixed order: results do not depend on the run.
+ * ---------------------------------------------------------------------- */
+#define MO_MAX_TOP 128
+
+/* Workspace of mo_token_logprobs and mo_distill_loss (may be 0: then the
+ * workspace may be NULL).  Host-only. */
+int mo_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int top, size_t* bytes);
+int mo_distill_loss_workspace_size(int64_t rows, int64_t vocab, int top, size_t* bytes);
+
+/* Per row: with l_j = z_j - log sum_i exp z_i,
+ *   logprob[r] = l_t of t = tokens[r]; 0 for a negative token (a position
+ *       that is not scored), NaN for a token >= vocab;
+ *   entropy[r] = -sum_j exp(l_j) l_j in nats (terms with exp(l_j) = 0 are 0);
+ *   top_index[r, i], top_logprob[r, i], i < top: the columns with the
+ *       largest logits, largest first, ties to the lower column (NaN above
+ *       everything, -0 equal to +0), and their l_j.
+ * -inf logits are tokens of probability zero.  A row that holds a NaN or
+ * +inf, or only -inf, has NaN logprob (scored tokens), entropy and
+ * top_logprob.
+ * tokens: device int64 [rows], logprob: fp32 [rows]: both or neither NULL.
+ * entropy: fp32 [rows] or NULL.  top in [0, min(vocab, MO_MAX_TOP)];
+ * top_index int64 and top_logprob fp32 [rows, top], NULL iff top = 0.
+ * Outputs may not overlap each other, an input or the workspace. */
+int mo_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                      const int64_t* tokens, float temperature, float* logprob, float* entropy,
+                      int top, int64_t* top_index, float* top_logprob,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits.  Row r's teacher gives `top`
+ * slots (top_index[r, k], top_logit[r, k]) (1 <= top <= MO_MAX_TOP); a
+ * negative index is an absent slot.  With p the softmax of top_logit /
+ * temperature over the row's present slots and q the softmax of z,
+ *   loss[r] = temperature^2 sum_k p_k (log p_k - log q_{i_k}),
+ *   grad[r, j] = g_r dloss[r] / dlogits[r, j]
+ *              = g_r temperature (q_j - sum_{k: i_k = j} p_k),
+ * g = grad_loss (fp32 [rows], the gradient that reaches each loss), 1 when
+ * NULL.  Terms with p_k = 0 are 0; a column named twice counts twice.  One
+ * slot per row makes the loss the cross entropy of that label (at
+ * temperature 1).
+ * A row without present slots, or whose present top_logits are all -inf, is
+ * skipped: loss 0 and zero gradient whatever its logits.  g_r = 0 gives a
+ * zero gradient whatever the logits.  A present slot with an index >= vocab
+ * or a NaN or +inf top_logit makes the row's loss and gradient NaN; so does,
+ * in a row that is not skipped, a NaN or +inf logit or a row of -inf only.
+ * A teacher's token at logit -inf makes its row's loss +inf.
+ * loss: fp32 [rows] or NULL.  grad: [rows, vocab] in the logits' dtype, rows
+ * ld_grad elements apart, or NULL (then grad_loss is not read); columns
+ * vocab .. ld_grad - 1 are left as they were.  One of the two is needed.
+ * Outputs may not overlap each other, an input or the workspace. */
+int mo_distill_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                    const int64_t* top_index, const float* top_logit, int top,
+                    float temperature, const float* grad_loss, float* loss, void* grad,
+                    int64_t ld_grad, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Kernel classes for the timing counters below. */
 typedef enum mo_kernel_class {
     MO_K_MOMENTUM = 0,     /* momentum + Nesterov + norm partials + X_0 copy */
@@ -332,7 +462,12 @@ typedef enum mo_kernel_class {
     MO_K_SVD_COLUMN = 11,  /* SVD entropy: per-step reflector (one WG/matrix) */
     MO_K_SVD_EIG = 12,     /* SVD entropy: bisection, entropy and sigma      */
     MO_K_SVD_PANEL = 13,   /* SVD entropy: deferred rank-2 updates of a panel */
-    MO_K_COUNT = 14
+    MO_K_MX4_QUANT = 14,   /* MX4 quantisation (bytes moved)                 */
+    MO_K_MX4_DEQUANT = 15, /* MX4 images read back (bytes moved)             */
+    MO_K_MX4_MATMUL = 16,  /* MX4 product (flops)                            */
+    MO_K_LOGPROBS = 17,    /* token log probabilities (bytes moved)          */
+    MO_K_DISTILL = 18,     /* distillation loss and gradient (bytes moved)   */
+    MO_K_COUNT = 19
 } mo_kernel_class;
 
 /* Timing counters.  mo_profile_enable(mask): for every class k with bit k

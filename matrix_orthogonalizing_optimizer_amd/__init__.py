@@ -6,6 +6,11 @@ normalisation and quintic Newton-Schulz (Eq. 2), the 0.2 * sqrt(max(A, B))
 shape scale with decoupled weight decay (section 2.2, Eq. 4), and AdamW with
 the same learning rate and decay for non-matrix parameters.
 
+Next to the step stand the operators that a 4-bit student of the trained
+weights needs: microscaled 4-bit images of matrices and their products
+(``mx4_*``), token log probabilities with the top alternatives, and the
+distillation loss with its gradient.
+
 This module only marshals torch tensors into the C ABI of ``libmuon.so``
 (``include/muon.h``); PyTorch provides device memory and streams.  Every
 arithmetic step runs in the HIP library, and there is no fallback.
@@ -13,16 +18,19 @@ arithmetic step runs in the HIP library, and there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
-from typing import Iterable, List, Optional, Sequence, Tuple
+from typing import Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
-from ._lib import (KERNEL_CLASS_NAMES, MO_BF16, MO_F32, MoMatrix, MoTensor,  # noqa: F401
-                   MuonError, check, last_error, lib)
+from ._lib import (KERNEL_CLASS_NAMES, MO_BF16, MO_F32, MO_MAX_TOP, MoMatrix, MoMx4Image,  # noqa: F401
+                   MoMx4Item, MoTensor, MuonError, check, last_error, lib)
 
 __all__ = ["muon_step", "adamw_step", "newton_schulz", "muon_workspace_size",
            "newton_schulz_workspace_size", "svd_entropy", "svd_entropy_workspace_size",
+           "Mx4Matrix", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear",
+           "mx4_linear_backward", "TokenLogprobs", "token_logprobs", "distill_loss",
            "MuonPlan", "MuonAdamW", "profile_enable", "profile_read", "profile_reset",
            "MuonError", "KERNEL_CLASS_NAMES"]
 
@@ -346,6 +354,317 @@ def svd_entropy(mats: Sequence[torch.Tensor], *, sigma: bool = False,
     if not sigma:
         return ent
     return ent, list(torch.split(sig, counts))
+
+
+# ---------------------------------------------------------------- 4-bit matrices
+@contextlib.contextmanager
+def _launch_on(device: torch.device, stream, tensors: Sequence[Optional[torch.Tensor]]):
+    """Device and stream of one call: outputs made inside belong to that
+    stream, and ``tensors`` used on another stream than the current one are
+    recorded on it, so that the allocator keeps their memory until then."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors of one call must share a device, got {t.device} and {device}")
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    with torch.cuda.device(device):
+        here = torch.cuda.current_stream(device)
+        handle = _stream_handle(device, stream)
+        if handle == here.cuda_stream:
+            yield handle
+            return
+        other = torch.cuda.ExternalStream(handle, device=device)
+        with torch.cuda.stream(other):
+            yield handle
+        for t in tensors:
+            if t is not None:
+                t.record_stream(other)
+
+
+def _rows_of(t: torch.Tensor, what: str) -> Tuple[int, int, int, int]:
+    """(pointer, rows, cols, row stride) of a 2-D tensor with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D, got shape {tuple(t.shape)}")
+    r, c = (int(v) for v in t.shape)
+    ld = int(t.stride(0)) if r > 1 else max(c, 1)
+    if (c > 1 and t.stride(1) != 1) or ld < c:
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap (strides {t.stride()})")
+    return t.data_ptr(), r, c, ld
+
+
+def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, shape: Tuple[int, ...], what: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _scratch(nbytes: int, handle: int, device: torch.device) -> Optional[torch.Tensor]:
+    """Workspace of one call: the cached one of (device, stream), or, while a
+    graph is being captured, memory of that graph alone."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _workspace(device, nbytes, handle)
+
+
+class Mx4Matrix:
+    """The microscaled 4-bit image of a [rows, cols] matrix: ``codes`` uint8
+    [rows, 16 nb] and ``scales`` uint8 [rows, 4 ceil(nb / 4)] with nb =
+    ceil(cols / 32) blocks per row, as ``include/muon.h`` lays them out."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        if codes.dim() != 2:
+            raise ValueError("codes must be 2-D")
+        rows, nb = int(codes.shape[0]), -(-int(cols) // 32)
+        if cols < 1 or rows < 1:
+            raise ValueError("an image has at least one row and one column")
+        for t, w, what in ((codes, 16 * nb, "codes"), (scales, -(-nb // 4) * 4, "scales")):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (rows, w) or not t.is_contiguous():
+                raise ValueError(f"{what} of a [{rows}, {cols}] image must be contiguous uint8 "
+                                 f"[{rows}, {w}], got {t.dtype} {tuple(t.shape)}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must share a device")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, int(cols)
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.rows, self.cols
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "Mx4Matrix":
+        """An image whose contents are still to be written."""
+        if rows < 1 or cols < 1:
+            raise ValueError(f"an image has at least one row and one column, got [{rows}, {cols}]")
+        nb = -(-cols // 32)
+        return cls(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
+                   torch.empty(rows, -(-nb // 4) * 4, dtype=torch.uint8, device=device), cols)
+
+    def _struct(self) -> MoMx4Image:
+        return MoMx4Image(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+
+    def __repr__(self) -> str:
+        return f"Mx4Matrix([{self.rows}, {self.cols}], device={self.device})"
+
+
+_IMAGES = ("rows", "cols", "both")
+
+
+def mx4_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str = "rows",
+                 out=None, stream=None):
+    """4-bit images of a 2-D matrix or of a list of them (``mo_mx4_quantize``;
+    fp32 or bf16, one dtype; rows may be strided).
+
+    ``images``: "rows" -- the image of x (blocks along its rows); "cols" --
+    the image of x^T (blocks along x's columns); "both" -- the pair of them,
+    from one reading of x.  A list gives a list.  ``out``: images of an
+    earlier call (same form) to overwrite.
+    """
+    if images not in _IMAGES:
+        raise ValueError(f"images must be one of {_IMAGES}")
+    single = isinstance(x, torch.Tensor)
+    xs = [x] if single else list(x)
+    if not xs:
+        return []
+    outs = None if out is None else ([out] if single else list(out))
+    if outs is not None and len(outs) != len(xs):
+        raise ValueError(f"out has {len(outs)} entries for {len(xs)} matrices")
+    dt = _dtype_code(_common_dtype(xs, "x"), "x")
+    dev = xs[0].device
+    views = [_rows_of(t, "x") for t in xs]
+    given = []                                   # (image, transposed image) of each matrix
+    if outs is not None:
+        for (_, r, c, _), o in zip(views, outs):
+            pair = tuple(o) if images == "both" else (o, None) if images == "rows" else (None, o)
+            if len(pair) != 2:
+                raise ValueError('out must hold pairs for images="both"')
+            for q, shape in zip(pair, ((r, c), (c, r))):
+                if q is not None and not isinstance(q, Mx4Matrix):
+                    raise TypeError("out must hold Mx4Matrix")
+                if q is not None and q.shape != shape:
+                    raise ValueError(f"out: expected an image of {shape}, got {q.shape}")
+            if (images != "cols" and pair[0] is None) or (images != "rows" and pair[1] is None):
+                raise ValueError("out lacks an image")
+            given.append(pair)
+    used = xs + [t for p in given for q in p if q is not None for t in (q.codes, q.scales)]
+    with _launch_on(dev, stream, used) as handle:
+        if outs is None:
+            given = [(Mx4Matrix.empty(r, c, dev) if images != "cols" else None,
+                      Mx4Matrix.empty(c, r, dev) if images != "rows" else None) for _, r, c, _ in views]
+        arr = (MoMx4Item * len(xs))()
+        for it, (ptr, r, c, ld), (q, qt) in zip(arr, views, given):
+            it.src, it.rows, it.cols, it.ld = ptr, r, c, ld
+            if q is not None:
+                it.codes, it.scales = q.codes.data_ptr(), q.scales.data_ptr()
+            if qt is not None:
+                it.codes_t, it.scales_t = qt.codes.data_ptr(), qt.scales.data_ptr()
+        check(lib().mo_mx4_quantize(arr, len(xs), dt, handle))
+    res = [p if images == "both" else p[0] if images == "rows" else p[1] for p in given]
+    return res[0] if single else res
+
+
+def mx4_dequantize(q: Union[Mx4Matrix, Sequence[Mx4Matrix]], *, dtype: torch.dtype = torch.bfloat16,
+                   stream=None):
+    """The values that an image, or each of a list, stands for (``mo_mx4_dequantize``)."""
+    single = isinstance(q, Mx4Matrix)
+    qs = [q] if single else list(q)
+    dt = _dtype_code(dtype, "dtype")
+    if not qs:
+        return []
+    dev = qs[0].device
+    with _launch_on(dev, stream, [t for i in qs for t in (i.codes, i.scales)]) as handle:
+        res = [torch.empty(i.shape, dtype=dtype, device=dev) for i in qs]
+        arr = (MoMx4Image * len(qs))(*[i._struct() for i in qs])
+        ptrs = (ctypes.c_void_p * len(qs))(*[t.data_ptr() for t in res])
+        check(lib().mo_mx4_dequantize(arr, ptrs, len(qs), dt, handle))
+    return res[0] if single else res
+
+
+def mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """``a b^T`` over the values of two images with equal columns
+    (``mo_mx4_matmul``): a [M, K], b [N, K] give [M, N], fp32 sums rounded
+    once.  ``out``: written instead of a new tensor (its dtype counts, rows
+    may be strided); with ``accumulate`` the product is added to it."""
+    if not isinstance(a, Mx4Matrix) or not isinstance(b, Mx4Matrix):
+        raise TypeError("a and b must be Mx4Matrix")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    dt = _dtype_code(out_dtype if out is None else out.dtype, "out")
+    used = [a.codes, a.scales, b.codes, b.scales, out]
+    with _launch_on(a.device, stream, used) as handle:
+        if out is None:
+            out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.device)
+        ptr, r, c, ld = _rows_of(out, "out")
+        if (r, c) != (a.rows, b.rows):
+            raise ValueError(f"out must be [{a.rows}, {b.rows}], got [{r}, {c}]")
+        sa, sb = a._struct(), b._struct()
+        check(lib().mo_mx4_matmul(ctypes.byref(sa), ctypes.byref(sb), ptr, dt, ld, int(accumulate), handle))
+    return out
+
+
+def _flat2(x: torch.Tensor) -> torch.Tensor:
+    return x if x.dim() == 2 else x.view(-1, x.shape[-1])
+
+
+def mx4_linear(x: torch.Tensor, w: Mx4Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
+               save: bool = False, stream=None):
+    """``y = x W^T`` with W [N, K] held in 4 bits and x [..., K] (fp32 or
+    bf16) quantised on the way.  ``save=True`` also returns the image of x^T
+    that :func:`mx4_linear_backward` takes."""
+    x2 = _flat2(x)
+    if x2.shape[1] != w.cols:
+        raise ValueError(f"x has {x2.shape[1]} features, the weights {w.cols}")
+    if x2.shape[0] == 0 and not save:
+        return torch.empty(*x.shape[:-1], w.rows, dtype=out_dtype, device=x.device)
+    if save:
+        xq, x_t = mx4_quantize(x2, images="both", stream=stream)
+    else:
+        xq = mx4_quantize(x2, stream=stream)
+    y = mx4_matmul(xq, w, out_dtype=out_dtype, stream=stream)
+    y = y if x.dim() == 2 else y.view(*x.shape[:-1], w.rows)
+    return (y, x_t) if save else y
+
+
+def mx4_linear_backward(dy: torch.Tensor, x_t: Mx4Matrix, w_t: Mx4Matrix, *,
+                        dx_dtype: torch.dtype = torch.bfloat16, dw: Optional[torch.Tensor] = None,
+                        accumulate: bool = False, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dW) of ``y = x W^T`` from dy [..., N] (fp32 or bf16), the image of
+    x^T [K, tokens] and the image of W^T [K, N]: dy is quantised along both of
+    its axes, dx = dy W contracts over N and dW = dy^T x over the tokens.  The
+    rounding of x and W passes gradients straight through.  dW is fp32 [N, K]
+    unless ``dw`` gives it; ``accumulate`` adds to ``dw``."""
+    d2 = _flat2(dy)
+    if d2.shape[0] != x_t.cols or d2.shape[1] != w_t.cols:
+        raise ValueError(f"dy is {tuple(d2.shape)}, the images want [{x_t.cols}, {w_t.cols}]")
+    dq, dq_t = mx4_quantize(d2, images="both", stream=stream)
+    dx = mx4_matmul(dq, w_t, out_dtype=dx_dtype, stream=stream)
+    dw = mx4_matmul(dq_t, x_t, out_dtype=torch.float32, out=dw, accumulate=accumulate, stream=stream)
+    return dx if dy.dim() == 2 else dx.view(*dy.shape[:-1], w_t.rows), dw
+
+
+# ------------------------------------------------- log probabilities, distillation
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]       # fp32 [rows], None without tokens
+    entropy: torch.Tensor                 # fp32 [rows], nats
+    top_logprob: torch.Tensor             # fp32 [rows, top]
+    top_index: torch.Tensor               # int64 [rows, top]
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top: int = 0,
+                   temperature: float = 1.0, stream=None) -> TokenLogprobs:
+    """Log probability of ``tokens`` (int64 [rows], negative: not scored, 0),
+    entropy and the ``top`` likeliest columns of softmax(logits /
+    temperature), logits fp32 or bf16 [rows, vocab] (``mo_token_logprobs``;
+    rows may be strided)."""
+    ptr, rows, vocab, ld = _rows_of(logits, "logits")
+    dt, dev = _dtype_code(logits.dtype, "logits"), logits.device
+    tok = _vector(tokens, torch.int64, (rows,), "tokens")
+    need = ctypes.c_size_t()
+    check(lib().mo_token_logprobs_workspace_size(rows, vocab, top, ctypes.byref(need)))
+    with _launch_on(dev, stream, [logits, tokens]) as handle:
+        lp = torch.empty(rows, dtype=torch.float32, device=dev) if tokens is not None else None
+        ent = torch.empty(rows, dtype=torch.float32, device=dev)
+        tlp = torch.empty(rows, top, dtype=torch.float32, device=dev)
+        tix = torch.empty(rows, top, dtype=torch.int64, device=dev)
+        if rows:
+            ws = _scratch(need.value, handle, dev)
+            check(lib().mo_token_logprobs(ptr, dt, rows, vocab, ld, tok, temperature,
+                                          lp.data_ptr() if lp is not None else None, ent.data_ptr(), top,
+                                          tix.data_ptr() if top else None, tlp.data_ptr() if top else None,
+                                          ws.data_ptr() if ws is not None else None,
+                                          ws.numel() if ws is not None else 0, handle))
+    return TokenLogprobs(lp, ent, tlp, tix)
+
+
+def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_logit: torch.Tensor, *,
+                 temperature: float = 1.0, grad_loss: Optional[torch.Tensor] = None, grad: bool = True,
+                 out_grad: Optional[torch.Tensor] = None, stream=None):
+    """Distillation from a teacher's top logits (``mo_distill_loss``): loss
+    fp32 [rows] = temperature^2 KL(teacher's softmax over its slots ||
+    softmax(logits / temperature)), and the gradient for ``logits`` [rows,
+    vocab] (fp32 or bf16) in its dtype, (loss, None) with ``grad=False``.
+
+    ``top_index`` int64 [rows, k] (negative: absent slot; a row without slots
+    is skipped) and ``top_logit`` fp32 [rows, k] -- ``top_index`` and
+    ``top_logprob`` of :func:`token_logprobs` on the teacher serve as they
+    are.  ``grad_loss`` fp32 [rows]: the gradient that reaches each row's
+    loss (1 when None).  ``out_grad``: written instead of a new tensor."""
+    ptr, rows, vocab, ld = _rows_of(logits, "logits")
+    dt, dev = _dtype_code(logits.dtype, "logits"), logits.device
+    if top_index.dim() != 2:
+        raise ValueError("top_index must be [rows, k]")
+    k = int(top_index.shape[1])
+    ti = _vector(top_index, torch.int64, (rows, k), "top_index")
+    tl = _vector(top_logit, torch.float32, (rows, k), "top_logit")
+    gl = _vector(grad_loss, torch.float32, (rows,), "grad_loss")
+    if out_grad is not None:
+        if not grad:
+            raise ValueError("out_grad given with grad=False")
+        if out_grad.dtype != logits.dtype or tuple(out_grad.shape) != (rows, vocab):
+            raise ValueError(f"out_grad must be {logits.dtype} [{rows}, {vocab}]")
+    need = ctypes.c_size_t()
+    check(lib().mo_distill_loss_workspace_size(rows, vocab, k, ctypes.byref(need)))
+    with _launch_on(dev, stream, [logits, top_index, top_logit, grad_loss, out_grad]) as handle:
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        g = out_grad
+        if grad and g is None:
+            g = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
+        gp, _, _, ldg = _rows_of(g, "out_grad") if grad else (None, 0, 0, 0)
+        if rows:
+            ws = _scratch(need.value, handle, dev)
+            check(lib().mo_distill_loss(ptr, dt, rows, vocab, ld, ti, tl, k, temperature, gl, loss.data_ptr(),
+                                        gp, ldg, ws.data_ptr() if ws is not None else None,
+                                        ws.numel() if ws is not None else 0, handle))
+    return loss, g
 
 
 def profile_enable(classes: Iterable[str] = ()) -> None:

@@ -18,10 +18,13 @@ MO_F32, MO_BF16 = 0, 1
 MO_SCALE_SHAPE, MO_SCALE_HIDDEN, MO_SCALE_UPDATE_NORM = 0, 1, 2
 (MO_K_MOMENTUM, MO_K_NORM, MO_K_GRAM, MO_K_POLY, MO_K_UPDATE, MO_K_APPLY,
  MO_K_APPLY_X0, MO_K_RMS, MO_K_ADAMW, MO_K_SVD_GRAM, MO_K_SVD_REDUCE,
- MO_K_SVD_COLUMN, MO_K_SVD_EIG, MO_K_SVD_PANEL) = range(14)
+ MO_K_SVD_COLUMN, MO_K_SVD_EIG, MO_K_SVD_PANEL, MO_K_MX4_QUANT, MO_K_MX4_DEQUANT,
+ MO_K_MX4_MATMUL, MO_K_LOGPROBS, MO_K_DISTILL) = range(19)
+MO_MAX_TOP = 128
 KERNEL_CLASS_NAMES = ["momentum", "norm", "gram", "poly", "update", "apply",
                       "apply_x0", "rms", "adamw", "svd_gram", "svd_reduce",
-                      "svd_column", "svd_eig", "svd_panel"]
+                      "svd_column", "svd_eig", "svd_panel", "mx4_quant", "mx4_dequant",
+                      "mx4_matmul", "logprobs", "distill"]
 
 STATUS_NAMES = {MO_OK: "MO_OK", MO_EINVAL: "MO_EINVAL",
                 MO_EUNSUPPORTED: "MO_EUNSUPPORTED",
@@ -36,6 +39,17 @@ class MoTensor(ctypes.Structure):
 
 class MoMatrix(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class MoMx4Image(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class MoMx4Item(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("codes_t", ctypes.c_void_p), ("scales_t", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64)]
 
 
 class MuonError(RuntimeError):
@@ -78,6 +92,20 @@ _SIGS = {
                                                  _c.POINTER(_c.c_size_t), _c.POINTER(_c.c_size_t)]),
     "mo_svd_entropy": (_c.c_int, [_c.POINTER(MoMatrix), _c.c_int64, _c.c_int, _P, _P, _P,
                                   _c.c_size_t, _P]),
+    "mo_mx4_image_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.POINTER(_c.c_size_t),
+                                     _c.POINTER(_c.c_size_t)]),
+    "mo_mx4_quantize": (_c.c_int, [_c.POINTER(MoMx4Item), _c.c_int64, _c.c_int, _P]),
+    "mo_mx4_dequantize": (_c.c_int, [_c.POINTER(MoMx4Image), _c.POINTER(_P), _c.c_int64, _c.c_int, _P]),
+    "mo_mx4_matmul": (_c.c_int, [_c.POINTER(MoMx4Image), _c.POINTER(MoMx4Image), _P, _c.c_int,
+                                 _c.c_int64, _c.c_int, _P]),
+    "mo_token_logprobs_workspace_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.c_int,
+                                                    _c.POINTER(_c.c_size_t)]),
+    "mo_distill_loss_workspace_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.c_int,
+                                                  _c.POINTER(_c.c_size_t)]),
+    "mo_token_logprobs": (_c.c_int, [_P, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _P, _c.c_float,
+                                     _P, _P, _c.c_int, _P, _P, _P, _c.c_size_t, _P]),
+    "mo_distill_loss": (_c.c_int, [_P, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _P, _P, _c.c_int,
+                                   _c.c_float, _P, _P, _P, _c.c_int64, _P, _c.c_size_t, _P]),
     "mo_profile_enable": (_c.c_int, [_c.c_uint]),
     "mo_profile_read": (_c.c_int, [_c.c_int, _c.POINTER(_c.c_int64), _c.POINTER(_c.c_double),
                                    _c.POINTER(_c.c_double)]),
