@@ -168,6 +168,8 @@ int matmul(const mo_mx4_image* a, const mo_mx4_image* b, void* out, int out_dtyp
   if ((rc = check_image(*a, "operand", 0)) || (rc = check_image(*b, "operand", 1))) return rc;
   if (a->cols != b->cols)
     return fail(MO_EINVAL, "operands have %lld and %lld columns: the contraction needs equal ones", ll(a->cols), ll(b->cols));
+  if (a->cols > kMx4MaxCols) return fail(MO_EINVAL, "operands have %lld columns, more than 2^25", ll(a->cols));
+  if (!mx4_matmul_fits(a->rows, b->rows)) return fail(MO_EINVAL, "too many output tiles for one launch");
   const int esz = esz_of(out_dtype);
   if (!out || !aligned(out, esz)) return fail(MO_EINVAL, "out must be non-NULL and aligned to its element");
   if (ldo < b->rows || ldo > (int64_t{1} << 40) / a->rows)

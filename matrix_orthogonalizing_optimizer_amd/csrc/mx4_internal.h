@@ -45,7 +45,12 @@ struct Mx4MatmulArgs {
   int nb;                // blocks per row of a and b
   int sp;                // bytes per row of scales
   int accumulate;
+  int tiles_m, tiles_n;  // filled in at the launch
 };
+
+// A product's 32-bit offsets cover 256 rows of an image.
+constexpr int64_t kMx4MaxCols = int64_t{1} << 25;
+bool mx4_matmul_fits(int64_t m, int64_t n);
 
 int64_t mx4_quant_tiles(int64_t rows, int64_t cols, bool row_image, bool col_image);
 int64_t mx4_dequant_tiles(int64_t rows, int64_t cols);
