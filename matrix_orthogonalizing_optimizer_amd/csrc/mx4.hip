@@ -158,27 +158,39 @@ __device__ __forceinline__ f32x16v mfma32(u32x4v a, u32x4v b, f32x16v c, uint32_
                                                          static_cast<int>(sb));
 }
 
+// Waits until at most `kLeft` of this wave's loads are outstanding, and for
+// its LDS reads.
+template <int kLeft>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(kLeft < 64, "the counter has 6 bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLeft) & (kWaitLgkm0 | (63 & 15) | (3 << 14)));
+  asm volatile("" ::: "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void store_out(T* o, float v, int accumulate) {
   if (accumulate) v += to_f(*o);
   *o = static_cast<T>(v);
 }
 
-// Tile kernel.  The contraction is cut into super-stages of 32 blocks (1024
-// columns) of up to four stages of 8 blocks.  Any order of the blocks is
-// right as long as A and B agree, so lanes 0..31 of a wave take the first
-// half of a super-stage and lanes 32..63 the second: a lane's scale bytes of
-// a super-stage are then 16 consecutive bytes (one load), a dword per stage,
-// a byte per instruction.  In the last, partial super-stage the halves are h
-// = 4, 8, 12 or 16 blocks.  Blocks past the end load the last block's codes
-// under zero scale bytes in both operands: 2^-254 of a value of at most 36
-// is zero in fp32.
-// LDS holds two stages; a row of a stage is 8 chunks of 16 bytes, stored at
-// chunk ^ (row & 7) so that the 8 rows of a fragment read touch all banks.
-// Stage t + 2 is requested once every wave has read stage t, during the last
-// of its four steps, while the first fragments of t + 1 are read: one
-// barrier per stage, no wait on memory unless it is late by a whole stage.
-constexpr int kTileChunk = 128;        // bytes of a row in one stage
+// Tile kernel.  The contraction runs in stages of 4 blocks (128 columns):
+// two instructions per output fragment, lanes 0..31 of a wave taking the
+// stage's first two blocks and lanes 32..63 the others (any order of blocks
+// is right as long as A and B agree).  LDS holds NST stages of both operands
+// and their scale dwords, filled by loads that bypass the registers:
+//   * scale bytes come for four stages at a time (16 bytes of a row): a
+//     request of 4 bytes per row costs as many cache lookups as the codes;
+//   * a row of a stage is 4 chunks of 16 bytes, stored at chunk ^ ((row / 4)
+//     & 3): the 16 rows that a 16-byte read serves at a time then touch each
+//     of the 64 banks once;
+//   * at the second step of stage t the wave waits for its requests of stage
+//     t + 1, the workgroup meets, and stage t's place is requested again for
+//     stage t + NST while the first fragments of t + 1 are read.  Products,
+//     reads and requests are interleaved one by one.
+// Blocks past the end load the last block's codes under zero scale bytes in
+// both operands: 2^-254 of a value of at most 36 is zero in fp32.
+constexpr int kStageRow = 64;          // bytes of a row in one stage
 
 // A wave-uniform address, said to be one.
 __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
@@ -188,12 +200,15 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
 }
 
-template <int TM, int TN, int WM, int WN, typename T>
-__global__ void __launch_bounds__(64 * WM * WN, 1) mx4_tile_kernel(const Mx4MatmulArgs p) {
+template <int TM, int TN, int WM, int WN, int NST, typename T>
+__global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4MatmulArgs p) {
   constexpr int NW = WM * WN, FM = TM / (32 * WM), FN = TN / (32 * WN);
-  constexpr int DA = TM / (8 * NW), DB = TN / (8 * NW);
-  constexpr int kStage = (TM + TN) * kTileChunk;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+  constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW);      // code requests of a wave and stage
+  constexpr int SA = TM / 64, SB = TN / 64;                    // scale requests of a group of stages
+  constexpr int DPW = DA + DB;
+  constexpr int kStage = (TM + TN) * kStageRow, kScales = NST * kStage, kGroup = (TM + TN) * 16;
+  static_assert(SA <= NW && SB <= NW, "one scale request of each operand per wave (some waves repeat one)");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * kStage + kGroup + 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int r32 = lane & 31, half = lane >> 5;
@@ -213,123 +228,176 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx4_tile_kernel(const Mx4Matm
     tn = __builtin_amdgcn_readfirstlane(static_cast<int>(in / rows));
   }
   const int64_t m0 = static_cast<int64_t>(tm) * TM, n0 = static_cast<int64_t>(tn) * TN;
-  const uint32_t pitch = static_cast<uint32_t>(p.nb) * 16u;
-  const uint8_t* a0 = p.a + m0 * pitch;
-  const uint8_t* b0 = p.b + n0 * pitch;
-  const uint8_t* sa0 = p.sa + m0 * p.sp;
-  const uint8_t* sb0 = p.sb + n0 * p.sp;
+  const uint32_t pitch = static_cast<uint32_t>(p.nb) * 16u, sp = static_cast<uint32_t>(p.sp);
+  const uint8_t* a0 = uniform_ptr(p.a + m0 * pitch);
+  const uint8_t* b0 = uniform_ptr(p.b + n0 * pitch);
+  const uint8_t* sa0 = uniform_ptr(p.sa + m0 * sp);
+  const uint8_t* sb0 = uniform_ptr(p.sb + n0 * sp);
   const int mlast = static_cast<int>(min(static_cast<int64_t>(TM), p.m - m0)) - 1;
   const int nlast = static_cast<int>(min(static_cast<int64_t>(TN), p.n - n0)) - 1;
+  const int stages = (p.nb + 3) / 4;
 
-  // rows past the end repeat the last row; their products are not stored
+  // Requests.  Lane l of a code request copies chunk l & 3 of row l / 4 of 16
+  // rows, so it fetches the chunk that is stored there; rows past the end
+  // repeat the last row (their products are not stored).
+  const int chunk = (lane & 3) ^ (lane >> 4);
   uint32_t arow[DA], brow[DB];
 #pragma unroll
-  for (int i = 0; i < DA; ++i) arow[i] = min(8 * (wave * DA + i) + lane / 8, mlast) * pitch;
+  for (int i = 0; i < DA; ++i) arow[i] = min(16 * (wave * DA + i) + lane / 4, mlast) * pitch + chunk * 16;
 #pragma unroll
-  for (int i = 0; i < DB; ++i) brow[i] = min(8 * (wave * DB + i) + lane / 8, nlast) * pitch;
-  uint32_t asrow[FM], bsrow[FN];
-#pragma unroll
-  for (int f = 0; f < FM; ++f) asrow[f] = min(wm * (TM / WM) + 32 * f + r32, mlast) * static_cast<uint32_t>(p.sp);
-#pragma unroll
-  for (int f = 0; f < FN; ++f) bsrow[f] = min(wn * (TN / WN) + 32 * f + r32, nlast) * static_cast<uint32_t>(p.sp);
-
-  const int full = p.nb / 32, rest = p.nb % 32;
-  const int htail = (rest + 7) / 8 * 4;                // blocks in a half of the last super-stage
-  const int stages = 4 * full + htail / 4;
-
-  const int slot = (lane & 7) ^ (lane >> 3);           // the chunk this lane fetches
-  auto request = [&](int t) __attribute__((always_inline)) {
-    t = __builtin_amdgcn_readfirstlane(t);
-    const uint8_t *pa = uniform_ptr(a0), *pb = uniform_ptr(b0);
-    const int h = t < 4 * full ? 16 : htail;
-    const int blk = (t >> 2) * 32 + (t & 3) * 4 + (slot < 4 ? slot : h + slot - 4);
-    const uint32_t off = static_cast<uint32_t>(min(blk, p.nb - 1)) * 16u;
-    const uint32_t base = lds_addr(smem) + (t & 1) * kStage;
-#pragma unroll
-    for (int i = 0; i < DA; ++i) lds_dma16(pa, arow[i] + off, base + (wave * DA + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < DB; ++i) lds_dma16(pb, brow[i] + off, base + TM * kTileChunk + (wave * DB + i) * 1024);
+  for (int i = 0; i < DB; ++i) brow[i] = min(16 * (wave * DB + i) + lane / 4, nlast) * pitch + chunk * 16;
+  const uint32_t asrow = min(64 * (wave % SA) + lane, mlast) * sp, bsrow = min(64 * (wave % SB) + lane, nlast) * sp;
+  const uint32_t lds0 = lds_addr(smem);
+  // one of the wave's requests of stage t into the place at byte `to`
+  auto request = [&](auto I, int t, uint32_t back, uint32_t to) __attribute__((always_inline)) {
+    constexpr int i = I;
+    if constexpr (i < DA) lds_dma16(uniform_ptr(a0 + t * 64), arow[i] - back, lds0 + to + (wave * DA + i) * 1024);
+    else lds_dma16(uniform_ptr(b0 + t * 64), brow[i - DA] - back, lds0 + to + TM * kStageRow + (wave * DB + i - DA) * 1024);
   };
-  auto scales = [&](const uint8_t* base, uint32_t row, int s) __attribute__((always_inline)) -> u32x4v {
-    if (s < full) return *reinterpret_cast<const u32x4a4*>(base + row + s * 32 + half * 16);
-    u32x4v v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int blk = s * 32 + half * htail + 4 * q;
-      if (4 * q < htail && blk < p.nb) {
-        uint32_t w = *reinterpret_cast<const uint32_t*>(base + row + blk);
-        if (p.nb - blk < 4) w &= (1u << (8 * (p.nb - blk))) - 1u;
-        v[q] = w;
-      }
-    }
-    return v;
+  // The scale dwords of a group of stages 4 g .. 4 g + 3, or the row's last
+  // four if those are fewer: `lead` dwords of an earlier group then come first.
+  const int dwords = p.sp / 4, groups = (stages + 3) / 4;
+  auto request_scales = [&](int g) __attribute__((always_inline)) {
+    const int off = min(4 * g, dwords - 4) * 4;
+    lds_dma16(uniform_ptr(sa0 + off), asrow, lds0 + kScales + (wave % SA) * 1024);
+    lds_dma16(uniform_ptr(sb0 + off), bsrow, lds0 + kScales + TM * 16 + (wave % SB) * 1024);
   };
-  // fragment f of step s: the rows of a fragment are 32 apart, so its chunk
-  // order is the same and only a constant is added
-  const uint8_t* abase = smem + (wm * (TM / WM) + r32) * kTileChunk;
-  const uint8_t* bbase = smem + TM * kTileChunk + (wn * (TN / WN) + r32) * kTileChunk;
-  uint32_t xs[4];
+  // bytes by which the lane's chunk of stage t lies past the last block
+  auto past = [&](int t) __attribute__((always_inline)) {
+    return static_cast<uint32_t>(max(t * 4 + chunk - (p.nb - 1), 0)) * 16u;
+  };
+
+  // Fragments: 32 rows, lane l holds row l & 31.
+  const uint8_t* abase = smem + (wm * (TM / WM) + r32) * kStageRow;
+  const uint8_t* bbase = smem + TM * kStageRow + (wn * (TN / WN) + r32) * kStageRow;
+  const uint8_t* asbase = smem + kScales + (wm * (TM / WM) + r32) * 16;
+  const uint8_t* bsbase = smem + kScales + TM * 16 + (wn * (TN / WN) + r32) * 16;
+  uint32_t xs[2];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) xs[s] = static_cast<uint32_t>(((half * 4 + s) ^ (r32 & 7)) * 16);
-  uint32_t buf = 0;                                    // byte offset of the stage being read
-  auto frag = [&](const uint8_t* base, int f, int s) __attribute__((always_inline)) -> u32x4v {
-    return *reinterpret_cast<const u32x4v*>(base + (buf + xs[s]) + f * 32 * kTileChunk);
+  for (int s = 0; s < 2; ++s) xs[s] = static_cast<uint32_t>(((half * 2 + s) ^ ((r32 >> 2) & 3)) * 16);
+  auto frag = [&](const uint8_t* base, uint32_t at, int f, int s) __attribute__((always_inline)) -> u32x4v {
+    return *reinterpret_cast<const u32x4v*>(base + (at + xs[s]) + f * 32 * kStageRow);
+  };
+  auto scale = [&](const uint8_t* base, int g, int f) __attribute__((always_inline)) -> u32x4v {
+    const int lead = max(4 * g - (dwords - 4), 0);     // what follows a row's last dword is not used
+    return *reinterpret_cast<const u32x4a4*>(base + f * 512 + lead * 4);
   };
 
   f32x16v acc[FM][FN] = {};
-  u32x4v af[2][FM], bf[2][FN], as[FM], bs[FN], asn[FM] = {}, bsn[FN] = {};
+  u32x4v af[2][FM], bf[2][FN];
+  u32x4v as[FM], bs[FN];
+  uint32_t sa[FM], sb[FN], san[FM], sbn[FN];
+  // the lane's two scale bytes of stage t in the low half of a dword, bytes
+  // of blocks past the end cleared
+  auto keep_of = [&](int t) __attribute__((always_inline)) -> uint32_t {
+    const int left = p.nb - 4 * t;
+    return left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+  };
 
-  request(0);
-#pragma unroll
-  for (int f = 0; f < FM; ++f) as[f] = scales(sa0, asrow[f], 0);
-#pragma unroll
-  for (int f = 0; f < FN; ++f) bs[f] = scales(sb0, bsrow[f], 0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // Request c of a stage follows product number when(c) of the 2 NP products
+  // between a barrier and the next: spread evenly, as the path from the
+  // caches takes about half of that time for them.
+  constexpr int NP = FM * FN, NR = FM + FN;
+  constexpr auto when = [](int c) constexpr { return c * 2 * NP / DPW + (NP > 2 ? 1 : 0); };
+  constexpr int kFirst = [when]() constexpr { int n = 0; while (n < DPW && when(n) < NP) ++n; return n; }();
+  static_assert(when(DPW - 1) < 2 * NP, "");
+
+  request_scales(0);
+  unroll<NST>([&](auto Q) __attribute__((always_inline)) {
+    const int t = min(static_cast<int>(Q), stages - 1);
+    const uint32_t back = past(t);
+    unroll<Q == NST - 1 ? kFirst : DPW>([&](auto I) __attribute__((always_inline)) { request(I, t, back, Q * kStage); });
+  });
+  wait_loads<(NST - 2) * DPW + kFirst>();
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  if (stages > 1) request(1);
+  {
+    const uint32_t keep = keep_of(0);
 #pragma unroll
-  for (int f = 0; f < FM; ++f) af[0][f] = frag(abase, f, 0);
-#pragma unroll
-  for (int f = 0; f < FN; ++f) bf[0][f] = frag(bbase, f, 0);
-
-  for (int t = 0; t < stages; ++t) {
-    // the next super-stage's scales, three stages ahead
-    if ((t & 3) == 0 && t + 4 < stages) {
-#pragma unroll
-      for (int f = 0; f < FM; ++f) asn[f] = scales(sa0, asrow[f], t / 4 + 1);
-#pragma unroll
-      for (int f = 0; f < FN; ++f) bsn[f] = scales(sb0, bsrow[f], t / 4 + 1);
+    for (int f = 0; f < FM; ++f) {
+      af[0][f] = frag(abase, 0, f, 0);
+      as[f] = scale(asbase, 0, f);
+      sa[f] = (as[f][0] & keep) >> (16 * half);
     }
-    unroll<4>([&](auto S) __attribute__((always_inline)) {
-      constexpr int s = S, cur = s & 1, nxt = cur ^ 1;
-      if constexpr (s == 3) {
-        // this wave's reads of stage t are done, stage t + 1 has arrived
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      bf[0][f] = frag(bbase, 0, f, 0);
+      bs[f] = scale(bsbase, 0, f);
+      sb[f] = (bs[f][0] & keep) >> (16 * half);
+    }
+  }
+
+  uint32_t at = 0, prev = (NST - 1) * kStage;          // places in LDS of this stage and of the one before
+  int tp = min(NST - 1, stages - 1);                   // the stage whose requests into `prev` are under way
+  uint32_t backp = past(tp);
+  // stage t, number q of its group
+  auto stage = [&](int t, auto Q) __attribute__((always_inline)) {
+    constexpr int q = Q;
+    const uint32_t next = at + kStage == NST * kStage ? 0u : at + kStage;
+    const uint32_t keep = keep_of(t + 1);
+    unroll<2>([&](auto S) __attribute__((always_inline)) {
+      constexpr int s = S, cur = s, nxt = cur ^ 1;
+      if constexpr (s == 1) {
+        // this wave's reads of stage t are done, its part of t + 1 has come
+        wait_loads<(NST - 2) * DPW>();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (t + 2 < stages) request(t + 2);
-        buf ^= kStage;
       }
-      // (the last stage reads its first step again, for nothing)
+      const uint32_t from = s == 1 ? next : at;
+      constexpr int RP = (2 * NR + NP - 1) / NP;
+      unroll<NP>([&](auto P) __attribute__((always_inline)) {
+        constexpr int i = P / FN, j = P % FN;
+        acc[i][j] = mfma32<s>(af[cur][i], bf[cur][j], acc[i][j], sa[i], sb[j]);
+        unroll<RP>([&](auto R) __attribute__((always_inline)) {
+          constexpr int r = P * RP + R;                 // order of need: A's first, all of B, the rest of A
+          constexpr int fa = r == 0 ? 0 : r > FN && r < NR ? r - FN : -1, fb = r >= 1 && r <= FN ? r - 1 : -1;
+          if constexpr (fa >= 0) {
+            af[nxt][fa] = frag(abase, from, fa, nxt);
+            if constexpr (s == 1 && q == 3) as[fa] = scale(asbase, min(t / 4 + 1, groups - 1), fa);
+          }
+          if constexpr (fb >= 0) {
+            bf[nxt][fb] = frag(bbase, from, fb, nxt);
+            if constexpr (s == 1 && q == 3) bs[fb] = scale(bsbase, min(t / 4 + 1, groups - 1), fb);
+          }
+        });
+        if constexpr (P == 0 && s == 1) {
+          if constexpr (q == 0) request_scales(min(t / 4 + 1, groups - 1));
+          prev = at;
+          tp = min(t + NST, stages - 1);               // past the end: the last stage again, unused
+          backp = past(tp);
+        }
+        unroll<DPW>([&](auto C) __attribute__((always_inline)) {
+          if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, tp, backp, prev);
+        });
+        if constexpr (P == NP - 1 && s == 1) {
 #pragma unroll
-      for (int f = 0; f < FM; ++f) af[nxt][f] = frag(abase, f, (s + 1) & 3);
+          for (int f = 0; f < FM; ++f) san[f] = (as[f][(q + 1) & 3] & keep) >> (16 * half);
 #pragma unroll
-      for (int f = 0; f < FN; ++f) bf[nxt][f] = frag(bbase, f, (s + 1) & 3);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma32<s>(af[cur][i], bf[cur][j], acc[i][j], as[i][0], bs[j][0]);
+          for (int f = 0; f < FN; ++f) sbn[f] = (bs[f][(q + 1) & 3] & keep) >> (16 * half);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
     });
-    // the next stage's scale dwords move to the front
-    const bool turn = (t & 3) == 3;
 #pragma unroll
-    for (int f = 0; f < FM; ++f) as[f] = turn ? asn[f] : u32x4v{as[f][1], as[f][2], as[f][3], 0u};
+    for (int f = 0; f < FM; ++f) sa[f] = san[f];
 #pragma unroll
-    for (int f = 0; f < FN; ++f) bs[f] = turn ? bsn[f] : u32x4v{bs[f][1], bs[f][2], bs[f][3], 0u};
+    for (int f = 0; f < FN; ++f) sb[f] = sbn[f];
+    at = next;
+  };
+
+  for (int t = 0;; t += 4) {
+    stage(t, std::integral_constant<int, 0>{});
+    if (t + 1 >= stages) break;
+    stage(t + 1, std::integral_constant<int, 1>{});
+    if (t + 2 >= stages) break;
+    stage(t + 2, std::integral_constant<int, 2>{});
+    if (t + 3 >= stages) break;
+    stage(t + 3, std::integral_constant<int, 3>{});
+    if (t + 4 >= stages) break;
   }
+  wait_loads<0>();                                     // no request outlives the workgroup
 
   T* out = static_cast<T*>(p.out);
 #pragma unroll
@@ -341,6 +409,70 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx4_tile_kernel(const Mx4Matm
         const int r = wm * (TM / WM) + 32 * i + 8 * (e / 4) + 4 * half + e % 4;
         const int c = wn * (TN / WN) + 32 * j + r32;
         if (r <= mlast && c <= nlast) store_out(out + (m0 + r) * p.ldo + n0 + c, acc[i][j][e], p.accumulate);
+      }
+}
+
+// Direct kernel, for contractions of at most 12 blocks (whose rows of scale
+// bytes are shorter than the tile kernel's requests): one wave per 32 x 32
+// outputs (2 x 2 tiles of 16 x 16), four waves per workgroup, no LDS.  The scaled 16 x 16 x 128 instruction takes from lane
+// l the 32 codes and the scale byte of row l % 16, block l / 16 of a step.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_direct_kernel(const Mx4MatmulArgs p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t tn = (static_cast<uint32_t>(p.n) + 63u) / 64u;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / tn) * 64 + (wave >> 1) * 32;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x % tn) * 64 + (wave & 1) * 32;
+  const int r16 = lane & 15, kb = lane >> 4;
+  const uint8_t *ac[2], *as[2], *bc[2], *bs[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // rows past the end read the last row; their products are not stored
+    const int64_t ar = min(m0 + 16 * i + r16, static_cast<int64_t>(p.m) - 1);
+    const int64_t br = min(n0 + 16 * i + r16, static_cast<int64_t>(p.n) - 1);
+    ac[i] = p.a + ar * p.nb * 16;
+    as[i] = p.sa + ar * p.sp;
+    bc[i] = p.b + br * p.nb * 16;
+    bs[i] = p.sb + br * p.sp;
+  }
+  f32x4v acc[2][2] = {};
+  for (int k = 0; k < p.nb; k += 4) {
+    const int b = k + kb;
+    i32x8v av[2] = {}, bv[2] = {};
+    int asv[2] = {}, bsv[2] = {};
+    if (b < p.nb) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const u32x4v x = *reinterpret_cast<const u32x4v*>(ac[i] + static_cast<int64_t>(b) * 16);
+        const u32x4v y = *reinterpret_cast<const u32x4v*>(bc[i] + static_cast<int64_t>(b) * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          av[i][j] = static_cast<int>(x[j]);
+          bv[i][j] = static_cast<int>(y[j]);
+        }
+        asv[i] = as[i][b];
+        bsv[i] = bs[i][b];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av[i], bv[j], acc[i][j], 4, 4, 0, asv[i], 0, bsv[j]);
+  }
+  T* out = static_cast<T*>(p.out);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t r = m0 + 16 * i + 4 * kb + q, c = n0 + 16 * j + r16;
+        if (r < p.m && c < p.n) {
+          T* o = out + r * p.ldo + c;
+          float v = acc[i][j][q];
+          if (p.accumulate) v += to_f(*o);
+          *o = static_cast<T>(v);
+        }
       }
 }
 
@@ -431,14 +563,22 @@ bool mx4_matmul_fits(int64_t m, int64_t n) {
   return ((m + 63) / 64) * ((n + 63) / 64) <= int64_t{0xffffffff} / 256 && (n + 15) / 16 <= int64_t{0xffffffff} / 1024;
 }
 
-template <int TM, int TN, int WM, int WN>
+template <int TM, int TN, int WM, int WN, int NST>
 static hipError_t run_tile(int out_dt, Mx4MatmulArgs a, hipStream_t s) {
   a.tiles_m = (a.m + TM - 1) / TM;
   a.tiles_n = (a.n + TN - 1) / TN;
   const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
   const dim3 g(static_cast<uint32_t>(tiles));
-  if (out_dt == F32) mx4_tile_kernel<TM, TN, WM, WN, float><<<g, 64 * WM * WN, 0, s>>>(a);
-  else mx4_tile_kernel<TM, TN, WM, WN, __bf16><<<g, 64 * WM * WN, 0, s>>>(a);
+  if (out_dt == F32) mx4_tile_kernel<TM, TN, WM, WN, NST, float><<<g, 64 * WM * WN, 0, s>>>(a);
+  else mx4_tile_kernel<TM, TN, WM, WN, NST, __bf16><<<g, 64 * WM * WN, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+static hipError_t run_direct(int out_dt, const Mx4MatmulArgs& a, hipStream_t s) {
+  const int64_t tn = (a.n + 63) / 64, tm = (a.m + 63) / 64;
+  const dim3 g(static_cast<uint32_t>(tn * tm));
+  if (out_dt == F32) mx4_direct_kernel<float><<<g, 256, 0, s>>>(a);
+  else mx4_direct_kernel<__bf16><<<g, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -462,11 +602,12 @@ hipError_t launch_mx4_matmul(int out_dt, const Mx4MatmulArgs& a, hipStream_t s) 
     if (a.m <= 32) return run_skinny<2>(out_dt, a, min(waves, 8), s);
     return run_skinny<4>(out_dt, a, min(waves, 8), s);
   }
+  if (a.nb <= 12) return run_direct(out_dt, a, s);
   const int64_t t256 = ((a.m + 255) / 256) * static_cast<int64_t>((a.n + 255) / 256);
   const int64_t t128 = ((a.m + 127) / 128) * static_cast<int64_t>((a.n + 127) / 128);
-  if (t256 >= 192) return run_tile<256, 256, 2, 2>(out_dt, a, s);
-  if (t128 >= 192) return run_tile<128, 128, 2, 2>(out_dt, a, s);
-  return run_tile<64, 64, 2, 2>(out_dt, a, s);
+  if (t256 >= 192) return run_tile<256, 256, 2, 4, 4>(out_dt, a, s);
+  if (t128 >= 192) return run_tile<128, 128, 2, 2, 4>(out_dt, a, s);
+  return run_tile<64, 64, 2, 2, 4>(out_dt, a, s);
 }
 
 }  // namespace mo
