@@ -25,6 +25,7 @@ int check_sizes(int64_t rows, int64_t vocab, int top, int top_min) {
   // a row is one workgroup of at most 1024 threads in a grid of fewer than 2^32
   if (rows < 0 || rows > (int64_t{1} << 22) - 1) return fail(MO_EINVAL, "rows must be in [0, 2^22)");
   if (vocab < 1 || vocab > INT32_MAX) return fail(MO_EINVAL, "vocab must be in [1, 2^31)");
+  if (!token_grid_fits(rows, vocab)) return fail(MO_EINVAL, "rows times vocab is too large for one launch");
   if (top < top_min || top > MO_MAX_TOP) return fail(MO_EINVAL, "top must be in [%d, %d] (got %d)", top_min, MO_MAX_TOP, top);
   return MO_OK;
 }

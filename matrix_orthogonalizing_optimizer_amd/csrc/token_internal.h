@@ -18,6 +18,11 @@ struct LogprobArgs {
   float *logprob, *entropy;
   int64_t* top_index;
   float* top_logprob;
+  // filled in at the launch: pieces of a row, columns of a piece, and each
+  // piece's {m, S, U, -} and sorted keys
+  int pieces, piece_len;
+  float4* part;
+  unsigned long long* part_keys;
 };
 
 struct DistillArgs {
@@ -30,8 +35,11 @@ struct DistillArgs {
   const float* grad_loss;
   float* loss;
   void* grad;
+  int pieces, piece_len;   // as above
+  float4* part;
 };
 
+bool token_grid_fits(int64_t rows, int64_t vocab);
 size_t logprobs_workspace(int64_t rows, int64_t vocab, int top);
 size_t distill_workspace(int64_t rows, int64_t vocab, int top);
 hipError_t launch_logprobs(int dt, const LogprobArgs& a, void* ws, hipStream_t s);

@@ -1,6 +1,21 @@
 // Token log probabilities, entropy and top alternatives, and the
 // distillation loss with its gradient (gfx950).  Definitions are those of
 // include/muon.h.
+//
+// Both read a row of logits once into registers: a workgroup's registers
+// hold up to 320 KiB, so the maximum, the sum against it, the alternatives
+// and the gradient all come from one reading.  Rows that are longer, or too
+// few to fill the chip, are cut into pieces of one workgroup each, whose
+// statistics a second launch joins.
+//
+// With m the largest logit of the row (or piece) and x_j = logit_j - m, the
+// sums are S = sum exp(x_j / tau) and U = sum exp(x_j / tau) x_j, and
+//   log p_j = x_j / tau - ln S,  entropy = ln S - U / (S tau).
+// The difference comes before the scaling: it is exact for logits that are
+// near each other, and logits of the type's lowest value do not overflow.
+// All sums are fp32, in a fixed order.
+#include <type_traits>
+
 #include "mo_internal.h"
 #include "token_internal.h"
 
@@ -8,107 +23,392 @@ namespace mo {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kLowest = -3.0e38f;
+typedef unsigned long long u64;
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f<__bf16>(__bf16 v) { return static_cast<float>(v); }
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
 
-// exp(d) for d <= 0 (or NaN), d given in units of log 2.
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Integer that orders as the value does: NaN above everything, -0 = +0.
+// Integer that orders as the value does: NaN above everything, -0 = +0; and
+// back.
 __device__ __forceinline__ uint32_t order_key(float v) {
   if (v != v) return 0xffffffffu;
   const uint32_t b = __float_as_uint(v + 0.0f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+// Largest first, then the lowest column: unique within a row, never 0.
+__device__ __forceinline__ u64 top_key(float v, int col) {
+  return (static_cast<u64>(order_key(v)) << 32) | (0xfffffffeu - static_cast<uint32_t>(col));
+}
+__device__ __forceinline__ int key_col(u64 k) { return static_cast<int>(0xfffffffeu - static_cast<uint32_t>(k)); }
 
-constexpr int kThreads = 256;
+struct Sum { template <typename V> __device__ V operator()(V a, V b) const { return a + b; } };
+struct Max { template <typename V> __device__ V operator()(V a, V b) const { return a > b ? a : b; } };
 
-// Reductions over the workgroup in a fixed order; every thread gets the
-// result.  `red` holds 4 slots and is free again after the call.
-template <typename V, typename F>
+// Reduction over the workgroup in a fixed order; every thread gets the
+// result.  `red` (one slot per wave) may be used again after the call.
+template <int NT, typename V, typename F>
 __device__ __forceinline__ V block_reduce(V v, V* red, F f) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = f(v, __shfl_xor(v, o, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = f(f(red[0], red[1]), f(red[2], red[3]));
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) v = f(v, red[w]);
   __syncthreads();
   return v;
 }
 
-struct Sum { template <typename V> __device__ V operator()(V a, V b) const { return a + b; } };
-struct Max { template <typename V> __device__ V operator()(V a, V b) const { return a > b ? a : b; } };
-
-}  // namespace
-
-// One workgroup per row: maximum, then the sums, then one pass per
-// alternative.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
-  __shared__ float redf[4];
-  __shared__ unsigned long long redu[4];
-  const int64_t r = blockIdx.x;
-  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
-  float m = -INFINITY;
-  for (int j = threadIdx.x; j < a.vocab; j += kThreads) m = fmaxf(m, to_f(z[j]));
-  m = block_reduce(m, redf, Max());
-  float s = 0.0f, t = 0.0f;
-  for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-    const float d = (to_f(z[j]) - m) * a.inv_tau;
-    const float e = exp2_fast(d * kLog2e);
-    s += e;
-    t += e > 0.0f ? e * -d : 0.0f;
+// Sixteen bytes of a row, aligned to the element only: rows of odd length
+// start anywhere, and the hardware's unaligned access costs less than peeling.
+template <typename T> struct Row;
+template <> struct Row<float> {
+  static constexpr int N = 4;
+  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+  typedef float reg __attribute__((ext_vector_type(4)));
+  __device__ static float get(reg v, int j) { return v[j]; }
+  __device__ static reg fill() { return reg{-INFINITY, -INFINITY, -INFINITY, -INFINITY}; }
+  __device__ static void put(reg& v, int j, float x) { v[j] = x; }
+  __device__ static reg pack(const float (&x)[4]) { return reg{x[0], x[1], x[2], x[3]}; }
+};
+template <> struct Row<__bf16> {
+  static constexpr int N = 8;
+  typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t reg __attribute__((ext_vector_type(4)));
+  __device__ static float get(reg v, int j) {
+    return __uint_as_float((j & 1) ? (v[j / 2] & 0xffff0000u) : (v[j / 2] << 16));
   }
-  s = block_reduce(s, redf, Sum());
-  t = block_reduce(t, redf, Sum());
-  const float log_s = logf(s);
-  if (threadIdx.x == 0) {
+  __device__ static reg fill() { return reg{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }
+  __device__ static void put(reg& v, int j, float x) {
+    const uint32_t h = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(x)));
+    v[j / 2] = (j & 1) ? (v[j / 2] & 0xffffu) | (h << 16) : (v[j / 2] & 0xffff0000u) | h;
+  }
+  __device__ static reg pack(const float (&x)[8]) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    reg v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x[2 * i], x[2 * i + 1]}), b2));
+    return v;
+  }
+};
+
+// A row, or a piece of one, in the registers of a workgroup of NT threads:
+// vector v of thread t holds the N elements from (v NT + t) N on; places past
+// the end hold -inf.
+template <typename T, int NT, int NV>
+struct RowRegs {
+  static constexpr int N = Row<T>::N, kCapacity = NT * NV * N;
+  typename Row<T>::reg x[NV];
+  int len;
+
+  __device__ __forceinline__ int at(int v) const { return (v * NT + static_cast<int>(threadIdx.x)) * N; }
+
+  __device__ __forceinline__ void load(const T* p, int n) {
+    len = n;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = at(v);
+      if (e + N <= n) {
+        x[v] = *reinterpret_cast<const typename Row<T>::vec*>(p + e);
+      } else {
+        x[v] = Row<T>::fill();
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (e + j < n) Row<T>::put(x[v], j, static_cast<float>(p[e + j]));
+      }
+    }
+  }
+  // Makes the compiler unpack the elements again rather than keep what an
+  // earlier pass unpacked (twice the registers, half the rows in flight).
+  __device__ __forceinline__ void fresh() {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) asm volatile("" : "+v"(x[v]));
+  }
+  // f(value) over the thread's places
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < N; ++j) f(Row<T>::get(x[v], j));
+  }
+  __device__ __forceinline__ float max_value() const {
+    float m = -INFINITY;
+    each([&](float z) { m = fmaxf(m, z); });
+    return m;
+  }
+  // emit(key) for every element that is not below `thr`
+  template <typename F>
+  __device__ __forceinline__ void scan(float thr, int col0, F emit) const {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < N; ++j) any |= !(Row<T>::get(x[v], j) < thr);
+      if (any) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float z = Row<T>::get(x[v], j);
+          if (!(z < thr) && at(v) + j < len) emit(top_key(z, col0 + at(v) + j));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ int count_from(u64 low, int col0) const {
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (at(v) + j < len && top_key(Row<T>::get(x[v], j), col0 + at(v) + j) >= low) ++n;
+    return n;
+  }
+  static constexpr bool kHalfKeys = sizeof(T) == 2;
+};
+
+// ------------------------------------------------------------ alternatives
+// The n largest keys, sorted, into lds.keys.  A lower bound comes from the n-th
+// largest of the threads' own maxima (n elements are at least that large; the
+// search looks at the upper half of the keys and rounds down); the elements
+// that reach it, little more than n unless many are equal, go to a list, and
+// each takes its place by counting the larger ones.  A list that overflows
+// (plateaus, rows with few columns) is replaced by an exact search for the
+// n-th key over all elements, a bit at a time.
+constexpr int kCand = 512;
+template <int NT>
+struct TopLds {
+  u64 cand[kCand], keys[kMaxTop];
+  uint32_t upper[NT];
+  int count;
+  uint32_t bound;
+  int red[NT / 64];
+};
+
+// The n-th largest upper half among NT threads' maxima, found by one wave.
+template <int NT>
+__device__ __forceinline__ float top_bound(uint32_t mine, int n, TopLds<NT>& l) {
+  l.upper[threadIdx.x] = mine >> 16;
+  if (threadIdx.x == 0) l.count = 0;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    uint32_t u[NT / 64];
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) u[w] = l.upper[w * 64 + threadIdx.x];
+    uint32_t b = 0;
+#pragma unroll
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t t = b | (1u << bit);
+      int c = 0;
+#pragma unroll
+      for (int w = 0; w < NT / 64; ++w) c += __popcll(__ballot(u[w] >= t));
+      if (c >= n) b = t;
+    }
+    if (threadIdx.x == 0) l.bound = b;
+  }
+  __syncthreads();
+  return key_value(l.bound << 16);
+}
+
+template <int NT>
+__device__ __forceinline__ void rank_sort(int count, int n, TopLds<NT>& l) {
+  for (int i = threadIdx.x; i < count; i += NT) {
+    const u64 k = l.cand[i];
+    int rank = 0;
+    for (int j = 0; j < count; ++j) rank += l.cand[j] > k;
+    if (rank < n) l.keys[rank] = k;
+  }
+  __syncthreads();
+}
+
+template <int NT>
+__device__ __forceinline__ void append(u64 k, TopLds<NT>& l) {
+  const int i = atomicAdd(&l.count, 1);       // any order: ranks decide
+  if (i < kCand) l.cand[i] = k;
+}
+
+template <typename T, int NT, int NV>
+__device__ __forceinline__ void select_top(RowRegs<T, NT, NV>& row, float mine, int col0, int n, TopLds<NT>& l) {
+  typedef RowRegs<T, NT, NV> R;
+  const float thr = top_bound<NT>(row.at(0) < row.len ? order_key(mine) : 0u, n, l);
+  row.fresh();
+  row.scan(thr, col0, [&](u64 k) { append<NT>(k, l); });
+  __syncthreads();
+  int count = l.count;
+  __syncthreads();
+  if (count > kCand) {
+    u64 low = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      u64 t = low | (u64{1} << bit);
+      if (R::kHalfKeys && bit == 47) {           // the lower halves of 16-bit values' keys are all 0 or all 1
+        t = low | (u64{0xffff} << 32);
+        bit = 32;
+      }
+      row.fresh();
+      if (block_reduce<NT>(row.count_from(t, col0), l.red, Sum()) >= n) low = t;
+    }
+    row.fresh();
+    if (threadIdx.x == 0) l.count = 0;
+    __syncthreads();
+    row.scan(key_value(static_cast<uint32_t>(low >> 32)), col0, [&](u64 k) {
+      if (k >= low) append<NT>(k, l);
+    });
+    __syncthreads();
+    count = n;
+  }
+  rank_sort<NT>(count, n, l);
+}
+
+struct Stats { float ref, s, u; };
+
+// The largest element (-inf for a row without any), S and U.
+template <bool kEntropy, typename T, int NT, int NV>
+__device__ __forceinline__ Stats row_stats(RowRegs<T, NT, NV>& row, float m, float c, float* red) {
+  m = block_reduce<NT>(m, red, Max());
+  row.fresh();
+  Stats st;
+  st.ref = m == -INFINITY ? 0.0f : m;
+  float s = 0.0f, u = 0.0f;
+  row.each([&](float z) {
+    const float x = z - st.ref, e = exp2_(x * c);
+    s += e;
+    if constexpr (kEntropy) u = fmaf(e, fmaxf(x, kLowest), u);   // 0 times -inf counts as 0
+  });
+  st.s = block_reduce<NT>(s, red, Sum());
+  st.u = kEntropy ? block_reduce<NT>(u, red, Sum()) : 0.0f;
+  if (m == -INFINITY) st.ref = -INFINITY;
+  return st;
+}
+
+// The outputs of one row.
+struct RowOut {
+  const LogprobArgs& a;
+  int64_t r;
+  Stats st;
+  float lg;
+  __device__ RowOut(const LogprobArgs& args, int64_t row, Stats s) : a(args), r(row), st(s) {
+    lg = s.ref == -INFINITY ? NAN : log2_(s.s) * kLn2;
+  }
+  __device__ float logp(float z) const { return (z - st.ref) * a.inv_tau - lg; }
+  template <typename T>
+  __device__ void scalars(const T* z) const {
     if (a.tokens) {
       const int64_t tok = a.tokens[r];
-      a.logprob[r] = tok < 0 ? 0.0f : tok < a.vocab ? (to_f(z[tok]) - m) * a.inv_tau - log_s : NAN;
+      a.logprob[r] = tok < 0 ? 0.0f : tok < a.vocab ? logp(static_cast<float>(z[tok])) : NAN;
     }
-    if (a.entropy) a.entropy[r] = s != s ? NAN : log_s + t / s;
+    if (a.entropy) a.entropy[r] = lg - st.u / st.s * a.inv_tau;
   }
-  unsigned long long last = ~0ull;   // every composite key is below it
-  for (int i = 0; i < a.top; ++i) {
-    unsigned long long best = 0;
-    for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-      const unsigned long long k =
-          (static_cast<unsigned long long>(order_key(to_f(z[j]))) << 32) | (0xfffffffeu - static_cast<uint32_t>(j));
-      if (k < last && k > best) best = k;
-    }
-    best = block_reduce(best, redu, Max());
-    last = best;
-    if (threadIdx.x == 0) {
-      const uint32_t j = 0xfffffffeu - static_cast<uint32_t>(best);
-      a.top_index[r * a.top + i] = j;
-      a.top_logprob[r * a.top + i] = (to_f(z[j]) - m) * a.inv_tau - log_s;
-    }
+  __device__ void top(int i, u64 k) const {
+    a.top_index[r * a.top + i] = key_col(k);
+    a.top_logprob[r * a.top + i] = logp(key_value(static_cast<uint32_t>(k >> 32)));
   }
-}
+};
 
-size_t logprobs_workspace(int64_t, int64_t, int) { return 0; }
-
-hipError_t launch_logprobs(int dt, const LogprobArgs& a, void*, hipStream_t s) {
-  if (dt == F32) logprobs_kernel<float><<<a.rows, kThreads, 0, s>>>(a);
-  else logprobs_kernel<__bf16><<<a.rows, kThreads, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-// One workgroup per row: the teacher's softmax over its slots, the student's
-// maximum and sum, the loss, and the gradient (the student's softmax
-// everywhere, then the teacher's columns again with their probability taken
-// off).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) {
-  __shared__ float redf[4];
-  __shared__ float prob[kMaxTop];
-  __shared__ int col[kMaxTop];       // -1: absent or of no weight
-  const int64_t r = blockIdx.x;
+// One workgroup per row (pieces = 1) or per piece, whose statistics and
+// sorted keys then go to the workspace.
+template <typename T, int NT, int NV>
+__global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobArgs a) {
+  __shared__ float red[NT / 64];
+  __shared__ TopLds<NT> lds;
+  const uint32_t pieces = static_cast<uint32_t>(a.pieces);
+  const int64_t r = blockIdx.x / pieces;
+  const int piece = static_cast<int>(blockIdx.x % pieces);
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+  const int col0 = piece * a.piece_len;
+  RowRegs<T, NT, NV> row;
+  row.load(z + col0, min(a.piece_len, a.vocab - col0));
+  const float mine = row.max_value();
+  const Stats st = row_stats<true>(row, mine, a.inv_tau * kLog2e, red);
+  const int n = min(a.top, row.len);
+  if (n > 0) select_top(row, mine, col0, n, lds);
+  if (pieces == 1) {
+    const RowOut out(a, r, st);
+    if (threadIdx.x == 0) out.scalars(z);
+    if (threadIdx.x < static_cast<uint32_t>(n)) out.top(threadIdx.x, lds.keys[threadIdx.x]);
+  } else {
+    if (threadIdx.x == 0) a.part[blockIdx.x] = {st.ref, st.s, st.u, 0.0f};
+    if (threadIdx.x < static_cast<uint32_t>(a.top))
+      a.part_keys[static_cast<int64_t>(blockIdx.x) * a.top + threadIdx.x] = threadIdx.x < static_cast<uint32_t>(n) ? lds.keys[threadIdx.x] : 0;
+  }
+}
+
+// Joined statistics of a row's pieces.
+template <int NT>
+__device__ __forceinline__ Stats join(const float4* part, int pieces, float c, float* red) {
+  Stats st{-INFINITY, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < pieces; i += NT) st.ref = fmaxf(st.ref, part[i].x);
+  st.ref = block_reduce<NT>(st.ref, red, Max());
+  for (int i = threadIdx.x; i < pieces; i += NT) {
+    const float4 p = part[i];
+    // a piece of -inf only adds nothing (but NaN, if that is its sum)
+    const float x = p.x - st.ref, w = st.ref == -INFINITY ? 0.0f : exp2_(x * c);
+    const float ws = w * p.y;
+    st.s += ws;
+    st.u += fmaf(ws, fmaxf(x, kLowest), w * p.z);
+  }
+  st.s = block_reduce<NT>(st.s, red, Sum());
+  st.u = block_reduce<NT>(st.u, red, Sum());
+  return st;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) logprobs_join_kernel(const LogprobArgs a) {
+  constexpr int NT = 256;
+  __shared__ float red[NT / 64];
+  __shared__ TopLds<NT> lds;
+  const int64_t r = blockIdx.x;
+  const RowOut out(a, r, join<NT>(a.part + r * a.pieces, a.pieces, a.inv_tau * kLog2e, red));
+  if (threadIdx.x == 0) out.scalars(static_cast<const T*>(a.logits) + r * a.ld);
+  const int n = a.top;
+  if (n == 0) return;
+  const u64* keys = a.part_keys + r * a.pieces * static_cast<int64_t>(n);
+  const int len = a.pieces * n;
+  // the keys of all pieces, as above; a piece's own n are sorted, so the
+  // threads' maxima spread over the pieces
+  uint32_t mine = 0;
+  for (int i = threadIdx.x; i < len; i += NT) mine = max(mine, static_cast<uint32_t>(keys[i] >> 32));
+  top_bound<NT>(mine, n, lds);
+  const u64 bound = static_cast<u64>(lds.bound) << 48;
+  for (int i = threadIdx.x; i < len; i += NT)
+    if (keys[i] >= bound && keys[i]) append<NT>(keys[i], lds);
+  __syncthreads();
+  int count = lds.count;
+  __syncthreads();
+  if (count > kCand) {
+    u64 low = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const u64 t = low | (u64{1} << bit);
+      int c = 0;
+      for (int i = threadIdx.x; i < len; i += NT) c += keys[i] >= t;
+      if (block_reduce<NT>(c, lds.red, Sum()) >= n) low = t;
+    }
+    if (threadIdx.x == 0) lds.count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < len; i += NT)
+      if (keys[i] >= low) append<NT>(keys[i], lds);
+    __syncthreads();
+    count = n;
+  }
+  rank_sort<NT>(count, n, lds);
+  if (threadIdx.x < static_cast<uint32_t>(n)) out.top(threadIdx.x, lds.keys[threadIdx.x]);
+}
+
+// ------------------------------------------------------------- distillation
+// The teacher's side of a row: softmax over its present slots, slot k in
+// thread k of the first two waves.
+struct Teacher {
+  float p, logp;
+  int col;               // -1: absent, of no weight, or not a column
+  bool skip, bad;
+};
+
+template <int NT>
+__device__ __forceinline__ Teacher teacher(const DistillArgs& a, int64_t r, float* red) {
   const int tid = threadIdx.x;
   int64_t idx = -1;
   float t = -INFINITY;
@@ -116,66 +416,241 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) 
     idx = a.top_index[r * a.top + tid];
     if (idx >= 0) t = a.top_logit[r * a.top + tid];
   }
-  const float bad = (idx >= a.vocab || t != t || t == INFINITY) ? NAN : 0.0f;
-  const float tm = block_reduce(t, redf, Max());
-  const float nan_row = block_reduce(bad, redf, Sum());
-  const bool skip = tm == -INFINITY && nan_row == 0.0f;
-  const float g = a.grad_loss ? a.grad_loss[r] : 1.0f;
-  T* grad = a.grad ? static_cast<T*>(a.grad) + r * a.ld_grad : nullptr;
-  if (grad && (skip || g == 0.0f)) {
-    for (int j = tid; j < a.vocab; j += kThreads) grad[j] = static_cast<T>(0.0f);
-    grad = nullptr;
-  }
-  if (skip) {
-    if (a.loss && tid == 0) a.loss[r] = 0.0f;
-    return;
-  }
-  const float td = (t - tm) * a.inv_tau;
-  float p = exp2_fast(td * kLog2e);
-  const float ts = block_reduce(tid < a.top ? p : 0.0f, redf, Sum());
-  p = tid < a.top ? p / ts : 0.0f;
-  float m = -INFINITY;
-  for (int j = tid; j < a.vocab; j += kThreads) m = fmaxf(m, to_f(z[j]));
-  m = block_reduce(m, redf, Max());
-  float s = 0.0f;
-  for (int j = tid; j < a.vocab; j += kThreads) s += exp2_fast((to_f(z[j]) - m) * a.inv_tau * kLog2e);
-  s = block_reduce(s, redf, Sum()) + nan_row;
-  if (a.loss) {
-    const float zk = p > 0.0f && idx < a.vocab ? (to_f(z[idx]) - m) * a.inv_tau : 0.0f;
-    const float term = p > 0.0f ? p * ((td - logf(ts)) - (zk - logf(s))) : 0.0f;
-    const float l = block_reduce(term, redf, Sum());
-    if (tid == 0) a.loss[r] = a.tau * a.tau * l + (s != s ? NAN : 0.0f);
-  }
-  if (!grad) return;
+  const float wrong = idx >= a.vocab || t != t || t == INFINITY ? 1.0f : 0.0f;
+  Teacher q;
+  q.bad = block_reduce<NT>(wrong, red, Max()) > 0.0f;
+  if (q.bad) t = -INFINITY;
+  const float m = block_reduce<NT>(t, red, Max());
+  q.skip = m == -INFINITY && !q.bad;
+  const float x = (t - (m == -INFINITY ? 0.0f : m)) * a.inv_tau, e = exp2_(x * kLog2e), s = block_reduce<NT>(e, red, Sum());
+  q.p = s > 0.0f ? e / s : 0.0f;
+  q.logp = x - log2_(s) * kLn2;
+  q.col = q.p > 0.0f ? static_cast<int>(idx) : -1;
+  return q;
+}
+
+// tau^2 sum p (log p - log q), in every thread.
+template <int NT, typename T>
+__device__ __forceinline__ float distill_value(const DistillArgs& a, const Teacher& q, const T* z, Stats st, float* red) {
+  const float lq = q.col >= 0 ? (static_cast<float>(z[q.col]) - st.ref) * a.inv_tau - log2_(st.s) * kLn2 : 0.0f;
+  const float l = block_reduce<NT>(q.col >= 0 ? q.p * (q.logp - lq) : 0.0f, red, Sum());
+  return q.bad || st.ref == -INFINITY || st.s != st.s ? NAN : a.tau * a.tau * l;
+}
+
+template <int NT>
+struct SlotLds {
+  float prob[kMaxTop];
+  int col[kMaxTop];
+};
+
+// Writes the gradient of the registers' elements: g tau q everywhere, then the
+// teacher's columns that lie in them again with their probabilities taken
+// off (a column's first slot adds up all of its slots).
+template <typename T, int NT, int NV>
+__device__ __forceinline__ void write_grad(const DistillArgs& a, RowRegs<T, NT, NV>& row, const T* z, T* grad, int col0,
+                                           const Teacher& q, Stats st, float g, SlotLds<NT>& l) {
+  const int tid = threadIdx.x;
   if (tid < a.top) {
-    prob[tid] = p;
-    col[tid] = p > 0.0f && idx < a.vocab ? static_cast<int>(idx) : -1;
+    l.prob[tid] = q.p;
+    l.col[tid] = q.col;
   }
-  const float c = g * a.tau, qs = 1.0f / s;
-  for (int j = tid; j < a.vocab; j += kThreads)
-    grad[j] = static_cast<T>(c * (exp2_fast((to_f(z[j]) - m) * a.inv_tau * kLog2e) * qs));
-  __builtin_amdgcn_s_waitcnt(0x0f70);   // the stores above before the teacher's columns
+  const bool nan_row = q.bad || st.ref == -INFINITY;
+  const bool zero = q.skip || g == 0.0f;
+  const float c = a.inv_tau * kLog2e, scale = zero ? 0.0f : g * a.tau;
+  const float w = nan_row ? NAN : scale / st.s, ref = nan_row ? 0.0f : st.ref;
+  T* out = grad + col0;
+  row.fresh();
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e = row.at(v);
+    float x[Row<T>::N];
+#pragma unroll
+    for (int j = 0; j < Row<T>::N; ++j) x[j] = zero ? 0.0f : exp2_((Row<T>::get(row.x[v], j) - ref) * c) * w;
+    const typename Row<T>::reg o = Row<T>::pack(x);
+    if (e + Row<T>::N <= row.len) {
+      *reinterpret_cast<typename Row<T>::vec*>(out + e) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < Row<T>::N; ++j)
+        if (e + j < row.len) out[e + j] = static_cast<T>(Row<T>::get(o, j));
+    }
+  }
+  if (zero || nan_row) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);            // these stores before the teacher's columns
   __syncthreads();
-  if (tid < a.top && col[tid] >= 0) {
-    const int j = col[tid];
-    float sum = 0.0f;
-    bool first = true;
-    for (int k = 0; k < a.top; ++k)
-      if (col[k] == j) {
-        if (k < tid) first = false;
-        sum += prob[k];
-      }
-    if (first)
-      grad[j] = static_cast<T>(c * (exp2_fast((to_f(z[j]) - m) * a.inv_tau * kLog2e) * qs - sum));
+  if (tid < a.top) {
+    const int j = l.col[tid];
+    if (j >= col0 && j < col0 + row.len) {
+      float sum = 0.0f;
+      bool first = true;
+      for (int k = 0; k < a.top; ++k)
+        if (l.col[k] == j) {
+          if (k < tid) first = false;
+          sum += l.prob[k];
+        }
+      if (first) grad[j] = static_cast<T>(exp2_((static_cast<float>(z[j]) - ref) * c) * w - scale * sum);
+    }
   }
 }
 
-size_t distill_workspace(int64_t, int64_t, int) { return 0; }
+// kPhase 0: a workgroup per row does everything.  1: a workgroup per piece
+// writes the piece's statistics.  2: a workgroup per piece joins its row's
+// and writes the piece's gradient (and, for the first piece, the loss).
+template <typename T, int NT, int NV, int kPhase>
+__global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a) {
+  __shared__ float red[NT / 64];
+  __shared__ SlotLds<NT> lds;
+  const uint32_t pieces = kPhase == 0 ? 1u : static_cast<uint32_t>(a.pieces);
+  const int64_t r = blockIdx.x / pieces;
+  const int piece = static_cast<int>(blockIdx.x % pieces);
+  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+  const int col0 = piece * a.piece_len;
+  if (kPhase == 2 && !a.grad && piece) return;
+  RowRegs<T, NT, NV> row;
+  if (kPhase != 2 || a.grad) row.load(z + col0, min(a.piece_len, a.vocab - col0));
+  if constexpr (kPhase == 1) {
+    const Stats st = row_stats<false>(row, row.max_value(), a.inv_tau * kLog2e, red);
+    if (threadIdx.x == 0) a.part[blockIdx.x] = {st.ref, st.s, 0.0f, 0.0f};
+    return;
+  } else {
+    const Teacher q = teacher<NT>(a, r, red);
+    const float g = a.grad && a.grad_loss ? a.grad_loss[r] : 1.0f;
+    Stats st;
+    if constexpr (kPhase == 0) st = row_stats<false>(row, row.max_value(), a.inv_tau * kLog2e, red);
+    else st = join<NT>(a.part + r * pieces, static_cast<int>(pieces), a.inv_tau * kLog2e, red);
+    if (a.loss && piece == 0) {
+      const float l = q.skip ? 0.0f : distill_value<NT>(a, q, z, st, red);
+      if (threadIdx.x == 0) a.loss[r] = l;
+    }
+    if (a.grad) write_grad(a, row, z, static_cast<T*>(a.grad) + r * a.ld_grad, col0, q, st, g, lds);
+  }
+}
 
-hipError_t launch_distill(int dt, const DistillArgs& a, void*, hipStream_t s) {
-  if (dt == F32) distill_kernel<float><<<a.rows, kThreads, 0, s>>>(a);
-  else distill_kernel<__bf16><<<a.rows, kThreads, 0, s>>>(a);
+}  // namespace
+
+// -------------------------------------------------------------------- launches
+// Pieces of a row.  Few rows leave most of the chip idle with a workgroup
+// each, so up to kFewRows rows of 16 KiB and more are cut into 8 KiB; rows
+// longer than a workgroup's registers (whole) are cut into 64 KiB.
+namespace {
+constexpr int64_t kFewRows = 96, kSmallPiece = 8 << 10, kLargePiece = 64 << 10;
+
+struct Cut { int pieces, len; };
+
+Cut cut(int64_t rows, int64_t vocab, int esz, int64_t whole) {
+  const int64_t bytes = vocab * esz;
+  int64_t piece = bytes;
+  if (rows <= kFewRows && bytes >= 2 * kSmallPiece) piece = kSmallPiece;
+  else if (bytes > whole) piece = kLargePiece;
+  const int64_t len = piece / esz, n = (vocab + len - 1) / len;
+  return {static_cast<int>(n), static_cast<int>(len)};
+}
+
+constexpr int64_t kLogprobsWhole = 64 << 10, kDistillWhole = 320 << 10;
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+}  // namespace
+
+static size_t logprobs_ws(const Cut& c, int64_t rows, int top) {
+  if (c.pieces == 1) return 0;
+  const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(c.pieces);
+  return up(n * sizeof(float4)) + up(n * static_cast<size_t>(top) * 8);
+}
+
+// The query does not know the element type: the larger of the two.
+size_t logprobs_workspace(int64_t rows, int64_t vocab, int top) {
+  const size_t a = logprobs_ws(cut(rows, vocab, 4, kLogprobsWhole), rows, top);
+  const size_t b = logprobs_ws(cut(rows, vocab, 2, kLogprobsWhole), rows, top);
+  return a > b ? a : b;
+}
+
+size_t distill_workspace(int64_t rows, int64_t vocab, int) {
+  size_t n = 0;
+  for (int esz : {4, 2}) {
+    const Cut c = cut(rows, vocab, esz, kDistillWhole);
+    const size_t b = c.pieces == 1 ? 0 : up(static_cast<size_t>(rows) * static_cast<size_t>(c.pieces) * sizeof(float4));
+    n = b > n ? b : n;
+  }
+  return n;
+}
+
+// Workgroups of a launch that covers `rows` rows.
+bool token_grid_fits(int64_t rows, int64_t vocab) {
+  for (int esz : {4, 2})
+    for (int64_t whole : {kLogprobsWhole, kDistillWhole}) {
+      const Cut c = cut(rows, vocab, esz, whole);
+      if (rows * c.pieces > int64_t{0xffffffff} / 1024) return false;
+    }
+  return true;
+}
+
+// Calls f with the smallest (threads, vectors) whose registers hold `bytes`:
+// enough waves per row to have many loads in flight, few enough that several
+// rows share a CU.
+template <bool kLong, typename F>
+static hipError_t with_size(int64_t bytes, F f) {
+#define MO_SIZE(NT, NV) f(std::integral_constant<int, NT>{}, std::integral_constant<int, NV>{})
+  if (bytes <= 4 << 10) return MO_SIZE(256, 1);
+  if (bytes <= 8 << 10) return MO_SIZE(256, 2);
+  if (bytes <= 16 << 10) return MO_SIZE(256, 4);
+  if (bytes <= 32 << 10) return MO_SIZE(512, 4);
+  if constexpr (kLong) {
+    if (bytes > 256 << 10) return MO_SIZE(1024, 20);
+    if (bytes > 128 << 10) return MO_SIZE(1024, 16);
+    if (bytes > 64 << 10) return MO_SIZE(1024, 8);
+  }
+  return MO_SIZE(512, 8);
+#undef MO_SIZE
+}
+
+template <typename T>
+static hipError_t run_logprobs(LogprobArgs a, void* ws, hipStream_t s) {
+  const Cut c = cut(a.rows, a.vocab, sizeof(T), kLogprobsWhole);
+  a.pieces = c.pieces;
+  a.piece_len = c.len;
+  const size_t n = static_cast<size_t>(a.rows) * static_cast<size_t>(c.pieces);
+  a.part = static_cast<float4*>(ws);
+  a.part_keys = reinterpret_cast<u64*>(static_cast<char*>(ws) + up(n * sizeof(float4)));
+  const hipError_t e = with_size<false>(static_cast<int64_t>(c.len) * sizeof(T), [&](auto NT, auto NV) {
+    logprobs_kernel<T, NT, NV><<<static_cast<uint32_t>(n), NT.value, 0, s>>>(a);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || c.pieces == 1) return e;
+  logprobs_join_kernel<T><<<a.rows, 256, 0, s>>>(a);
   return hipGetLastError();
+}
+
+hipError_t launch_logprobs(int dt, const LogprobArgs& a, void* ws, hipStream_t s) {
+  return dt == F32 ? run_logprobs<float>(a, ws, s) : run_logprobs<__bf16>(a, ws, s);
+}
+
+template <typename T>
+static hipError_t run_distill(DistillArgs a, void* ws, hipStream_t s) {
+  const Cut c = cut(a.rows, a.vocab, sizeof(T), kDistillWhole);
+  a.pieces = c.pieces;
+  a.piece_len = c.len;
+  a.part = static_cast<float4*>(ws);
+  const uint32_t n = static_cast<uint32_t>(a.rows) * static_cast<uint32_t>(c.pieces);
+  const int64_t bytes = static_cast<int64_t>(c.len) * sizeof(T);
+  if (c.pieces == 1)
+    return with_size<true>(bytes, [&](auto NT, auto NV) {
+      distill_kernel<T, NT, NV, 0><<<n, NT.value, 0, s>>>(a);
+      return hipGetLastError();
+    });
+  // pieces have one of two sizes
+  auto both = [&](auto NT, auto NV) {
+    distill_kernel<T, NT, NV, 1><<<n, NT.value, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    distill_kernel<T, NT, NV, 2><<<n, NT.value, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  return bytes <= kSmallPiece ? both(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{})
+                              : both(std::integral_constant<int, 512>{}, std::integral_constant<int, 8>{});
+}
+
+hipError_t launch_distill(int dt, const DistillArgs& a, void* ws, hipStream_t s) {
+  return dt == F32 ? run_distill<float>(a, ws, s) : run_distill<__bf16>(a, ws, s);
 }
 
 }  // namespace mo
