@@ -357,28 +357,44 @@ def svd_entropy(mats: Sequence[torch.Tensor], *, sigma: bool = False,
 
 
 # ---------------------------------------------------------------- 4-bit matrices
-@contextlib.contextmanager
-def _launch_on(device: torch.device, stream, tensors: Sequence[Optional[torch.Tensor]]):
+class _launch_on:
     """Device and stream of one call: outputs made inside belong to that
     stream, and ``tensors`` used on another stream than the current one are
-    recorded on it, so that the allocator keeps their memory until then."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors of one call must share a device, got {t.device} and {device}")
-    if device.type != "cuda":
-        raise ValueError("tensors must live on the GPU")
-    with torch.cuda.device(device):
-        here = torch.cuda.current_stream(device)
-        handle = _stream_handle(device, stream)
-        if handle == here.cuda_stream:
-            yield handle
-            return
-        other = torch.cuda.ExternalStream(handle, device=device)
-        with torch.cuda.stream(other):
-            yield handle
+    recorded on it, so that the allocator keeps their memory until then.
+    Gives the stream's handle.  A class, and nothing switched where nothing
+    changes: small calls cost little more than their launch."""
+
+    __slots__ = ("device", "stream", "tensors", "stack")
+
+    def __init__(self, device: torch.device, stream, tensors: Sequence[Optional[torch.Tensor]]):
+        if device.type != "cuda":
+            raise ValueError("tensors must live on the GPU")
         for t in tensors:
-            if t is not None:
-                t.record_stream(other)
+            if t is not None and t.device != device:
+                raise ValueError(f"tensors of one call must share a device, got {t.device} and {device}")
+        self.device, self.stream, self.tensors, self.stack = device, stream, tensors, None
+
+    def __enter__(self) -> int:
+        dev = self.device
+        same_device = torch.cuda.current_device() == dev.index
+        handle = here = torch.cuda.current_stream(dev).cuda_stream
+        if self.stream is not None:
+            handle = _stream_handle(dev, self.stream)
+        if same_device and handle == here:
+            return handle
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(dev))
+        if handle != here:
+            other = torch.cuda.ExternalStream(handle, device=dev)
+            self.stack.enter_context(torch.cuda.stream(other))
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(other)
+        return handle
+
+    def __exit__(self, *exc) -> None:
+        if self.stack is not None:
+            self.stack.close()
 
 
 def _rows_of(t: torch.Tensor, what: str) -> Tuple[int, int, int, int]:

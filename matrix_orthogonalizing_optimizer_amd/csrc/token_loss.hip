@@ -45,6 +45,10 @@ __device__ __forceinline__ u64 top_key(float v, int col) {
 }
 __device__ __forceinline__ int key_col(u64 k) { return static_cast<int>(0xfffffffeu - static_cast<uint32_t>(k)); }
 
+// Waves per SIMD that the registers leave room for: the row's own (4 NV), what
+// a pass needs beside them, and no more, so that several rows are in flight.
+constexpr int waves_for(int nt, int nv) { return nt == 1024 ? 4 : nv == 8 ? 6 : 8; }
+
 struct Sum { template <typename V> __device__ V operator()(V a, V b) const { return a + b; } };
 struct Max { template <typename V> __device__ V operator()(V a, V b) const { return a > b ? a : b; } };
 
@@ -143,33 +147,25 @@ struct RowRegs {
     each([&](float z) { m = fmaxf(m, z); });
     return m;
   }
-  // emit(key) for every element that is not below `thr`
+  // emit(column) for every element that is not below `thr`
   template <typename F>
-  __device__ __forceinline__ void scan(float thr, int col0, F emit) const {
+  __device__ __forceinline__ void scan(float thr, F emit) const {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       bool any = false;
 #pragma unroll
       for (int j = 0; j < N; ++j) any |= !(Row<T>::get(x[v], j) < thr);
       if (any) {
+        uint32_t hits = 0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float z = Row<T>::get(x[v], j);
-          if (!(z < thr) && at(v) + j < len) emit(top_key(z, col0 + at(v) + j));
+        for (int j = 0; j < N; ++j) hits |= !(Row<T>::get(x[v], j) < thr) ? 1u << j : 0u;
+        for (; hits; hits &= hits - 1) {
+          const int c = at(v) + __builtin_ctz(hits);
+          if (c < len) emit(c);
         }
       }
     }
   }
-  __device__ __forceinline__ int count_from(u64 low, int col0) const {
-    int n = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (at(v) + j < len && top_key(Row<T>::get(x[v], j), col0 + at(v) + j) >= low) ++n;
-    return n;
-  }
-  static constexpr bool kHalfKeys = sizeof(T) == 2;
 };
 
 // ------------------------------------------------------------ alternatives
@@ -232,33 +228,40 @@ __device__ __forceinline__ void append(u64 k, TopLds<NT>& l) {
   if (i < kCand) l.cand[i] = k;
 }
 
+// The exact search over key(0) .. key(len - 1): the n-th largest a bit at a
+// time, then the list again.
+template <int NT, typename K>
+__device__ __forceinline__ void exact_top(K key, int len, int n, TopLds<NT>& l) {
+  u64 low = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const u64 t = low | (u64{1} << bit);
+    int c = 0;
+    for (int i = threadIdx.x; i < len; i += NT) c += key(i) >= t;
+    if (block_reduce<NT>(c, l.red, Sum()) >= n) low = t;
+  }
+  if (threadIdx.x == 0) l.count = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < len; i += NT)
+    if (key(i) >= low) append<NT>(key(i), l);
+  __syncthreads();
+}
+
 template <typename T, int NT, int NV>
-__device__ __forceinline__ void select_top(RowRegs<T, NT, NV>& row, float mine, int col0, int n, TopLds<NT>& l) {
-  typedef RowRegs<T, NT, NV> R;
+__device__ __forceinline__ void select_top(RowRegs<T, NT, NV>& row, const T* z, float mine, int col0, int n, TopLds<NT>& l) {
   const float thr = top_bound<NT>(row.at(0) < row.len ? order_key(mine) : 0u, n, l);
   row.fresh();
-  row.scan(thr, col0, [&](u64 k) { append<NT>(k, l); });
+  row.scan(thr, [&](int c) { append<NT>(static_cast<u64>(c), l); });
   __syncthreads();
   int count = l.count;
   __syncthreads();
-  if (count > kCand) {
-    u64 low = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      u64 t = low | (u64{1} << bit);
-      if (R::kHalfKeys && bit == 47) {           // the lower halves of 16-bit values' keys are all 0 or all 1
-        t = low | (u64{0xffff} << 32);
-        bit = 32;
-      }
-      row.fresh();
-      if (block_reduce<NT>(row.count_from(t, col0), l.red, Sum()) >= n) low = t;
-    }
-    row.fresh();
-    if (threadIdx.x == 0) l.count = 0;
+  // the list holds columns; their values are read again rather than picked
+  // out of registers by an index
+  auto key = [&](int c) { return top_key(static_cast<float>(z[c]), col0 + c); };
+  if (count <= kCand) {
+    for (int i = threadIdx.x; i < count; i += NT) l.cand[i] = key(static_cast<int>(l.cand[i]));
     __syncthreads();
-    row.scan(key_value(static_cast<uint32_t>(low >> 32)), col0, [&](u64 k) {
-      if (k >= low) append<NT>(k, l);
-    });
-    __syncthreads();
+  } else {
+    exact_top<NT>(key, row.len, n, l);
     count = n;
   }
   rank_sort<NT>(count, n, l);
@@ -270,15 +273,21 @@ struct Stats { float ref, s, u; };
 template <bool kEntropy, typename T, int NT, int NV>
 __device__ __forceinline__ Stats row_stats(RowRegs<T, NT, NV>& row, float m, float c, float* red) {
   m = block_reduce<NT>(m, red, Max());
-  row.fresh();
   Stats st;
   st.ref = m == -INFINITY ? 0.0f : m;
   float s = 0.0f, u = 0.0f;
-  row.each([&](float z) {
-    const float x = z - st.ref, e = exp2_(x * c);
-    s += e;
-    if constexpr (kEntropy) u = fmaf(e, fmaxf(x, kLowest), u);   // 0 times -inf counts as 0
-  });
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    // a vector at a time: unpacking the next ones early takes registers from
+    // other rows
+    asm volatile("" : "+v"(row.x[v]), "+v"(s), "+v"(u));
+#pragma unroll
+    for (int j = 0; j < Row<T>::N; ++j) {
+      const float x = Row<T>::get(row.x[v], j) - st.ref, e = exp2_(x * c);
+      s += e;
+      if constexpr (kEntropy) u = fmaf(e, fmaxf(x, kLowest), u);   // 0 times -inf counts as 0
+    }
+  }
   st.s = block_reduce<NT>(s, red, Sum());
   st.u = kEntropy ? block_reduce<NT>(u, red, Sum()) : 0.0f;
   if (m == -INFINITY) st.ref = -INFINITY;
@@ -312,7 +321,7 @@ struct RowOut {
 // One workgroup per row (pieces = 1) or per piece, whose statistics and
 // sorted keys then go to the workspace.
 template <typename T, int NT, int NV>
-__global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(NT, waves_for(NT, NV)) logprobs_kernel(const LogprobArgs a) {
   __shared__ float red[NT / 64];
   __shared__ TopLds<NT> lds;
   const uint32_t pieces = static_cast<uint32_t>(a.pieces);
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobArgs a) {
   const float mine = row.max_value();
   const Stats st = row_stats<true>(row, mine, a.inv_tau * kLog2e, red);
   const int n = min(a.top, row.len);
-  if (n > 0) select_top(row, mine, col0, n, lds);
+  if (n > 0) select_top(row, z + col0, mine, col0, n, lds);
   if (pieces == 1) {
     const RowOut out(a, r, st);
     if (threadIdx.x == 0) out.scalars(z);
@@ -380,18 +389,7 @@ __global__ void __launch_bounds__(256) logprobs_join_kernel(const LogprobArgs a)
   int count = lds.count;
   __syncthreads();
   if (count > kCand) {
-    u64 low = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const u64 t = low | (u64{1} << bit);
-      int c = 0;
-      for (int i = threadIdx.x; i < len; i += NT) c += keys[i] >= t;
-      if (block_reduce<NT>(c, lds.red, Sum()) >= n) low = t;
-    }
-    if (threadIdx.x == 0) lds.count = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < len; i += NT)
-      if (keys[i] >= low) append<NT>(keys[i], lds);
-    __syncthreads();
+    exact_top<NT>([&](int i) { return keys[i]; }, len, n, lds);
     count = n;
   }
   rank_sort<NT>(count, n, lds);
@@ -497,7 +495,7 @@ __device__ __forceinline__ void write_grad(const DistillArgs& a, RowRegs<T, NT, 
 // writes the piece's statistics.  2: a workgroup per piece joins its row's
 // and writes the piece's gradient (and, for the first piece, the loss).
 template <typename T, int NT, int NV, int kPhase>
-__global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(NT, waves_for(NT, NV)) distill_kernel(const DistillArgs a) {
   __shared__ float red[NT / 64];
   __shared__ SlotLds<NT> lds;
   const uint32_t pieces = kPhase == 0 ? 1u : static_cast<uint32_t>(a.pieces);
