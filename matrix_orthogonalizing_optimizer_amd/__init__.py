@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from typing import Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
@@ -357,6 +358,15 @@ def svd_entropy(mats: Sequence[torch.Tensor], *, sigma: bool = False,
 
 
 # ---------------------------------------------------------------- 4-bit matrices
+def _raw_stream(index: int) -> int:
+    """Handle of the current stream of a device (torch's quick form of
+    ``torch.cuda.current_stream(index).cuda_stream`` where it has one)."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 class _launch_on:
     """Device and stream of one call: outputs made inside belong to that
     stream, and ``tensors`` used on another stream than the current one are
@@ -376,11 +386,10 @@ class _launch_on:
 
     def __enter__(self) -> int:
         dev = self.device
-        same_device = torch.cuda.current_device() == dev.index
-        handle = here = torch.cuda.current_stream(dev).cuda_stream
+        handle = here = _raw_stream(dev.index)
         if self.stream is not None:
             handle = _stream_handle(dev, self.stream)
-        if same_device and handle == here:
+        if handle == here and torch.cuda.current_device() == dev.index:
             return handle
         self.stack = contextlib.ExitStack()
         self.stack.enter_context(torch.cuda.device(dev))
@@ -414,6 +423,13 @@ def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, shape: Tuple[int, ...
     if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _token_workspace(query: str, rows: int, vocab: int, top: int) -> int:
+    need = ctypes.c_size_t()
+    check(getattr(lib(), query)(rows, vocab, top, ctypes.byref(need)))
+    return need.value
 
 
 def _scratch(nbytes: int, handle: int, device: torch.device) -> Optional[torch.Tensor]:
@@ -461,8 +477,11 @@ class Mx4Matrix:
         if rows < 1 or cols < 1:
             raise ValueError(f"an image has at least one row and one column, got [{rows}, {cols}]")
         nb = -(-cols // 32)
-        return cls(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
-                   torch.empty(rows, -(-nb // 4) * 4, dtype=torch.uint8, device=device), cols)
+        q = object.__new__(cls)                 # right by construction: no checks
+        q.codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, -(-nb // 4) * 4), dtype=torch.uint8, device=device)
+        q.rows, q.cols = rows, cols
+        return q
 
     def _struct(self) -> MoMx4Image:
         return MoMx4Image(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
@@ -624,15 +643,14 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     ptr, rows, vocab, ld = _rows_of(logits, "logits")
     dt, dev = _dtype_code(logits.dtype, "logits"), logits.device
     tok = _vector(tokens, torch.int64, (rows,), "tokens")
-    need = ctypes.c_size_t()
-    check(lib().mo_token_logprobs_workspace_size(rows, vocab, top, ctypes.byref(need)))
+    need = _token_workspace("mo_token_logprobs_workspace_size", rows, vocab, top)
     with _launch_on(dev, stream, [logits, tokens]) as handle:
         lp = torch.empty(rows, dtype=torch.float32, device=dev) if tokens is not None else None
         ent = torch.empty(rows, dtype=torch.float32, device=dev)
         tlp = torch.empty(rows, top, dtype=torch.float32, device=dev)
         tix = torch.empty(rows, top, dtype=torch.int64, device=dev)
         if rows:
-            ws = _scratch(need.value, handle, dev)
+            ws = _scratch(need, handle, dev)
             check(lib().mo_token_logprobs(ptr, dt, rows, vocab, ld, tok, temperature,
                                           lp.data_ptr() if lp is not None else None, ent.data_ptr(), top,
                                           tix.data_ptr() if top else None, tlp.data_ptr() if top else None,
@@ -667,8 +685,7 @@ def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_logit: torch
             raise ValueError("out_grad given with grad=False")
         if out_grad.dtype != logits.dtype or tuple(out_grad.shape) != (rows, vocab):
             raise ValueError(f"out_grad must be {logits.dtype} [{rows}, {vocab}]")
-    need = ctypes.c_size_t()
-    check(lib().mo_distill_loss_workspace_size(rows, vocab, k, ctypes.byref(need)))
+    need = _token_workspace("mo_distill_loss_workspace_size", rows, vocab, k)
     with _launch_on(dev, stream, [logits, top_index, top_logit, grad_loss, out_grad]) as handle:
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
         g = out_grad
@@ -676,7 +693,7 @@ def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_logit: torch
             g = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
         gp, _, _, ldg = _rows_of(g, "out_grad") if grad else (None, 0, 0, 0)
         if rows:
-            ws = _scratch(need.value, handle, dev)
+            ws = _scratch(need, handle, dev)
             check(lib().mo_distill_loss(ptr, dt, rows, vocab, ld, ti, tl, k, temperature, gl, loss.data_ptr(),
                                         gp, ldg, ws.data_ptr() if ws is not None else None,
                                         ws.numel() if ws is not None else 0, handle))

@@ -47,7 +47,7 @@ __device__ __forceinline__ int key_col(u64 k) { return static_cast<int>(0xffffff
 
 // Waves per SIMD that the registers leave room for: the row's own (4 NV), what
 // a pass needs beside them, and no more, so that several rows are in flight.
-constexpr int waves_for(int nt, int nv) { return nt == 1024 ? 4 : nv == 8 ? 6 : 8; }
+constexpr int waves_for(int, int nv) { return nv >= 16 ? 4 : nv == 8 ? 6 : 8; }
 
 struct Sum { template <typename V> __device__ V operator()(V a, V b) const { return a + b; } };
 struct Max { template <typename V> __device__ V operator()(V a, V b) const { return a > b ? a : b; } };
@@ -77,6 +77,8 @@ template <> struct Row<float> {
   __device__ static float get(reg v, int j) { return v[j]; }
   __device__ static reg fill() { return reg{-INFINITY, -INFINITY, -INFINITY, -INFINITY}; }
   __device__ static void put(reg& v, int j, float x) { v[j] = x; }
+  // element j, not known at compile time
+  __device__ static float pick(reg v, int j) { return j < 2 ? (j ? v[1] : v[0]) : (j & 1 ? v[3] : v[2]); }
   __device__ static reg pack(const float (&x)[4]) { return reg{x[0], x[1], x[2], x[3]}; }
 };
 template <> struct Row<__bf16> {
@@ -90,6 +92,10 @@ template <> struct Row<__bf16> {
   __device__ static void put(reg& v, int j, float x) {
     const uint32_t h = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(x)));
     v[j / 2] = (j & 1) ? (v[j / 2] & 0xffffu) | (h << 16) : (v[j / 2] & 0xffff0000u) | h;
+  }
+  __device__ static float pick(reg v, int j) {
+    const uint32_t w = j < 4 ? (j < 2 ? v[0] : v[1]) : (j < 6 ? v[2] : v[3]);
+    return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
   }
   __device__ static reg pack(const float (&x)[8]) {
     typedef float f2 __attribute__((ext_vector_type(2)));
@@ -147,7 +153,7 @@ struct RowRegs {
     each([&](float z) { m = fmaxf(m, z); });
     return m;
   }
-  // emit(column) for every element that is not below `thr`
+  // emit(value, column) for every element that is not below `thr`
   template <typename F>
   __device__ __forceinline__ void scan(float thr, F emit) const {
 #pragma unroll
@@ -160,8 +166,8 @@ struct RowRegs {
 #pragma unroll
         for (int j = 0; j < N; ++j) hits |= !(Row<T>::get(x[v], j) < thr) ? 1u << j : 0u;
         for (; hits; hits &= hits - 1) {
-          const int c = at(v) + __builtin_ctz(hits);
-          if (c < len) emit(c);
+          const int j = __builtin_ctz(hits);
+          if (at(v) + j < len) emit(Row<T>::pick(x[v], j), at(v) + j);
         }
       }
     }
@@ -250,18 +256,12 @@ template <typename T, int NT, int NV>
 __device__ __forceinline__ void select_top(RowRegs<T, NT, NV>& row, const T* z, float mine, int col0, int n, TopLds<NT>& l) {
   const float thr = top_bound<NT>(row.at(0) < row.len ? order_key(mine) : 0u, n, l);
   row.fresh();
-  row.scan(thr, [&](int c) { append<NT>(static_cast<u64>(c), l); });
+  row.scan(thr, [&](float v, int c) { append<NT>(top_key(v, col0 + c), l); });
   __syncthreads();
   int count = l.count;
   __syncthreads();
-  // the list holds columns; their values are read again rather than picked
-  // out of registers by an index
-  auto key = [&](int c) { return top_key(static_cast<float>(z[c]), col0 + c); };
-  if (count <= kCand) {
-    for (int i = threadIdx.x; i < count; i += NT) l.cand[i] = key(static_cast<int>(l.cand[i]));
-    __syncthreads();
-  } else {
-    exact_top<NT>(key, row.len, n, l);
+  if (count > kCand) {
+    exact_top<NT>([&](int c) { return top_key(static_cast<float>(z[c]), col0 + c); }, row.len, n, l);
     count = n;
   }
   rank_sort<NT>(count, n, l);
@@ -527,19 +527,18 @@ __global__ void __launch_bounds__(NT, waves_for(NT, NV)) distill_kernel(const Di
 }  // namespace
 
 // -------------------------------------------------------------------- launches
-// Pieces of a row.  Few rows leave most of the chip idle with a workgroup
-// each, so up to kFewRows rows of 16 KiB and more are cut into 8 KiB; rows
-// longer than a workgroup's registers (whole) are cut into 64 KiB.
+// Pieces of a row: a row that a workgroup's registers hold (`whole`) is not
+// cut.  Longer ones are cut into 64 KiB, or, where that leaves most of the
+// chip idle, into 16 KiB.
 namespace {
-constexpr int64_t kFewRows = 96, kSmallPiece = 8 << 10, kLargePiece = 64 << 10;
+constexpr int64_t kSmallPiece = 16 << 10, kLargePiece = 64 << 10;
 
 struct Cut { int pieces, len; };
 
 Cut cut(int64_t rows, int64_t vocab, int esz, int64_t whole) {
   const int64_t bytes = vocab * esz;
   int64_t piece = bytes;
-  if (rows <= kFewRows && bytes >= 2 * kSmallPiece) piece = kSmallPiece;
-  else if (bytes > whole) piece = kLargePiece;
+  if (bytes > whole) piece = rows * bytes < 256 * kLargePiece ? kSmallPiece : kLargePiece;
   const int64_t len = piece / esz, n = (vocab + len - 1) / len;
   return {static_cast<int>(n), static_cast<int>(len)};
 }
@@ -585,17 +584,18 @@ bool token_grid_fits(int64_t rows, int64_t vocab) {
 // Calls f with the smallest (threads, vectors) whose registers hold `bytes`:
 // enough waves per row to have many loads in flight, few enough that several
 // rows share a CU.
-template <bool kLong, typename F>
+template <int64_t kWhole, typename F>
 static hipError_t with_size(int64_t bytes, F f) {
 #define MO_SIZE(NT, NV) f(std::integral_constant<int, NT>{}, std::integral_constant<int, NV>{})
   if (bytes <= 4 << 10) return MO_SIZE(256, 1);
   if (bytes <= 8 << 10) return MO_SIZE(256, 2);
   if (bytes <= 16 << 10) return MO_SIZE(256, 4);
+  if constexpr (kWhole == 64 << 10) return bytes <= 32 << 10 ? MO_SIZE(256, 8) : MO_SIZE(256, 16);
   if (bytes <= 32 << 10) return MO_SIZE(512, 4);
-  if constexpr (kLong) {
+  if constexpr (kWhole > 64 << 10) {
     if (bytes > 256 << 10) return MO_SIZE(1024, 20);
     if (bytes > 128 << 10) return MO_SIZE(1024, 16);
-    if (bytes > 64 << 10) return MO_SIZE(1024, 8);
+    if (bytes > 64 << 10) return MO_SIZE(512, 16);
   }
   return MO_SIZE(512, 8);
 #undef MO_SIZE
@@ -609,7 +609,7 @@ static hipError_t run_logprobs(LogprobArgs a, void* ws, hipStream_t s) {
   const size_t n = static_cast<size_t>(a.rows) * static_cast<size_t>(c.pieces);
   a.part = static_cast<float4*>(ws);
   a.part_keys = reinterpret_cast<u64*>(static_cast<char*>(ws) + up(n * sizeof(float4)));
-  const hipError_t e = with_size<false>(static_cast<int64_t>(c.len) * sizeof(T), [&](auto NT, auto NV) {
+  const hipError_t e = with_size<kLogprobsWhole>(static_cast<int64_t>(c.len) * sizeof(T), [&](auto NT, auto NV) {
     logprobs_kernel<T, NT, NV><<<static_cast<uint32_t>(n), NT.value, 0, s>>>(a);
     return hipGetLastError();
   });
@@ -631,7 +631,7 @@ static hipError_t run_distill(DistillArgs a, void* ws, hipStream_t s) {
   const uint32_t n = static_cast<uint32_t>(a.rows) * static_cast<uint32_t>(c.pieces);
   const int64_t bytes = static_cast<int64_t>(c.len) * sizeof(T);
   if (c.pieces == 1)
-    return with_size<true>(bytes, [&](auto NT, auto NV) {
+    return with_size<kDistillWhole>(bytes, [&](auto NT, auto NV) {
       distill_kernel<T, NT, NV, 0><<<n, NT.value, 0, s>>>(a);
       return hipGetLastError();
     });
@@ -643,7 +643,7 @@ static hipError_t run_distill(DistillArgs a, void* ws, hipStream_t s) {
     distill_kernel<T, NT, NV, 2><<<n, NT.value, 0, s>>>(a);
     return hipGetLastError();
   };
-  return bytes <= kSmallPiece ? both(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{})
+  return bytes <= kSmallPiece ? both(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{})
                               : both(std::integral_constant<int, 512>{}, std::integral_constant<int, 8>{});
 }
 
