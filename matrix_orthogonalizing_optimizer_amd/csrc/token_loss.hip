@@ -590,14 +590,13 @@ static hipError_t with_size(int64_t bytes, F f) {
   if (bytes <= 4 << 10) return MO_SIZE(256, 1);
   if (bytes <= 8 << 10) return MO_SIZE(256, 2);
   if (bytes <= 16 << 10) return MO_SIZE(256, 4);
-  if constexpr (kWhole == 64 << 10) return bytes <= 32 << 10 ? MO_SIZE(256, 8) : MO_SIZE(256, 16);
-  if (bytes <= 32 << 10) return MO_SIZE(512, 4);
+  if (bytes <= 32 << 10) return MO_SIZE(256, 8);
   if constexpr (kWhole > 64 << 10) {
     if (bytes > 256 << 10) return MO_SIZE(1024, 20);
     if (bytes > 128 << 10) return MO_SIZE(1024, 16);
     if (bytes > 64 << 10) return MO_SIZE(512, 16);
   }
-  return MO_SIZE(512, 8);
+  return MO_SIZE(256, 16);
 #undef MO_SIZE
 }
 
@@ -644,7 +643,7 @@ static hipError_t run_distill(DistillArgs a, void* ws, hipStream_t s) {
     return hipGetLastError();
   };
   return bytes <= kSmallPiece ? both(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{})
-                              : both(std::integral_constant<int, 512>{}, std::integral_constant<int, 8>{});
+                              : both(std::integral_constant<int, 256>{}, std::integral_constant<int, 16>{});
 }
 
 hipError_t launch_distill(int dt, const DistillArgs& a, void* ws, hipStream_t s) {
