@@ -26,118 +26,340 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   return e > 2u ? e - 2u : 0u;
 }
 
-// One block of 32 values, `n` of them present, `step` elements apart.
-template <typename T>
-__device__ void quant_block(const T* p, int64_t step, int n, uint8_t* codes, uint8_t* scale) {
-  float v[32];
-  uint32_t amax = 0;
+// Sixteen bytes, aligned to the element only: rows may start anywhere, and the
+// hardware's unaligned access costs less than peeling.
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4u2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+typedef float f32x2v __attribute__((ext_vector_type(2)));
+
+// Eight consecutive elements of a row.
+template <typename T> struct Oct;
+template <> struct Oct<float> {
+  f32x4v lo, hi;
+  __device__ __forceinline__ void load(const float* p, int n) {        // n > 0 present, the others 0
+    if (n >= 8) {
+      lo = *reinterpret_cast<const f32x4u*>(p);
+      hi = *reinterpret_cast<const f32x4u*>(p + 4);
+    } else {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    v[j] = j < n ? to_f(p[j * step]) : 0.0f;
-    amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-  }
-  const uint32_t sb = scale_byte(amax);
-  u32x4v q = {0u, 0u, 0u, 0u};
-  if (sb != 255u) {
-    const float s = __uint_as_float(sb << 23);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t r = 0;
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * w + 0], v[8 * w + 1], s, 0);
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * w + 2], v[8 * w + 3], s, 1);
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * w + 4], v[8 * w + 5], s, 2);
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[8 * w + 6], v[8 * w + 7], s, 3);
-      q[w] = r;
+      for (int j = 0; j < 4; ++j) {
+        lo[j] = j < n ? p[j] : 0.0f;
+        hi[j] = j + 4 < n ? p[j + 4] : 0.0f;
+      }
     }
   }
-  *reinterpret_cast<u32x4v*>(codes) = q;
-  *scale = static_cast<uint8_t>(sb);
+  __device__ __forceinline__ void clear() { lo = hi = f32x4v{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ __forceinline__ float get(int j) const { return j < 4 ? lo[j] : hi[j - 4]; }
+  __device__ __forceinline__ uint32_t bits(int j) const { return __float_as_uint(get(j)) & 0x7fffffffu; }
+  // bits of the largest magnitude
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, bits(j));
+    return m;
+  }
+  // the eight codes, element 0 lowest
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo[0], lo[1], s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo[2], lo[3], s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, hi[0], hi[1], s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, hi[2], hi[3], s, 3);
+  }
+};
+template <> struct Oct<__bf16> {
+  u32x4v v;
+  __device__ __forceinline__ void load(const __bf16* p, int n) {
+    if (n >= 8) {
+      v = *reinterpret_cast<const u32x4u2*>(p);
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = (2 * j < n ? q[2 * j] : 0u) | (2 * j + 1 < n ? static_cast<uint32_t>(q[2 * j + 1]) << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ void clear() { v = u32x4v{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ bf16x2v pair(int i) const {
+    const uint32_t w = v[i];             // a bit cast of the vector's element itself reads element 0
+    return __builtin_bit_cast(bf16x2v, w);
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float((j & 1) ? (v[j / 2] & 0xffff0000u) : (v[j / 2] << 16));
+  }
+  __device__ __forceinline__ uint32_t bits(int j) const { return __float_as_uint(get(j)) & 0x7fffffffu; }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, bits(j));
+    return m;
+  }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(0), s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(1), s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(2), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(3), s, 3);
+  }
+};
+
+// The scale of a block as the conversions take it: only its exponent counts,
+// and an exponent of 0 means 2^-127.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Largest of a quad of lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true)));   // lanes 1 0 3 2
+  return max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true)));   // lanes 2 3 0 1
+}
+
+// Codes of the lane's eighth of a row's block, whose scale byte it also gives:
+// the four lanes of a quad share a block.
+template <typename T>
+__device__ __forceinline__ uint32_t row_codes(const Oct<T>& o, uint32_t& byte) {
+  byte = scale_byte(quad_max(o.amax()));
+  const uint32_t c = o.codes(scale_of(byte));
+  return byte == 255u ? 0u : c;
+}
+
+// The matrix that workgroup `b` belongs to: the last whose first one is not
+// past it.
+template <typename A>
+__device__ __forceinline__ int find_item(const A& a, int64_t b) {
+  int lo = 0, hi = a.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.item[mid].tile0 <= b) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 }  // namespace
 
-// One thread per block: the row image's blocks first, then the transpose's.
-// The thread of a row's last block also clears the row's scale padding.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_quant_kernel(const Mx4QuantArgs a) {
-  int i = 0;
-  while (i + 1 < a.count && static_cast<int64_t>(blockIdx.x) >= a.item[i + 1].tile0) ++i;
-  const Mx4QuantItem& it = a.item[i];
+// Row images: a thread takes eighths of blocks (8 columns), consecutive
+// threads consecutive ones, so that a wave reads and writes whole lines.  HBM
+// bound: 2.53 (bf16) or 4.53 (fp32) bytes an element.
+constexpr int kOctsPerThread = 4;
+template <typename T, int G>
+__global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const Mx4QuantArgs<G> a) {
+  const Mx4QuantItem& it = a.item[G == 1 ? 0 : find_item(a, blockIdx.x)];
   const T* src = static_cast<const T*>(it.src);
-  int64_t t = (static_cast<int64_t>(blockIdx.x) - it.tile0) * 256 + threadIdx.x;
-  const int64_t nb = mx4_blocks(it.cols), nbt = mx4_blocks(it.rows);
-  if (it.codes) {
-    if (t < it.rows * nb) {
-      const int64_t r = t / nb, b = t % nb;
-      const int64_t sp = mx4_scale_pitch(it.cols);
-      quant_block(src + r * it.ld + b * 32, 1, static_cast<int>(min(int64_t{32}, it.cols - b * 32)),
-                  it.codes + (r * nb + b) * 16, it.scales + r * sp + b);
-      if (b == nb - 1)
-        for (int64_t p = nb; p < sp; ++p) it.scales[r * sp + p] = 0;
-      return;
+  const uint32_t nb = static_cast<uint32_t>(mx4_blocks(it.cols)), sp = static_cast<uint32_t>(mx4_scale_pitch(it.cols));
+  const int64_t octs = static_cast<int64_t>(it.rows) * nb * 4;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) - it.tile0) * (256 * kOctsPerThread) + threadIdx.x;
+  Oct<T> o[kOctsPerThread];
+  int64_t row[kOctsPerThread];
+  uint32_t col8[kOctsPerThread];
+#pragma unroll
+  for (int i = 0; i < kOctsPerThread; ++i) {
+    const int64_t u = first + i * 256;
+    o[i].clear();
+    row[i] = -1;
+    if (u < octs) {
+      row[i] = octs <= 0xffffffffll ? static_cast<uint32_t>(u) / (nb * 4) : u / (nb * 4);
+      col8[i] = static_cast<uint32_t>(u - row[i] * (nb * 4));
+      const int left = it.cols - static_cast<int>(col8[i]) * 8;
+      if (left > 0) o[i].load(src + row[i] * it.ld + col8[i] * 8, left);
     }
-    t -= it.rows * nb;
   }
-  if (it.codes_t && t < it.cols * nbt) {
-    const int64_t c = t % it.cols, b = t / it.cols;
-    const int64_t sp = mx4_scale_pitch(it.rows);
-    quant_block(src + b * 32 * it.ld + c, it.ld, static_cast<int>(min(int64_t{32}, it.rows - b * 32)),
-                it.codes_t + (c * nbt + b) * 16, it.scales_t + c * sp + b);
-    if (b == nbt - 1)
-      for (int64_t p = nbt; p < sp; ++p) it.scales_t[c * sp + p] = 0;
+#pragma unroll
+  for (int i = 0; i < kOctsPerThread; ++i) {
+    uint32_t byte;
+    const uint32_t c = row_codes(o[i], byte);       // whole quads are inside or outside
+    if (row[i] < 0) continue;
+    *reinterpret_cast<uint32_t*>(it.codes + (row[i] * nb * 4 + col8[i]) * 4) = c;
+    if ((col8[i] & 3) == 0) {
+      uint8_t* s = it.scales + row[i] * sp;
+      const uint32_t b = col8[i] / 4;
+      s[b] = static_cast<uint8_t>(byte);
+      if (b == nb - 1)
+        for (uint32_t p = nb; p < sp; ++p) s[p] = 0;
+    }
   }
 }
 
-int64_t mx4_quant_tiles(int64_t rows, int64_t cols, bool row_image, bool col_image) {
-  const int64_t t = (row_image ? rows * mx4_blocks(cols) : 0) + (col_image ? cols * mx4_blocks(rows) : 0);
-  return (t + 255) / 256;
+// Images of the transpose (and, with codes given, of the matrix itself) from
+// one reading: a workgroup of 8 waves takes 256 rows x 128 columns, a wave 32
+// rows, lane l the columns 8 (l & 15) .. + 7 of rows 8 (l / 16) .. + 7.  A
+// column's block then lies in 4 lanes of a wave (l, l ^ 16, l ^ 32, l ^ 48),
+// each with 8 consecutive codes of it, and a row's block in 4 neighbours.  The
+// columns' codes go through LDS so that they leave as whole 128-byte lines.
+constexpr int kColTileRows = 256, kColTileCols = 128;
+template <typename T, int G>
+__global__ void __launch_bounds__(512, 4) mx4_quant_cols_kernel(const Mx4QuantArgs<G> a) {
+  __shared__ uint32_t codes[kColTileCols][33];     // 128 bytes a column, and a dword against bank conflicts
+  __shared__ __attribute__((aligned(8))) uint8_t bytes[kColTileCols][8];
+  const Mx4QuantItem& it = a.item[G == 1 ? 0 : find_item(a, blockIdx.x)];
+  const T* src = static_cast<const T*>(it.src);
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) - it.tile0;
+  const int64_t tiles_c = (it.cols + kColTileCols - 1) / kColTileCols;
+  const int64_t row0 = tile / tiles_c * kColTileRows, col0 = tile % tiles_c * kColTileCols;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t r0 = row0 + wave * 32 + (lane >> 4) * 8, c0 = col0 + (lane & 15) * 8;
+  const int left_c = static_cast<int>(min(int64_t{8}, it.cols - c0)), left_r = static_cast<int>(min(int64_t{8}, it.rows - r0));
+
+  Oct<T> o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    o[i].clear();
+    if (i < left_r && left_c > 0) o[i].load(src + (r0 + i) * it.ld + c0, left_c);
+  }
+  if (it.codes) {
+    const int64_t nb = mx4_blocks(it.cols), sp = mx4_scale_pitch(it.cols);
+    const int64_t b = c0 / 32;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t byte;
+      const uint32_t c = row_codes(o[i], byte);
+      const int64_t r = r0 + i;
+      if (i < left_r && b < nb) {
+        *reinterpret_cast<uint32_t*>(it.codes + r * nb * 16 + c0 / 2) = c;
+        if ((lane & 3) == 0) {
+          it.scales[r * sp + b] = static_cast<uint8_t>(byte);
+          if (b == nb - 1)
+            for (int64_t p = nb; p < sp; ++p) it.scales[r * sp + p] = 0;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, o[i].bits(j));
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16, 64)));
+    m = max(m, lane_xor32(m));
+    const uint32_t byte = scale_byte(m);
+    const float s = scale_of(byte);
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o[0].get(j), o[1].get(j), s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o[2].get(j), o[3].get(j), s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o[4].get(j), o[5].get(j), s, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o[6].get(j), o[7].get(j), s, 3);
+    const int c = (lane & 15) * 8 + j;
+    codes[c][wave * 4 + (lane >> 4)] = byte == 255u ? 0u : r;
+    if (lane < 16) bytes[c][wave] = static_cast<uint8_t>(byte);
+  }
+  __syncthreads();
+  const int64_t nbt = mx4_blocks(it.rows), spt = mx4_scale_pitch(it.rows), b0 = row0 / 32;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = i * 512 + threadIdx.x, c = u >> 3, b = u & 7;       // block b of column c
+    if (col0 + c < it.cols && b0 + b < nbt) {
+      u32x4v v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = codes[c][b * 4 + k];
+      *reinterpret_cast<u32x4v*>(it.codes_t + ((col0 + c) * nbt + b0 + b) * 16) = v;
+    }
+  }
+  if (threadIdx.x < kColTileCols * 2) {
+    // scale bytes past the last block come from rows that are not there: zero
+    const int c = threadIdx.x >> 1, d = (threadIdx.x & 1) * 4;
+    if (col0 + c < it.cols && b0 + d < spt)
+      *reinterpret_cast<uint32_t*>(it.scales_t + (col0 + c) * spt + b0 + d) = *reinterpret_cast<const uint32_t*>(&bytes[c][d]);
+  }
 }
 
-hipError_t launch_mx4_quant(int dt, const Mx4QuantArgs& a, int64_t tiles, hipStream_t s) {
+int64_t mx4_quant_tiles(int64_t rows, int64_t cols, bool cols_image) {
+  if (cols_image) return ((rows + kColTileRows - 1) / kColTileRows) * ((cols + kColTileCols - 1) / kColTileCols);
+  const int64_t octs = rows * mx4_blocks(cols) * 4;
+  return (octs + 256 * kOctsPerThread - 1) / (256 * kOctsPerThread);
+}
+
+template <int G>
+hipError_t launch_mx4_quant(int dt, bool cols_image, const Mx4QuantArgs<G>& a, int64_t tiles, hipStream_t s) {
   const dim3 g(static_cast<uint32_t>(tiles));
-  if (dt == F32) mx4_quant_kernel<float><<<g, 256, 0, s>>>(a);
-  else mx4_quant_kernel<__bf16><<<g, 256, 0, s>>>(a);
+  if (cols_image) {
+    if (dt == F32) mx4_quant_cols_kernel<float, G><<<g, 512, 0, s>>>(a);
+    else mx4_quant_cols_kernel<__bf16, G><<<g, 512, 0, s>>>(a);
+  } else {
+    if (dt == F32) mx4_quant_rows_kernel<float, G><<<g, 256, 0, s>>>(a);
+    else mx4_quant_rows_kernel<__bf16, G><<<g, 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
+template hipError_t launch_mx4_quant<1>(int, bool, const Mx4QuantArgs<1>&, int64_t, hipStream_t);
+template hipError_t launch_mx4_quant<kMx4Group>(int, bool, const Mx4QuantArgs<kMx4Group>&, int64_t, hipStream_t);
 
-// Value of a code: sign, two exponent bits, one mantissa bit.
-__device__ __forceinline__ float code_value(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float v = e ? __uint_as_float(((e + 126u) << 23) | (m << 22)) : 0.5f * static_cast<float>(m);
-  return (c & 8u) ? -v : v;
-}
-
-// 2^(byte - 127); NaN for 255.  Byte 0 is the subnormal 2^-127.
-__device__ __forceinline__ float scale_value(uint32_t sb) {
-  return sb == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(sb ? sb << 23 : 0x00400000u);
-}
-
+// Reading back: the threads share the work as in the row images.
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_dequant_kernel(const Mx4DequantArgs a) {
-  int i = 0;
-  while (i + 1 < a.count && static_cast<int64_t>(blockIdx.x) >= a.item[i + 1].tile0) ++i;
-  const Mx4DequantItem& it = a.item[i];
-  const int64_t nb = mx4_blocks(it.cols), sp = mx4_scale_pitch(it.cols);
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) - it.tile0) * 256 + threadIdx.x;
-  if (t >= it.rows * nb) return;
-  const int64_t r = t / nb, b = t % nb;
-  const float s = scale_value(it.scales[r * sp + b]);
-  T* dst = static_cast<T*>(it.dst) + r * it.cols + b * 32;
-  const int n = static_cast<int>(min(int64_t{32}, it.cols - b * 32));
-  for (int j = 0; j < n; ++j) {
-    const uint32_t c = it.codes[(r * nb + b) * 16 + j / 2] >> (4 * (j & 1));
-    dst[j] = static_cast<T>(code_value(c & 15u) * s);
+__device__ __forceinline__ void store_oct(T* p, uint32_t codes, uint32_t byte, int n);
+template <>
+__device__ __forceinline__ void store_oct<float>(float* p, uint32_t codes, uint32_t byte, int n) {
+  const float s = scale_of(byte), nan = __uint_as_float(0x7fc00000u);
+  const f32x2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 1);
+  const f32x2v c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 3);
+  f32x4v lo = {a[0], a[1], b[0], b[1]}, hi = {c[0], c[1], d[0], d[1]};
+  if (byte == 255u) lo = hi = f32x4v{nan, nan, nan, nan};
+  if (n >= 8) {
+    *reinterpret_cast<f32x4u*>(p) = lo;
+    *reinterpret_cast<f32x4u*>(p + 4) = hi;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < n) p[j] = lo[j];
+      if (j + 4 < n) p[j + 4] = hi[j];
+    }
+  }
+}
+template <>
+__device__ __forceinline__ void store_oct<__bf16>(__bf16* p, uint32_t codes, uint32_t byte, int n) {
+  const float s = scale_of(byte);
+  u32x4v v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2)),
+              __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3))};
+  if (byte == 255u) v = u32x4v{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+  if (n >= 8) {
+    *reinterpret_cast<u32x4u2*>(p) = v;
+  } else {
+    uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) q[j] = static_cast<uint16_t>(v[j / 2] >> (16 * (j & 1)));
   }
 }
 
-int64_t mx4_dequant_tiles(int64_t rows, int64_t cols) { return (rows * mx4_blocks(cols) + 255) / 256; }
+template <typename T, int G>
+__global__ void __launch_bounds__(256) mx4_dequant_kernel(const Mx4DequantArgs<G> a) {
+  const Mx4DequantItem& it = a.item[G == 1 ? 0 : find_item(a, blockIdx.x)];
+  const uint32_t nb = static_cast<uint32_t>(mx4_blocks(it.cols)), sp = static_cast<uint32_t>(mx4_scale_pitch(it.cols));
+  const int64_t octs = static_cast<int64_t>(it.rows) * nb * 4;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) - it.tile0) * (256 * kOctsPerThread) + threadIdx.x;
+  uint32_t codes[kOctsPerThread], byte[kOctsPerThread];
+  int64_t at[kOctsPerThread];
+  int left[kOctsPerThread];
+#pragma unroll
+  for (int i = 0; i < kOctsPerThread; ++i) {
+    const int64_t u = first + i * 256;
+    left[i] = 0;
+    if (u < octs) {
+      const int64_t row = octs <= 0xffffffffll ? static_cast<uint32_t>(u) / (nb * 4) : u / (nb * 4);
+      const uint32_t col8 = static_cast<uint32_t>(u - row * (nb * 4));
+      codes[i] = *reinterpret_cast<const uint32_t*>(it.codes + u * 4);
+      byte[i] = it.scales[row * sp + col8 / 4];
+      left[i] = it.cols - static_cast<int>(col8) * 8;
+      at[i] = row * it.cols + col8 * 8;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kOctsPerThread; ++i)
+    if (left[i] > 0) store_oct(static_cast<T*>(it.dst) + at[i], codes[i], byte[i], left[i]);
+}
 
-hipError_t launch_mx4_dequant(int dt, const Mx4DequantArgs& a, int64_t tiles, hipStream_t s) {
+int64_t mx4_dequant_tiles(int64_t rows, int64_t cols) { return mx4_quant_tiles(rows, cols, false); }
+
+template <int G>
+hipError_t launch_mx4_dequant(int dt, const Mx4DequantArgs<G>& a, int64_t tiles, hipStream_t s) {
   const dim3 g(static_cast<uint32_t>(tiles));
-  if (dt == F32) mx4_dequant_kernel<float><<<g, 256, 0, s>>>(a);
-  else mx4_dequant_kernel<__bf16><<<g, 256, 0, s>>>(a);
+  if (dt == F32) mx4_dequant_kernel<float, G><<<g, 256, 0, s>>>(a);
+  else mx4_dequant_kernel<__bf16, G><<<g, 256, 0, s>>>(a);
   return hipGetLastError();
 }
+template hipError_t launch_mx4_dequant<1>(int, const Mx4DequantArgs<1>&, int64_t, hipStream_t);
+template hipError_t launch_mx4_dequant<kMx4Group>(int, const Mx4DequantArgs<kMx4Group>&, int64_t, hipStream_t);
 
 // ------------------------------------------------------------------ product
 // C = A B^T on the scaled matrix instruction, whose operands are 32 codes and

@@ -70,7 +70,37 @@ int esz_of(int dt) { return dt == MO_F32 ? 4 : 2; }
 
 // Launches are limited by kMx4Group matrices and by a grid of fewer than
 // 2^32 threads.
-constexpr int64_t kMaxTiles = 0xffffffff / 256;
+constexpr int64_t kMaxTiles = 0xffffffff / 512;
+
+// Launches over the matrices that want (or do not want) an image of the
+// transpose, up to G per launch.
+template <int G>
+int quant_group(const mo_mx4_item* items, int64_t count, int dtype, bool cols_image, hipStream_t s) {
+  const int esz = esz_of(dtype);
+  for (int64_t i = 0; i < count;) {
+    Mx4QuantArgs<G> a;
+    a.count = 0;
+    int64_t tiles = 0;
+    double bytes = 0;
+    for (; i < count && a.count < G; ++i) {
+      const mo_mx4_item& x = items[i];
+      if ((x.codes_t != nullptr) != cols_image) continue;
+      const int64_t t = mx4_quant_tiles(x.rows, x.cols, cols_image);
+      if (a.count && tiles + t > kMaxTiles) break;
+      a.item[a.count++] = {x.src, static_cast<uint8_t*>(x.codes), static_cast<uint8_t*>(x.scales),
+                           static_cast<uint8_t*>(x.codes_t), static_cast<uint8_t*>(x.scales_t), x.ld,
+                           static_cast<int32_t>(x.rows), static_cast<int32_t>(x.cols), tiles};
+      tiles += t;
+      bytes += static_cast<double>(x.rows) * x.cols * esz;
+      if (x.codes) bytes += static_cast<double>(code_bytes(x.rows, x.cols) + scale_bytes(x.rows, x.cols));
+      if (x.codes_t) bytes += static_cast<double>(code_bytes(x.cols, x.rows) + scale_bytes(x.cols, x.rows));
+    }
+    if (!a.count) continue;
+    ProfScope ps(MO_K_MX4_QUANT, s, bytes);
+    if (int rc = checked(launch_mx4_quant(dtype, cols_image, a, tiles, s), s, "mx4 quantize")) return rc;
+  }
+  return MO_OK;
+}
 
 int quantize(const mo_mx4_item* items, int64_t count, int dtype, hipStream_t s) {
   int rc;
@@ -90,7 +120,7 @@ int quantize(const mo_mx4_item* items, int64_t count, int dtype, hipStream_t s) 
       return fail(MO_EINVAL, "matrix %lld: an image needs codes and scales, and one image is needed", ll(i));
     if (!aligned(x.codes, 16) || !aligned(x.codes_t, 16) || !aligned(x.scales, 4) || !aligned(x.scales_t, 4))
       return fail(MO_EINVAL, "matrix %lld: codes must be 16-byte and scales 4-byte aligned", ll(i));
-    if (mx4_quant_tiles(x.rows, x.cols, x.codes != nullptr, x.codes_t != nullptr) > kMaxTiles)
+    if (mx4_quant_tiles(x.rows, x.cols, x.codes_t != nullptr) > kMaxTiles)
       return fail(MO_EINVAL, "matrix %lld: too large for one launch", ll(i));
     add_range(ranges, x.src, view_bytes(x.rows, x.cols, x.ld, esz), i, false);
     add_range(ranges, x.codes, code_bytes(x.rows, x.cols), i, true);
@@ -99,25 +129,35 @@ int quantize(const mo_mx4_item* items, int64_t count, int dtype, hipStream_t s) 
     add_range(ranges, x.scales_t, scale_bytes(x.cols, x.rows), i, true);
   }
   if ((rc = check_overlap(ranges, "matrix"))) return rc;
+  if (count == 1) return quant_group<1>(items, count, dtype, items[0].codes_t != nullptr, s);
+  // matrices with an image of the transpose, then those without
+  for (bool cols_image : {true, false})
+    if ((rc = quant_group<kMx4Group>(items, count, dtype, cols_image, s))) return rc;
+  return MO_OK;
+}
+
+// Launches over the images of one kind, up to G per launch.
+template <int G>
+int dequant_group(const mo_mx4_image* images, void* const* dst, int64_t count, int dtype, hipStream_t s) {
+  const int esz = esz_of(dtype);
   for (int64_t i = 0; i < count;) {
-    Mx4QuantArgs a{};
+    Mx4DequantArgs<G> a;
+    a.count = 0;
     int64_t tiles = 0;
     double bytes = 0;
-    while (i < count && a.count < kMx4Group) {
-      const mo_mx4_item& x = items[i];
-      const int64_t t = mx4_quant_tiles(x.rows, x.cols, x.codes != nullptr, x.codes_t != nullptr);
+    while (i < count && a.count < G) {
+      const mo_mx4_image& x = images[i];
+      const int64_t t = mx4_dequant_tiles(x.rows, x.cols);
       if (a.count && tiles + t > kMaxTiles) break;
-      a.item[a.count++] = {x.src, static_cast<uint8_t*>(x.codes), static_cast<uint8_t*>(x.scales),
-                           static_cast<uint8_t*>(x.codes_t), static_cast<uint8_t*>(x.scales_t), x.ld,
+      a.item[a.count++] = {static_cast<const uint8_t*>(x.codes), static_cast<const uint8_t*>(x.scales), dst[i],
                            static_cast<int32_t>(x.rows), static_cast<int32_t>(x.cols), tiles};
       tiles += t;
-      bytes += static_cast<double>(x.rows) * x.cols * esz;
-      if (x.codes) bytes += static_cast<double>(code_bytes(x.rows, x.cols) + scale_bytes(x.rows, x.cols));
-      if (x.codes_t) bytes += static_cast<double>(code_bytes(x.cols, x.rows) + scale_bytes(x.cols, x.rows));
+      bytes += static_cast<double>(x.rows) * x.cols * esz +
+               static_cast<double>(code_bytes(x.rows, x.cols) + scale_bytes(x.rows, x.cols));
       ++i;
     }
-    ProfScope ps(MO_K_MX4_QUANT, s, bytes);
-    if ((rc = checked(launch_mx4_quant(dtype, a, tiles, s), s, "mx4 quantize"))) return rc;
+    ProfScope ps(MO_K_MX4_DEQUANT, s, bytes);
+    if (int rc = checked(launch_mx4_dequant(dtype, a, tiles, s), s, "mx4 dequantize")) return rc;
   }
   return MO_OK;
 }
@@ -139,25 +179,7 @@ int dequantize(const mo_mx4_image* images, void* const* dst, int64_t count, int 
     add_range(ranges, dst[i], view_bytes(x.rows, x.cols, x.cols, esz), i, true);
   }
   if ((rc = check_overlap(ranges, "image"))) return rc;
-  for (int64_t i = 0; i < count;) {
-    Mx4DequantArgs a{};
-    int64_t tiles = 0;
-    double bytes = 0;
-    while (i < count && a.count < kMx4Group) {
-      const mo_mx4_image& x = images[i];
-      const int64_t t = mx4_dequant_tiles(x.rows, x.cols);
-      if (a.count && tiles + t > kMaxTiles) break;
-      a.item[a.count++] = {static_cast<const uint8_t*>(x.codes), static_cast<const uint8_t*>(x.scales), dst[i],
-                           static_cast<int32_t>(x.rows), static_cast<int32_t>(x.cols), tiles};
-      tiles += t;
-      bytes += static_cast<double>(x.rows) * x.cols * esz +
-               static_cast<double>(code_bytes(x.rows, x.cols) + scale_bytes(x.rows, x.cols));
-      ++i;
-    }
-    ProfScope ps(MO_K_MX4_DEQUANT, s, bytes);
-    if ((rc = checked(launch_mx4_dequant(dtype, a, tiles, s), s, "mx4 dequantize"))) return rc;
-  }
-  return MO_OK;
+  return count == 1 ? dequant_group<1>(images, dst, count, dtype, s) : dequant_group<kMx4Group>(images, dst, count, dtype, s);
 }
 
 int matmul(const mo_mx4_image* a, const mo_mx4_image* b, void* out, int out_dtype, int64_t ldo, int accumulate,

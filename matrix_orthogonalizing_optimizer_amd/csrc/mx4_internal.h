@@ -11,8 +11,8 @@ namespace mo {
 __host__ __device__ inline int64_t mx4_blocks(int64_t cols) { return (cols + 31) / 32; }
 __host__ __device__ inline int64_t mx4_scale_pitch(int64_t cols) { return (mx4_blocks(cols) + 3) / 4 * 4; }
 
-// Quantisation of up to kMx4Group matrices per launch; tile0 is the first
-// workgroup of the matrix.
+// Quantisation of up to kMx4Group matrices per launch (G of them, or 1, whose
+// launch arguments are smaller); tile0 is the first workgroup of the matrix.
 constexpr int kMx4Group = 48;
 struct Mx4QuantItem {
   const void* src;
@@ -21,8 +21,9 @@ struct Mx4QuantItem {
   int32_t rows, cols;
   int64_t tile0;
 };
+template <int G>
 struct Mx4QuantArgs {
-  Mx4QuantItem item[kMx4Group];
+  Mx4QuantItem item[G];
   int count;
 };
 
@@ -32,8 +33,9 @@ struct Mx4DequantItem {
   int32_t rows, cols;
   int64_t tile0;
 };
+template <int G>
 struct Mx4DequantArgs {
-  Mx4DequantItem item[kMx4Group];
+  Mx4DequantItem item[G];
   int count;
 };
 
@@ -52,10 +54,12 @@ struct Mx4MatmulArgs {
 constexpr int64_t kMx4MaxCols = int64_t{1} << 25;
 bool mx4_matmul_fits(int64_t m, int64_t n);
 
-int64_t mx4_quant_tiles(int64_t rows, int64_t cols, bool row_image, bool col_image);
+int64_t mx4_quant_tiles(int64_t rows, int64_t cols, bool cols_image);
 int64_t mx4_dequant_tiles(int64_t rows, int64_t cols);
-hipError_t launch_mx4_quant(int dt, const Mx4QuantArgs& a, int64_t tiles, hipStream_t s);
-hipError_t launch_mx4_dequant(int dt, const Mx4DequantArgs& a, int64_t tiles, hipStream_t s);
+template <int G>
+hipError_t launch_mx4_quant(int dt, bool cols_image, const Mx4QuantArgs<G>& a, int64_t tiles, hipStream_t s);
+template <int G>
+hipError_t launch_mx4_dequant(int dt, const Mx4DequantArgs<G>& a, int64_t tiles, hipStream_t s);
 hipError_t launch_mx4_matmul(int out_dt, const Mx4MatmulArgs& a, hipStream_t s);
 
 }  // namespace mo
