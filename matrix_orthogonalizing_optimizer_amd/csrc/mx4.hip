@@ -422,15 +422,26 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
 }
 
+// lds_dma16 where `go` (wave-uniform) is not 0.  The branch is inside, so that
+// the loop around it stays one block for the compiler, which would otherwise
+// move products across the barrier.
+__device__ __forceinline__ void lds_dma16_if(int go, const void* sbase, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lmx4_skip%=\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+               "global_load_lds_dwordx4 %0, %1\n.Lmx4_skip%=:"
+               :
+               : "v"(voff), "s"(sbase), "s"(lds_base), "s"(__builtin_amdgcn_readfirstlane(go))
+               : "memory", "m0", "scc");
+}
+
 template <int TM, int TN, int WM, int WN, int NST, typename T>
-__global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4MatmulArgs p) {
+__global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1 : 2) mx4_tile_kernel(const Mx4MatmulArgs p) {
   constexpr int NW = WM * WN, FM = TM / (32 * WM), FN = TN / (32 * WN);
   constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW);      // code requests of a wave and stage
   constexpr int SA = TM / 64, SB = TN / 64;                    // scale requests of a group of stages
   constexpr int DPW = DA + DB;
   constexpr int kStage = (TM + TN) * kStageRow, kScales = NST * kStage, kGroup = (TM + TN) * 16;
   static_assert(SA <= NW && SB <= NW, "one scale request of each operand per wave (some waves repeat one)");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * kStage + kGroup + 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * kStage + 2 * kGroup];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int r32 = lane & 31, half = lane >> 5;
@@ -476,13 +487,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4Matm
     if constexpr (i < DA) lds_dma16(uniform_ptr(a0 + t * 64), arow[i] - back, lds0 + to + (wave * DA + i) * 1024);
     else lds_dma16(uniform_ptr(b0 + t * 64), brow[i - DA] - back, lds0 + to + TM * kStageRow + (wave * DB + i - DA) * 1024);
   };
-  // The scale dwords of a group of stages 4 g .. 4 g + 3, or the row's last
-  // four if those are fewer: `lead` dwords of an earlier group then come first.
-  const int dwords = p.sp / 4, groups = (stages + 3) / 4;
-  auto request_scales = [&](int g) __attribute__((always_inline)) {
-    const int off = min(4 * g, dwords - 4) * 4;
-    lds_dma16(uniform_ptr(sa0 + off), asrow, lds0 + kScales + (wave % SA) * 1024);
-    lds_dma16(uniform_ptr(sb0 + off), bsrow, lds0 + kScales + TM * 16 + (wave % SB) * 1024);
+  // The scale dwords of a group of stages 4 g .. 4 g + 3 (the row's last four
+  // if those are fewer), two groups in turn in LDS.
+  const int dwords = p.sp / 4;
+  auto first_of = [&](int g) __attribute__((always_inline)) { return min(4 * g, dwords - 4); };
+  auto request_scales = [&](int g, int go) __attribute__((always_inline)) {
+    const uint32_t to = lds0 + kScales + (g & 1) * kGroup;
+    const int off = first_of(g) * 4;
+    lds_dma16_if(go, uniform_ptr(sa0 + off), asrow, to + (wave % SA) * 1024);
+    lds_dma16_if(go, uniform_ptr(sb0 + off), bsrow, to + TM * 16 + (wave % SB) * 1024);
   };
   // bytes by which the lane's chunk of stage t lies past the last block
   auto past = [&](int t) __attribute__((always_inline)) {
@@ -500,14 +513,17 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4Matm
   auto frag = [&](const uint8_t* base, uint32_t at, int f, int s) __attribute__((always_inline)) -> u32x4v {
     return *reinterpret_cast<const u32x4v*>(base + (at + xs[s]) + f * 32 * kStageRow);
   };
-  auto scale = [&](const uint8_t* base, int g, int f) __attribute__((always_inline)) -> u32x4v {
-    const int lead = max(4 * g - (dwords - 4), 0);     // what follows a row's last dword is not used
-    return *reinterpret_cast<const u32x4a4*>(base + f * 512 + lead * 4);
+  // the scale dword of fragment f in stage t
+  auto scale_at = [&](int t) __attribute__((always_inline)) -> uint32_t {
+    const int g = t / 4;
+    return static_cast<uint32_t>((g & 1) * kGroup + (t - first_of(g)) * 4);
+  };
+  auto scale = [&](const uint8_t* base, uint32_t sat, int f) __attribute__((always_inline)) -> uint32_t {
+    return *reinterpret_cast<const uint32_t*>(base + sat + f * 512);
   };
 
   f32x16v acc[FM][FN] = {};
   u32x4v af[2][FM], bf[2][FN];
-  u32x4v as[FM], bs[FN];
   uint32_t sa[FM], sb[FN], san[FM], sbn[FN];
   // the lane's two scale bytes of stage t in the low half of a dword, bytes
   // of blocks past the end cleared
@@ -524,7 +540,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4Matm
   constexpr int kFirst = [when]() constexpr { int n = 0; while (n < DPW && when(n) < NP) ++n; return n; }();
   static_assert(when(DPW - 1) < 2 * NP, "");
 
-  request_scales(0);
+  request_scales(0, 1);
   unroll<NST>([&](auto Q) __attribute__((always_inline)) {
     const int t = min(static_cast<int>(Q), stages - 1);
     const uint32_t back = past(t);
@@ -539,25 +555,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4Matm
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
       af[0][f] = frag(abase, 0, f, 0);
-      as[f] = scale(asbase, 0, f);
-      sa[f] = (as[f][0] & keep) >> (16 * half);
+      sa[f] = (scale(asbase, scale_at(0), f) & keep) >> (16 * half);
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
       bf[0][f] = frag(bbase, 0, f, 0);
-      bs[f] = scale(bsbase, 0, f);
-      sb[f] = (bs[f][0] & keep) >> (16 * half);
+      sb[f] = (scale(bsbase, scale_at(0), f) & keep) >> (16 * half);
     }
   }
 
   uint32_t at = 0, prev = (NST - 1) * kStage;          // places in LDS of this stage and of the one before
   int tp = min(NST - 1, stages - 1);                   // the stage whose requests into `prev` are under way
   uint32_t backp = past(tp);
-  // stage t, number q of its group
-  auto stage = [&](int t, auto Q) __attribute__((always_inline)) {
-    constexpr int q = Q;
+  for (int t = 0; t < stages; ++t) {
     const uint32_t next = at + kStage == NST * kStage ? 0u : at + kStage;
-    const uint32_t keep = keep_of(t + 1);
+    const uint32_t keep = keep_of(t + 1), sat = scale_at(min(t + 1, stages - 1));
     unroll<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int s = S, cur = s, nxt = cur ^ 1;
       if constexpr (s == 1) {
@@ -577,15 +589,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4Matm
           constexpr int fa = r == 0 ? 0 : r > FN && r < NR ? r - FN : -1, fb = r >= 1 && r <= FN ? r - 1 : -1;
           if constexpr (fa >= 0) {
             af[nxt][fa] = frag(abase, from, fa, nxt);
-            if constexpr (s == 1 && q == 3) as[fa] = scale(asbase, min(t / 4 + 1, groups - 1), fa);
+            if constexpr (s == 1) san[fa] = scale(asbase, sat, fa);
           }
           if constexpr (fb >= 0) {
             bf[nxt][fb] = frag(bbase, from, fb, nxt);
-            if constexpr (s == 1 && q == 3) bs[fb] = scale(bsbase, min(t / 4 + 1, groups - 1), fb);
+            if constexpr (s == 1) sbn[fb] = scale(bsbase, sat, fb);
           }
         });
         if constexpr (P == 0 && s == 1) {
-          if constexpr (q == 0) request_scales(min(t / 4 + 1, groups - 1));
+          // into the place of the group before this one, read to its end
+          request_scales(t / 4 + 1, (t & 3) == 0 && t + 4 < stages);
           prev = at;
           tp = min(t + NST, stages - 1);               // past the end: the last stage again, unused
           backp = past(tp);
@@ -593,31 +606,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) mx4_tile_kernel(const Mx4Matm
         unroll<DPW>([&](auto C) __attribute__((always_inline)) {
           if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, tp, backp, prev);
         });
-        if constexpr (P == NP - 1 && s == 1) {
-#pragma unroll
-          for (int f = 0; f < FM; ++f) san[f] = (as[f][(q + 1) & 3] & keep) >> (16 * half);
-#pragma unroll
-          for (int f = 0; f < FN; ++f) sbn[f] = (bs[f][(q + 1) & 3] & keep) >> (16 * half);
-        }
         __builtin_amdgcn_sched_barrier(0);
       });
     });
 #pragma unroll
-    for (int f = 0; f < FM; ++f) sa[f] = san[f];
+    for (int f = 0; f < FM; ++f) sa[f] = (san[f] & keep) >> (16 * half);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sb[f] = sbn[f];
+    for (int f = 0; f < FN; ++f) sb[f] = (sbn[f] & keep) >> (16 * half);
     at = next;
-  };
-
-  for (int t = 0;; t += 4) {
-    stage(t, std::integral_constant<int, 0>{});
-    if (t + 1 >= stages) break;
-    stage(t + 1, std::integral_constant<int, 1>{});
-    if (t + 2 >= stages) break;
-    stage(t + 2, std::integral_constant<int, 2>{});
-    if (t + 3 >= stages) break;
-    stage(t + 3, std::integral_constant<int, 3>{});
-    if (t + 4 >= stages) break;
   }
   wait_loads<0>();                                     // no request outlives the workgroup
 
@@ -827,7 +823,7 @@ hipError_t launch_mx4_matmul(int out_dt, const Mx4MatmulArgs& a, hipStream_t s) 
   if (a.nb <= 12) return run_direct(out_dt, a, s);
   const int64_t t256 = ((a.m + 255) / 256) * static_cast<int64_t>((a.n + 255) / 256);
   const int64_t t128 = ((a.m + 127) / 128) * static_cast<int64_t>((a.n + 127) / 128);
-  if (t256 >= 192) return run_tile<256, 256, 2, 4, 4>(out_dt, a, s);
+  if (t256 >= 192) return run_tile<256, 256, 2, 2, 4>(out_dt, a, s);
   if (t128 >= 192) return run_tile<128, 128, 2, 2, 4>(out_dt, a, s);
   return run_tile<64, 64, 2, 2, 4>(out_dt, a, s);
 }
