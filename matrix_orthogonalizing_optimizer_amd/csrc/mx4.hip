@@ -396,6 +396,29 @@ __device__ __forceinline__ void store_out(T* o, float v, int accumulate) {
   *o = static_cast<T>(v);
 }
 
+// Four consecutive outputs, n of them inside.
+template <typename T>
+__device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate) {
+  if (n >= 4) {
+    if constexpr (sizeof(T) == 4) {
+      if (accumulate) v += *reinterpret_cast<const f32x4u*>(o);
+      *reinterpret_cast<f32x4u*>(o) = v;
+    } else {
+      typedef uint32_t u32x2u2 __attribute__((ext_vector_type(2), aligned(2)));
+      if (accumulate) {
+        const u32x2u2 w = *reinterpret_cast<const u32x2u2*>(o);
+        v += f32x4v{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                    __uint_as_float(w[1] & 0xffff0000u)};
+      }
+      *reinterpret_cast<u32x2u2*>(o) = u32x2u2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) store_out(o + k, v[k], accumulate);
+  }
+}
+
 // Tile kernel.  The contraction runs in stages of 4 blocks (128 columns):
 // two instructions per output fragment, lanes 0..31 of a wave taking the
 // stage's first two blocks and lanes 32..63 the others (any order of blocks
@@ -430,6 +453,15 @@ __device__ __forceinline__ void lds_dma16_if(int go, const void* sbase, uint32_t
                "global_load_lds_dwordx4 %0, %1\n.Lmx4_skip%=:"
                :
                : "v"(voff), "s"(sbase), "s"(lds_base), "s"(__builtin_amdgcn_readfirstlane(go))
+               : "memory", "m0", "scc");
+}
+
+// lds_dma16 to lds_base + kPlus.
+template <int kPlus>
+__device__ __forceinline__ void lds_dma16_at(const void* sbase, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(voff), "s"(sbase), "s"(lds_base), "n"(kPlus)
                : "memory", "m0", "scc");
 }
 
@@ -481,25 +513,26 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   for (int i = 0; i < DB; ++i) brow[i] = min(16 * (wave * DB + i) + lane / 4, nlast) * pitch + chunk * 16;
   const uint32_t asrow = min(64 * (wave % SA) + lane, mlast) * sp, bsrow = min(64 * (wave % SB) + lane, nlast) * sp;
   const uint32_t lds0 = lds_addr(smem);
-  // one of the wave's requests of stage t into the place at byte `to`
-  auto request = [&](auto I, int t, uint32_t back, uint32_t to) __attribute__((always_inline)) {
+  const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * kStageRow + wave * DB * 1024;
+  // Bytes by which the lane's chunk of the last stage lies past the last
+  // block, which it then loads in its place.
+  const uint32_t back_last = static_cast<uint32_t>(max((stages - 1) * 4 + chunk - (p.nb - 1), 0)) * 16u;
+  // request i of a stage whose codes start at pa and pb, into the place at byte
+  // `to`, `back` as above
+  auto request = [&](auto I, const uint8_t* pa, const uint8_t* pb, uint32_t back, uint32_t to) __attribute__((always_inline)) {
     constexpr int i = I;
-    if constexpr (i < DA) lds_dma16(uniform_ptr(a0 + t * 64), arow[i] - back, lds0 + to + (wave * DA + i) * 1024);
-    else lds_dma16(uniform_ptr(b0 + t * 64), brow[i - DA] - back, lds0 + to + TM * kStageRow + (wave * DB + i - DA) * 1024);
+    if constexpr (i < DA) lds_dma16_at<i * 1024>(pa, arow[i] - back, dst + to);
+    else lds_dma16_at<(i - DA) * 1024>(pb, brow[i - DA] - back, dstb + to);
   };
   // The scale dwords of a group of stages 4 g .. 4 g + 3 (the row's last four
   // if those are fewer), two groups in turn in LDS.
-  const int dwords = p.sp / 4;
-  auto first_of = [&](int g) __attribute__((always_inline)) { return min(4 * g, dwords - 4); };
-  auto request_scales = [&](int g, int go) __attribute__((always_inline)) {
+  const int last_group = (stages - 1) / 4, dwords = p.sp / 4;
+  const uint32_t shift = static_cast<uint32_t>(max(4 * last_group - (dwords - 4), 0)) * 4u;   // of the last group
+  auto request_scales = [&](bool b, int g, int go) __attribute__((always_inline)) {
     const uint32_t to = lds0 + kScales + (g & 1) * kGroup;
-    const int off = first_of(g) * 4;
-    lds_dma16_if(go, uniform_ptr(sa0 + off), asrow, to + (wave % SA) * 1024);
-    lds_dma16_if(go, uniform_ptr(sb0 + off), bsrow, to + TM * 16 + (wave % SB) * 1024);
-  };
-  // bytes by which the lane's chunk of stage t lies past the last block
-  auto past = [&](int t) __attribute__((always_inline)) {
-    return static_cast<uint32_t>(max(t * 4 + chunk - (p.nb - 1), 0)) * 16u;
+    const int off = min(4 * g, dwords - 4) * 4;
+    if (b) lds_dma16_if(go, uniform_ptr(sb0 + off), bsrow, to + TM * 16 + (wave % SB) * 1024);
+    else lds_dma16_if(go, uniform_ptr(sa0 + off), asrow, to + (wave % SA) * 1024);
   };
 
   // Fragments: 32 rows, lane l holds row l & 31.
@@ -515,8 +548,7 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   };
   // the scale dword of fragment f in stage t
   auto scale_at = [&](int t) __attribute__((always_inline)) -> uint32_t {
-    const int g = t / 4;
-    return static_cast<uint32_t>((g & 1) * kGroup + (t - first_of(g)) * 4);
+    return static_cast<uint32_t>(((t >> 2) & 1) * kGroup + (t & 3) * 4) + ((t >> 2) == last_group ? shift : 0u);
   };
   auto scale = [&](const uint8_t* base, uint32_t sat, int f) __attribute__((always_inline)) -> uint32_t {
     return *reinterpret_cast<const uint32_t*>(base + sat + f * 512);
@@ -525,12 +557,10 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   f32x16v acc[FM][FN] = {};
   u32x4v af[2][FM], bf[2][FN];
   uint32_t sa[FM], sb[FN], san[FM], sbn[FN];
-  // the lane's two scale bytes of stage t in the low half of a dword, bytes
-  // of blocks past the end cleared
-  auto keep_of = [&](int t) __attribute__((always_inline)) -> uint32_t {
-    const int left = p.nb - 4 * t;
-    return left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1u : 0u;
-  };
+  // The lane's two scale bytes of a stage in the low half of a dword; the
+  // last stage's bytes of blocks past the end are cleared.
+  const uint32_t keep_last = (p.nb & 3) ? (1u << (8 * (p.nb & 3))) - 1u : ~0u;
+  auto keep_of = [&](int t) __attribute__((always_inline)) -> uint32_t { return t == stages - 1 ? keep_last : ~0u; };
 
   // Request c of a stage follows product number when(c) of the 2 NP products
   // between a barrier and the next: spread evenly, as the path from the
@@ -539,12 +569,15 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   constexpr auto when = [](int c) constexpr { return c * 2 * NP / DPW + (NP > 2 ? 1 : 0); };
   constexpr int kFirst = [when]() constexpr { int n = 0; while (n < DPW && when(n) < NP) ++n; return n; }();
   static_assert(when(DPW - 1) < 2 * NP, "");
+  constexpr int kScaleA = NP > 8 ? 3 : 0, kScaleB = NP > 8 ? 7 : NP / 2;
 
-  request_scales(0, 1);
+  request_scales(false, 0, 1);
+  request_scales(true, 0, 1);
   unroll<NST>([&](auto Q) __attribute__((always_inline)) {
     const int t = min(static_cast<int>(Q), stages - 1);
-    const uint32_t back = past(t);
-    unroll<Q == NST - 1 ? kFirst : DPW>([&](auto I) __attribute__((always_inline)) { request(I, t, back, Q * kStage); });
+    const uint8_t *pa = uniform_ptr(a0 + t * 64), *pb = uniform_ptr(b0 + t * 64);
+    const uint32_t back = t == stages - 1 ? back_last : 0u;
+    unroll<Q == NST - 1 ? kFirst : DPW>([&](auto I) __attribute__((always_inline)) { request(I, pa, pb, back, Q * kStage); });
   });
   wait_loads<(NST - 2) * DPW + kFirst>();
   __builtin_amdgcn_sched_barrier(0);
@@ -564,12 +597,14 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
     }
   }
 
-  uint32_t at = 0, prev = (NST - 1) * kStage;          // places in LDS of this stage and of the one before
-  int tp = min(NST - 1, stages - 1);                   // the stage whose requests into `prev` are under way
-  uint32_t backp = past(tp);
+  // Places in LDS of this stage and of the one before, whose requests (of
+  // stage tp, at pa and pb) are under way.
+  uint32_t at = 0, prev = (NST - 1) * kStage;
+  int tp = min(NST - 1, stages - 1);
+  const uint8_t *pa = uniform_ptr(a0 + tp * 64), *pb = uniform_ptr(b0 + tp * 64);
+  uint32_t backp = tp == stages - 1 ? back_last : 0u;
   for (int t = 0; t < stages; ++t) {
-    const uint32_t next = at + kStage == NST * kStage ? 0u : at + kStage;
-    const uint32_t keep = keep_of(t + 1), sat = scale_at(min(t + 1, stages - 1));
+    uint32_t next = 0, keep = 0, sat = 0;
     unroll<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int s = S, cur = s, nxt = cur ^ 1;
       if constexpr (s == 1) {
@@ -579,33 +614,45 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }
-      const uint32_t from = s == 1 ? next : at;
       constexpr int RP = (2 * NR + NP - 1) / NP;
+      // A product at a time, and behind each a little of everything else: a
+      // wave issues a handful of instructions while its product runs.
       unroll<NP>([&](auto P) __attribute__((always_inline)) {
         constexpr int i = P / FN, j = P % FN;
-        acc[i][j] = mfma32<s>(af[cur][i], bf[cur][j], acc[i][j], sa[i], sb[j]);
+        acc[i][j] = mfma32<s>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
         unroll<RP>([&](auto R) __attribute__((always_inline)) {
           constexpr int r = P * RP + R;                 // order of need: A's first, all of B, the rest of A
           constexpr int fa = r == 0 ? 0 : r > FN && r < NR ? r - FN : -1, fb = r >= 1 && r <= FN ? r - 1 : -1;
           if constexpr (fa >= 0) {
-            af[nxt][fa] = frag(abase, from, fa, nxt);
+            af[nxt][fa] = frag(abase, s == 1 ? next : at, fa, nxt);
             if constexpr (s == 1) san[fa] = scale(asbase, sat, fa);
           }
           if constexpr (fb >= 0) {
-            bf[nxt][fb] = frag(bbase, from, fb, nxt);
+            bf[nxt][fb] = frag(bbase, s == 1 ? next : at, fb, nxt);
             if constexpr (s == 1) sbn[fb] = scale(bsbase, sat, fb);
           }
         });
-        if constexpr (P == 0 && s == 1) {
-          // into the place of the group before this one, read to its end
-          request_scales(t / 4 + 1, (t & 3) == 0 && t + 4 < stages);
+        if constexpr (s == 1 && P == 0) {
+          // past the end: the last stage again, unused
+          const bool more = tp + 1 < stages;
+          tp += more;
+          pa = uniform_ptr(pa + (more ? 64 : 0));
+          pb = uniform_ptr(pb + (more ? 64 : 0));
+          backp = tp == stages - 1 ? back_last : 0u;
           prev = at;
-          tp = min(t + NST, stages - 1);               // past the end: the last stage again, unused
-          backp = past(tp);
         }
         unroll<DPW>([&](auto C) __attribute__((always_inline)) {
-          if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, tp, backp, prev);
+          if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, pa, pb, backp, prev);
         });
+        // the next group's scales, into the place of the group before this
+        // one, which has been read to its end
+        if constexpr (s == 1 && P == kScaleA) request_scales(false, t / 4 + 1, (t & 3) == 0 && t + 4 < stages);
+        if constexpr (s == 1 && P == kScaleB) request_scales(true, t / 4 + 1, (t & 3) == 0 && t + 4 < stages);
+        if constexpr (s == 0 && P == NP - 1 - (NP > 4)) {
+          next = at + kStage == NST * kStage ? 0u : at + kStage;
+          keep = keep_of(t + 1);
+          sat = scale_at(min(t + 1, stages - 1));
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
     });
@@ -617,17 +664,31 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   }
   wait_loads<0>();                                     // no request outlives the workgroup
 
-  T* out = static_cast<T*>(p.out);
+  __syncthreads();
+  // Lane l holds row l & 31 of each 32 x 32 fragment (the operands are given
+  // in reverse), four consecutive columns at a time.  Each wave turns 32 rows
+  // at a time through LDS of its own, so that rows leave as whole lines; the
+  // 16 bytes of padding per row spread 16 rows over all banks.
+  constexpr int W = TN / WN, kPitch = W * 4 + 16, kLanes = W / 4;       // columns, and lanes to a row
+  static_assert(NW * 32 * kPitch <= NST * kStage, "the stages' places are free now");
+  uint8_t* turn = smem + wave * 32 * kPitch;
+  T* out = static_cast<T*>(p.out) + m0 * p.ldo + n0;
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+  for (int i = 0; i < FM; ++i) {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = wm * (TM / WM) + 32 * i + 8 * (e / 4) + 4 * half + e % 4;
-        const int c = wn * (TN / WN) + 32 * j + r32;
-        if (r <= mlast && c <= nlast) store_out(out + (m0 + r) * p.ldo + n0 + c, acc[i][j][e], p.accumulate);
-      }
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4v*>(turn + r32 * kPitch + (32 * j + 8 * e + 4 * half) * 4) =
+            f32x4v{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+#pragma unroll
+    for (int k = 0; k < 32 * kLanes / 64; ++k) {
+      const int row = k * (64 / kLanes) + lane / kLanes, col = lane % kLanes * 4;
+      const f32x4v v = *reinterpret_cast<const f32x4v*>(turn + row * kPitch + col * 4);
+      const int r = wm * (TM / WM) + 32 * i + row, c = wn * W + col;
+      if (r <= mlast) store4_out(out + r * p.ldo + c, v, nlast + 1 - c, p.accumulate);
+    }
+  }
 }
 
 // Direct kernel, for contractions of at most 12 blocks (whose rows of scale
