@@ -424,8 +424,10 @@ __device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate
 // stage's first two blocks and lanes 32..63 the others (any order of blocks
 // is right as long as A and B agree).  LDS holds NST stages of both operands
 // and their scale dwords, filled by loads that bypass the registers:
-//   * scale bytes come for four stages at a time (16 bytes of a row): a
-//     request of 4 bytes per row costs as many cache lookups as the codes;
+//   * scale bytes come for 16 stages at a time (64 bytes of a row): a request
+//     costs a cache line's lookup and transfer per row however little of the
+//     line it takes (4 bytes a row and stage cost 40% of the kernel's time, 16
+//     bytes for four stages 13%);
 //   * a row of a stage is 4 chunks of 16 bytes, stored at chunk ^ ((row / 4)
 //     & 3): the 16 rows that a 16-byte read serves at a time then touch each
 //     of the 64 banks once;
@@ -469,10 +471,8 @@ template <int TM, int TN, int WM, int WN, int NST, typename T>
 __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1 : 2) mx4_tile_kernel(const Mx4MatmulArgs p) {
   constexpr int NW = WM * WN, FM = TM / (32 * WM), FN = TN / (32 * WN);
   constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW);      // code requests of a wave and stage
-  constexpr int SA = TM / 64, SB = TN / 64;                    // scale requests of a group of stages
   constexpr int DPW = DA + DB;
-  constexpr int kStage = (TM + TN) * kStageRow, kScales = NST * kStage, kGroup = (TM + TN) * 16;
-  static_assert(SA <= NW && SB <= NW, "one scale request of each operand per wave (some waves repeat one)");
+  constexpr int kStage = (TM + TN) * kStageRow, kScales = NST * kStage, kGroup = (TM + TN) * kStageRow;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * kStage + 2 * kGroup];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -511,7 +511,6 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   for (int i = 0; i < DA; ++i) arow[i] = min(16 * (wave * DA + i) + lane / 4, mlast) * pitch + chunk * 16;
 #pragma unroll
   for (int i = 0; i < DB; ++i) brow[i] = min(16 * (wave * DB + i) + lane / 4, nlast) * pitch + chunk * 16;
-  const uint32_t asrow = min(64 * (wave % SA) + lane, mlast) * sp, bsrow = min(64 * (wave % SB) + lane, nlast) * sp;
   const uint32_t lds0 = lds_addr(smem);
   const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * kStageRow + wave * DB * 1024;
   // Bytes by which the lane's chunk of the last stage lies past the last
@@ -524,34 +523,39 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
     if constexpr (i < DA) lds_dma16_at<i * 1024>(pa, arow[i] - back, dst + to);
     else lds_dma16_at<(i - DA) * 1024>(pb, brow[i - DA] - back, dstb + to);
   };
-  // The scale dwords of a group of stages 4 g .. 4 g + 3 (the row's last four
-  // if those are fewer), two groups in turn in LDS.
-  const int last_group = (stages - 1) / 4, dwords = p.sp / 4;
-  const uint32_t shift = static_cast<uint32_t>(max(4 * last_group - (dwords - 4), 0)) * 4u;   // of the last group
-  auto request_scales = [&](bool b, int g, int go) __attribute__((always_inline)) {
-    const uint32_t to = lds0 + kScales + (g & 1) * kGroup;
-    const int off = min(4 * g, dwords - 4) * 4;
-    if (b) lds_dma16_if(go, uniform_ptr(sb0 + off), bsrow, to + TM * 16 + (wave % SB) * 1024);
-    else lds_dma16_if(go, uniform_ptr(sa0 + off), asrow, to + (wave % SA) * 1024);
+  // Scale bytes come for a group of 16 stages, 64 bytes of a row, chunks of 16
+  // placed as those of the codes; two groups in turn in LDS.  A chunk that
+  // would pass the row's end is the row's last 16 bytes: its dwords then lie
+  // `shift` further on.
+  const int last_chunk = (stages - 1) / 4, last_group = last_chunk / 4;
+  const uint32_t shift = static_cast<uint32_t>(last_chunk * 16) - min(static_cast<uint32_t>(last_chunk * 16), sp - 16u);
+  auto request_scales = [&](int q, int g, int go) __attribute__((always_inline)) {
+    const bool b = q >= DA;
+    const int row = 16 * (b ? wave * DB + q - DA : wave * DA + q) + lane / 4;
+    const uint32_t off = min(static_cast<uint32_t>(g * 64 + chunk * 16), sp - 16u);
+    const uint32_t to = (g & 1) * kGroup + kScales + (b ? TM * kStageRow + (wave * DB + q - DA) * 1024 : (wave * DA + q) * 1024);
+    lds_dma16_if(go, uniform_ptr(b ? sb0 : sa0), __umul24(min(row, b ? nlast : mlast), sp) + off, lds0 + to);
   };
 
   // Fragments: 32 rows, lane l holds row l & 31.
   const uint8_t* abase = smem + (wm * (TM / WM) + r32) * kStageRow;
   const uint8_t* bbase = smem + TM * kStageRow + (wn * (TN / WN) + r32) * kStageRow;
-  const uint8_t* asbase = smem + kScales + (wm * (TM / WM) + r32) * 16;
-  const uint8_t* bsbase = smem + kScales + TM * 16 + (wn * (TN / WN) + r32) * 16;
+  const uint8_t* asbase = smem + kScales + (wm * (TM / WM) + r32) * kStageRow;
+  const uint8_t* bsbase = smem + kScales + (TM + wn * (TN / WN) + r32) * kStageRow;
   uint32_t xs[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) xs[s] = static_cast<uint32_t>(((half * 2 + s) ^ ((r32 >> 2) & 3)) * 16);
   auto frag = [&](const uint8_t* base, uint32_t at, int f, int s) __attribute__((always_inline)) -> u32x4v {
     return *reinterpret_cast<const u32x4v*>(base + (at + xs[s]) + f * 32 * kStageRow);
   };
-  // the scale dword of fragment f in stage t
+  // the lane's offset to the scale dwords of stage t, and that of fragment f
   auto scale_at = [&](int t) __attribute__((always_inline)) -> uint32_t {
-    return static_cast<uint32_t>(((t >> 2) & 1) * kGroup + (t & 3) * 4) + ((t >> 2) == last_group ? shift : 0u);
+    const int c = t >> 2;
+    return static_cast<uint32_t>(((c >> 2) & 1) * kGroup + (t & 3) * 4) + (c == last_chunk ? shift : 0u) +
+           static_cast<uint32_t>(((c & 3) ^ ((r32 >> 2) & 3)) * 16);
   };
   auto scale = [&](const uint8_t* base, uint32_t sat, int f) __attribute__((always_inline)) -> uint32_t {
-    return *reinterpret_cast<const uint32_t*>(base + sat + f * 512);
+    return *reinterpret_cast<const uint32_t*>(base + sat + f * 32 * kStageRow);
   };
 
   f32x16v acc[FM][FN] = {};
@@ -569,10 +573,10 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   constexpr auto when = [](int c) constexpr { return c * 2 * NP / DPW + (NP > 2 ? 1 : 0); };
   constexpr int kFirst = [when]() constexpr { int n = 0; while (n < DPW && when(n) < NP) ++n; return n; }();
   static_assert(when(DPW - 1) < 2 * NP, "");
-  constexpr int kScaleA = NP > 8 ? 3 : 0, kScaleB = NP > 8 ? 7 : NP / 2;
+  constexpr int kScaleAt = NP > 8 ? 11 : NP - 1;
+  static_assert(DPW <= 8, "a group's requests are under way long before its first stage");
 
-  request_scales(false, 0, 1);
-  request_scales(true, 0, 1);
+  for (int q = 0; q < DPW; ++q) request_scales(q, 0, 1);
   unroll<NST>([&](auto Q) __attribute__((always_inline)) {
     const int t = min(static_cast<int>(Q), stages - 1);
     const uint8_t *pa = uniform_ptr(a0 + t * 64), *pb = uniform_ptr(b0 + t * 64);
@@ -644,10 +648,10 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
         unroll<DPW>([&](auto C) __attribute__((always_inline)) {
           if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, pa, pb, backp, prev);
         });
-        // the next group's scales, into the place of the group before this
-        // one, which has been read to its end
-        if constexpr (s == 1 && P == kScaleA) request_scales(false, t / 4 + 1, (t & 3) == 0 && t + 4 < stages);
-        if constexpr (s == 1 && P == kScaleB) request_scales(true, t / 4 + 1, (t & 3) == 0 && t + 4 < stages);
+        // the next group's scales, a request a stage, into the place of the
+        // group before this one, which has been read to its end
+        if constexpr (s == 1 && P == kScaleAt)
+          request_scales(t & 15, t / 16 + 1, (t & 15) < DPW && t / 16 < last_group);
         if constexpr (s == 0 && P == NP - 1 - (NP > 4)) {
           next = at + kStage == NST * kStage ? 0u : at + kStage;
           keep = keep_of(t + 1);
@@ -884,9 +888,9 @@ hipError_t launch_mx4_matmul(int out_dt, const Mx4MatmulArgs& a, hipStream_t s) 
   if (a.nb <= 12) return run_direct(out_dt, a, s);
   const int64_t t256 = ((a.m + 255) / 256) * static_cast<int64_t>((a.n + 255) / 256);
   const int64_t t128 = ((a.m + 127) / 128) * static_cast<int64_t>((a.n + 127) / 128);
-  if (t256 >= 192) return run_tile<256, 256, 2, 2, 4>(out_dt, a, s);
-  if (t128 >= 192) return run_tile<128, 128, 2, 2, 4>(out_dt, a, s);
-  return run_tile<64, 64, 2, 2, 4>(out_dt, a, s);
+  if (t256 >= 192) return run_tile<256, 256, 2, 2, 3>(out_dt, a, s);
+  if (t128 >= 192) return run_tile<128, 128, 2, 2, 3>(out_dt, a, s);
+  return run_tile<64, 64, 2, 2, 3>(out_dt, a, s);
 }
 
 }  // namespace mo
