@@ -447,17 +447,6 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
 }
 
-// lds_dma16 where `go` (wave-uniform) is not 0.  The branch is inside, so that
-// the loop around it stays one block for the compiler, which would otherwise
-// move products across the barrier.
-__device__ __forceinline__ void lds_dma16_if(int go, const void* sbase, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lmx4_skip%=\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
-               "global_load_lds_dwordx4 %0, %1\n.Lmx4_skip%=:"
-               :
-               : "v"(voff), "s"(sbase), "s"(lds_base), "s"(__builtin_amdgcn_readfirstlane(go))
-               : "memory", "m0", "scc");
-}
-
 // lds_dma16 to lds_base + kPlus.
 template <int kPlus>
 __device__ __forceinline__ void lds_dma16_at(const void* sbase, uint32_t voff, uint32_t lds_base) {
@@ -511,6 +500,11 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   for (int i = 0; i < DA; ++i) arow[i] = min(16 * (wave * DA + i) + lane / 4, mlast) * pitch + chunk * 16;
 #pragma unroll
   for (int i = 0; i < DB; ++i) brow[i] = min(16 * (wave * DB + i) + lane / 4, nlast) * pitch + chunk * 16;
+  uint32_t asrow[DA], bsrow[DB];
+#pragma unroll
+  for (int i = 0; i < DA; ++i) asrow[i] = min(16 * (wave * DA + i) + lane / 4, mlast) * sp;
+#pragma unroll
+  for (int i = 0; i < DB; ++i) bsrow[i] = min(16 * (wave * DB + i) + lane / 4, nlast) * sp;
   const uint32_t lds0 = lds_addr(smem);
   const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * kStageRow + wave * DB * 1024;
   // Bytes by which the lane's chunk of the last stage lies past the last
@@ -529,12 +523,13 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   // `shift` further on.
   const int last_chunk = (stages - 1) / 4, last_group = last_chunk / 4;
   const uint32_t shift = static_cast<uint32_t>(last_chunk * 16) - min(static_cast<uint32_t>(last_chunk * 16), sp - 16u);
-  auto request_scales = [&](int q, int g, int go) __attribute__((always_inline)) {
-    const bool b = q >= DA;
-    const int row = 16 * (b ? wave * DB + q - DA : wave * DA + q) + lane / 4;
-    const uint32_t off = min(static_cast<uint32_t>(g * 64 + chunk * 16), sp - 16u);
-    const uint32_t to = (g & 1) * kGroup + kScales + (b ? TM * kStageRow + (wave * DB + q - DA) * 1024 : (wave * DA + q) * 1024);
-    lds_dma16_if(go, uniform_ptr(b ? sb0 : sa0), __umul24(min(row, b ? nlast : mlast), sp) + off, lds0 + to);
+  auto request_scales = [&](int g) __attribute__((always_inline)) {
+    const uint32_t off = min(static_cast<uint32_t>(g * 64 + chunk * 16), sp - 16u), to = (g & 1) * kGroup + kScales;
+    unroll<DPW>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = I;
+      if constexpr (i < DA) lds_dma16_at<i * 1024>(sa0, asrow[i] + off, dst + to);
+      else lds_dma16_at<(i - DA) * 1024>(sb0, bsrow[i - DA] + off, dstb + to);
+    });
   };
 
   // Fragments: 32 rows, lane l holds row l & 31.
@@ -573,10 +568,8 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   constexpr auto when = [](int c) constexpr { return c * 2 * NP / DPW + (NP > 2 ? 1 : 0); };
   constexpr int kFirst = [when]() constexpr { int n = 0; while (n < DPW && when(n) < NP) ++n; return n; }();
   static_assert(when(DPW - 1) < 2 * NP, "");
-  constexpr int kScaleAt = NP > 8 ? 11 : NP - 1;
-  static_assert(DPW <= 8, "a group's requests are under way long before its first stage");
 
-  for (int q = 0; q < DPW; ++q) request_scales(q, 0, 1);
+  request_scales(0);
   unroll<NST>([&](auto Q) __attribute__((always_inline)) {
     const int t = min(static_cast<int>(Q), stages - 1);
     const uint8_t *pa = uniform_ptr(a0 + t * 64), *pb = uniform_ptr(b0 + t * 64);
@@ -607,7 +600,12 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   int tp = min(NST - 1, stages - 1);
   const uint8_t *pa = uniform_ptr(a0 + tp * 64), *pb = uniform_ptr(b0 + tp * 64);
   uint32_t backp = tp == stages - 1 ? back_last : 0u;
-  for (int t = 0; t < stages; ++t) {
+  for (int g = 0; g <= last_group; ++g) {
+  // the next group's scales, into the place of the group before this one:
+  // its last dwords were read two barriers ago
+  if (g < last_group) request_scales(g + 1);
+  const int end = min(16 * g + 16, stages);
+  for (int t = 16 * g; t < end; ++t) {
     uint32_t next = 0, keep = 0, sat = 0;
     unroll<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int s = S, cur = s, nxt = cur ^ 1;
@@ -648,14 +646,10 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
         unroll<DPW>([&](auto C) __attribute__((always_inline)) {
           if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, pa, pb, backp, prev);
         });
-        // the next group's scales, a request a stage, into the place of the
-        // group before this one, which has been read to its end
-        if constexpr (s == 1 && P == kScaleAt)
-          request_scales(t & 15, t / 16 + 1, (t & 15) < DPW && t / 16 < last_group);
         if constexpr (s == 0 && P == NP - 1 - (NP > 4)) {
           next = at + kStage == NST * kStage ? 0u : at + kStage;
           keep = keep_of(t + 1);
-          sat = scale_at(min(t + 1, stages - 1));
+          sat = scale_at(t + 1);                       // (past the end: a place that holds something)
         }
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -665,6 +659,7 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
 #pragma unroll
     for (int f = 0; f < FN; ++f) sb[f] = (sbn[f] & keep) >> (16 * half);
     at = next;
+  }
   }
   wait_loads<0>();                                     // no request outlives the workgroup
 

@@ -153,7 +153,9 @@ def _check_product(got, av, bv, k, add=None):
 
 MM = [(1, 1, 1), (1, 17, 33), (3, 5, 31), (16, 16, 128), (17, 33, 129), (1, 300, 2048), (2, 130, 4097), (15, 257, 500),
       (31, 64, 96), (64, 64, 512), (65, 63, 640), (128, 128, 1024), (129, 255, 1025), (200, 72, 3), (256, 256, 512),
-      (257, 130, 2050), (300, 520, 64), (512, 384, 1536), (1, 2048, 64), (48, 1408, 70), (33, 1000, 5000)]
+      (257, 130, 2050), (300, 520, 64), (512, 384, 1536), (1, 2048, 64), (48, 1408, 70), (33, 1000, 5000),
+      # several groups of stages, with whole and partial last ones, in tiles of every size
+      (70, 100, 4130), (130, 90, 6176), (1500, 1700, 2111), (3900, 3301, 4300), (3900, 3301, 416)]
 
 
 @pytest.mark.parametrize("out_dtype", DTYPES)
