@@ -80,7 +80,7 @@ def parse():
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=3)
-    ap.add_argument("--workload", default="large_n5",
+    ap.add_argument("--workload", default=None,
                     help="large_n5 (default), large_n10, dense800m, llama1p5b_gqa, moe_share, "
                          "fp32_128x512, kv_heads")
     ap.add_argument("--scaling", default="shape", choices=["shape", "hidden", "update_norm"],
@@ -91,10 +91,16 @@ def parse():
     ap.add_argument("--svd-entropy", action="store_true",
                     help="time the SVD-entropy diagnostic (section 3.4) over the workload's "
                          "Muon weight matrices instead of the optimizer step")
+    ap.add_argument("--distill", action="store_true",
+                    help="time a distillation step of the workload's LM head held in 4 bits instead "
+                         "of the optimizer step (default workload: dense800m)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-profile", action="store_true",
                     help="do not bracket launches with HIP events")
-    return ap.parse_args()
+    args = ap.parse_args()
+    if args.workload is None:
+        args.workload = "dense800m" if args.distill else "large_n5"
+    return args
 
 
 def cpu_model() -> str:
@@ -190,6 +196,85 @@ def measured_peaks():
 
 
 FP64_PEAK_TFLOPS = 78.6       # fp64 vector and matrix
+
+
+DISTILL_TOKENS, DISTILL_TOP = 4096, 64
+FP4_PEAK_TFLOPS = 256 * 4 * 4096 * 2.4e9 / 1e12    # 32x32x64 scaled MFMA: 4096 flop per SIMD and clock
+
+
+def distill_main(args, torch, mo_amd, W, wl, dev):
+    """One distillation step of the workload's LM head held in 4 bits: the
+    teacher's alternatives from its bf16 logits, 4-bit images of the head,
+    logits of the hidden states through them, the loss with its gradient,
+    the head's and the hidden states' gradients, and the head's AdamW step.
+    The roofline is that of the 4-bit products (three of tokens x vocabulary
+    x hidden)."""
+    heads = [v for v in wl.vecs if v.name == "lm_head"]
+    if not heads:
+        print(f"bench.py --distill needs a workload with an LM head, {wl.key} has none", file=sys.stderr)
+        sys.exit(2)
+    vocab, hidden = heads[0].shape
+    tokens, top = DISTILL_TOKENS, DISTILL_TOP
+    g = torch.Generator(device=dev).manual_seed(W.seed_of(wl.cid, 4, 1))
+    head = torch.randn(vocab, hidden, generator=g, device=dev) * wl.w_std
+    x = torch.randn(tokens, hidden, generator=g, device=dev).to(torch.bfloat16)
+    teacher = torch.empty(tokens, vocab, dtype=torch.bfloat16, device=dev)
+    for a in range(0, tokens, 512):                     # its logits: the head before rounding, and noise
+        z = x[a:a + 512].float() @ head.T
+        teacher[a:a + 512] = z + 0.1 * torch.randn(z.shape, generator=g, device=dev)
+    m, v = torch.zeros_like(head), torch.zeros_like(head)
+    scale = torch.full((tokens,), 1.0 / tokens, device=dev)
+    images, step_no = [None], [0]
+
+    def run():
+        step_no[0] += 1
+        t = mo_amd.token_logprobs(teacher, top=top)
+        images[0] = mo_amd.mx4_quantize(head, images="both", out=images[0])
+        w, w_t = images[0]
+        z, x_t = mo_amd.mx4_linear(x, w, save=True)
+        loss, dz = mo_amd.distill_loss(z, t.top_index, t.top_logprob, grad_loss=scale)
+        _, dw = mo_amd.mx4_linear_backward(dz, x_t, w_t)
+        mo_amd.adamw_step([head], [dw], [m], [v], lr=HYPER["lr"], wd=HYPER["wd"], step=step_no[0])
+        return loss
+
+    for _ in range(args.warmup):
+        run()
+    torch.cuda.synchronize()
+    classes = ["logprobs", "mx4_quant", "mx4_matmul", "distill", "adamw"]
+    mo_amd.profile_reset()
+    if not args.no_profile:
+        mo_amd.profile_enable(classes)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        loss = run()
+    torch.cuda.synchronize()
+    elapsed = time.perf_counter() - t0
+    mo_amd.profile_enable([])
+    prof = {c: mo_amd.profile_read(c) for c in classes}
+    ms_per_step = elapsed * 1e3 / args.steps
+    kernels = {}
+    for c in classes:
+        n, ms, work = prof[c]
+        if n:
+            unit = "TFLOP/s" if c == "mx4_matmul" else "GB/s"
+            rate = work / (ms * 1e-3) / (1e12 if unit == "TFLOP/s" else 1e9)
+            kernels[c] = {"launches": n, "mean_ms": ms / n, "rate": rate, "unit": unit,
+                          "frac": rate / (FP4_PEAK_TFLOPS if unit == "TFLOP/s" else HBM_PEAK_GBS)}
+    mm, roofline = prof["mx4_matmul"], None
+    if mm[0]:
+        ach = mm[2] / (mm[1] * 1e-3) / 1e12
+        roofline = {"bound": "mfma", "achieved": ach, "peak": FP4_PEAK_TFLOPS, "unit": "TFLOP/s",
+                    "frac": ach / FP4_PEAK_TFLOPS, "traffic": None, "kernel": "mx4_tile products of 4-bit images",
+                    "flops_per_launch": mm[2] / mm[0], "mean_launch_ms": mm[1] / mm[0]}
+    print(json.dumps({
+        "metric": "distillation steps/s of a 4-bit LM head", "value": 1e3 / ms_per_step, "unit": "steps/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms_per_step,
+        "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "mxfp4",
+        "data": "synthetic (seeded; random-init head, Gaussian hidden states)",
+        "config": {"workload": wl.key, "tokens": tokens, "vocab": vocab, "hidden": hidden, "alternatives": top},
+        "tokens_per_s": tokens * 1e3 / ms_per_step, "loss_mean": float(loss.mean()),
+        "kernels": kernels, "roofline": roofline}), flush=True)
 
 
 def svd_main(args, torch, mo_amd, W, wl, dev):
@@ -298,6 +383,9 @@ def main():
     mo_amd._lib.lib()
     if args.svd_entropy:
         svd_main(args, torch, mo_amd, W, wl, dev)
+        return
+    if args.distill:
+        distill_main(args, torch, mo_amd, W, wl, dev)
         return
 
     T = W.make_muon_tensors(wl, dev)

@@ -381,8 +381,8 @@ int mo_mx4_dequantize(const mo_mx4_image* images, void* const* dst, int64_t coun
  * accumulation) is rounded once to out_dtype (MO_F32 or MO_BF16).  out: rows
  * ldo elements apart (ldo >= N), aligned to its element; columns N .. ldo - 1
  * are left as they were.  out may not overlap an image.  Results do not
- * depend on the run (no atomics).  K <= 2^25, ceil(M / 64) ceil(N / 64) < 2^24
- * and N <= 2^26. */
+ * depend on the run (no atomics).  K <= 2^25 and ceil(M / 64) ceil(N / 64) <
+ * 2^24. */
 int mo_mx4_matmul(const mo_mx4_image* a, const mo_mx4_image* b, void* out, int out_dtype,
                   int64_t ldo, int accumulate, void* stream);
 

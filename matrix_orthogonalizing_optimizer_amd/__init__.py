@@ -727,6 +727,12 @@ class MuonAdamW:
 
     State lives in torch tensors owned here (momentum per Muon matrix; m, v
     per AdamW tensor), so checkpointing is saving ``state_dict()``.
+
+    ``mx4`` ("rows", "cols" or "both"): keep 4-bit images of the Muon
+    matrices in ``self.mx4`` (as :func:`mx4_quantize` gives them, in the
+    matrices' order), rewritten in place behind every step, so that 4-bit
+    layers always multiply the current weights.  ``refresh_mx4()`` makes them
+    before the first step, or after weights were loaded.
     """
 
     def __init__(self, muon_params: Sequence[torch.Tensor],
@@ -734,7 +740,9 @@ class MuonAdamW:
                  wd: float = 0.1, mu: float = 0.95, nesterov: bool = True,
                  ns_steps: int = 5, mom_dtype: torch.dtype = torch.bfloat16,
                  ns_dtype: torch.dtype = torch.bfloat16, betas=(0.9, 0.999),
-                 adam_eps: float = 1e-8):
+                 adam_eps: float = 1e-8, mx4: Optional[str] = None):
+        if mx4 is not None and mx4 not in _IMAGES:
+            raise ValueError(f"mx4 must be None or one of {_IMAGES}")
         self.muon_params: List[torch.Tensor] = list(muon_params)
         self.adamw_params: List[torch.Tensor] = list(adamw_params)
         for p in self.muon_params:
@@ -747,6 +755,15 @@ class MuonAdamW:
         self.t = 0
         self._plan: Optional[MuonPlan] = None
         self.plans_created = 0
+        self._mx4_images = mx4
+        self.mx4: Optional[list] = None
+
+    def refresh_mx4(self) -> list:
+        """Rewrite the 4-bit images from the matrices as they are now."""
+        if self._mx4_images is None:
+            raise RuntimeError('MuonAdamW was made without mx4="rows", "cols" or "both"')
+        self.mx4 = mx4_quantize([p.detach() for p in self.muon_params], images=self._mx4_images, out=self.mx4)
+        return self.mx4
 
     def _grads(self, ps):
         gs = [p.grad for p in ps]
@@ -780,6 +797,8 @@ class MuonAdamW:
             self._plan.step(lr=lr, wd=self.wd, mu=self.mu, nesterov=self.nesterov,
                             ns_steps=self.ns_steps, update_rms=update_rms)
             self._plan.release_grads()
+            if self._mx4_images is not None:
+                self.refresh_mx4()
         if self.adamw_params:
             adamw_step(self.adamw_params, self._grads(self.adamw_params), self.exp_avg,
                        self.exp_avg_sq, lr=lr, step=self.t, wd=self.wd, beta1=self.betas[0],

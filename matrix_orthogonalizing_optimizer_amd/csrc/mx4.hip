@@ -1,6 +1,9 @@
 // MX4: quantisation to microscaled 4-bit images, reading back, and the
 // product of two images on the matrix cores (gfx950).  Layout and rounding
 // are those of include/muon.h.
+#include <algorithm>
+#include <cmath>
+
 #include "mo_internal.h"
 #include "mx4_internal.h"
 #include "ns_common.h"
@@ -601,65 +604,65 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
   const uint8_t *pa = uniform_ptr(a0 + tp * 64), *pb = uniform_ptr(b0 + tp * 64);
   uint32_t backp = tp == stages - 1 ? back_last : 0u;
   for (int g = 0; g <= last_group; ++g) {
-  // the next group's scales, into the place of the group before this one:
-  // its last dwords were read two barriers ago
-  if (g < last_group) request_scales(g + 1);
-  const int end = min(16 * g + 16, stages);
-  for (int t = 16 * g; t < end; ++t) {
-    uint32_t next = 0, keep = 0, sat = 0;
-    unroll<2>([&](auto S) __attribute__((always_inline)) {
-      constexpr int s = S, cur = s, nxt = cur ^ 1;
-      if constexpr (s == 1) {
-        // this wave's reads of stage t are done, its part of t + 1 has come
-        wait_loads<(NST - 2) * DPW>();
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      constexpr int RP = (2 * NR + NP - 1) / NP;
-      // A product at a time, and behind each a little of everything else: a
-      // wave issues a handful of instructions while its product runs.
-      unroll<NP>([&](auto P) __attribute__((always_inline)) {
-        constexpr int i = P / FN, j = P % FN;
-        acc[i][j] = mfma32<s>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
-        unroll<RP>([&](auto R) __attribute__((always_inline)) {
-          constexpr int r = P * RP + R;                 // order of need: A's first, all of B, the rest of A
-          constexpr int fa = r == 0 ? 0 : r > FN && r < NR ? r - FN : -1, fb = r >= 1 && r <= FN ? r - 1 : -1;
-          if constexpr (fa >= 0) {
-            af[nxt][fa] = frag(abase, s == 1 ? next : at, fa, nxt);
-            if constexpr (s == 1) san[fa] = scale(asbase, sat, fa);
-          }
-          if constexpr (fb >= 0) {
-            bf[nxt][fb] = frag(bbase, s == 1 ? next : at, fb, nxt);
-            if constexpr (s == 1) sbn[fb] = scale(bsbase, sat, fb);
-          }
-        });
-        if constexpr (s == 1 && P == 0) {
-          // past the end: the last stage again, unused
-          const bool more = tp + 1 < stages;
-          tp += more;
-          pa = uniform_ptr(pa + (more ? 64 : 0));
-          pb = uniform_ptr(pb + (more ? 64 : 0));
-          backp = tp == stages - 1 ? back_last : 0u;
-          prev = at;
+    // the next group's scales, into the place of the group before this one,
+    // whose last dwords every wave had read by the last barrier
+    if (g < last_group) request_scales(g + 1);
+    const int end = min(16 * g + 16, stages);
+    for (int t = 16 * g; t < end; ++t) {
+      uint32_t next = 0, keep = 0, sat = 0;
+      unroll<2>([&](auto S) __attribute__((always_inline)) {
+        constexpr int s = S, cur = s, nxt = cur ^ 1;
+        if constexpr (s == 1) {
+          // this wave's reads of stage t are done, its part of t + 1 has come
+          wait_loads<(NST - 2) * DPW>();
+          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
         }
-        unroll<DPW>([&](auto C) __attribute__((always_inline)) {
-          if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, pa, pb, backp, prev);
+        constexpr int RP = (2 * NR + NP - 1) / NP;
+        // A product at a time, and behind each a little of everything else: a
+        // wave issues a handful of instructions while its product runs.
+        unroll<NP>([&](auto P) __attribute__((always_inline)) {
+          constexpr int i = P / FN, j = P % FN;
+          acc[i][j] = mfma32<s>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+          unroll<RP>([&](auto R) __attribute__((always_inline)) {
+            constexpr int r = P * RP + R;                 // order of need: A's first, all of B, the rest of A
+            constexpr int fa = r == 0 ? 0 : r > FN && r < NR ? r - FN : -1, fb = r >= 1 && r <= FN ? r - 1 : -1;
+            if constexpr (fa >= 0) {
+              af[nxt][fa] = frag(abase, s == 1 ? next : at, fa, nxt);
+              if constexpr (s == 1) san[fa] = scale(asbase, sat, fa);
+            }
+            if constexpr (fb >= 0) {
+              bf[nxt][fb] = frag(bbase, s == 1 ? next : at, fb, nxt);
+              if constexpr (s == 1) sbn[fb] = scale(bsbase, sat, fb);
+            }
+          });
+          if constexpr (s == 1 && P == 0) {
+            // past the end: the last stage again, unused
+            const bool more = tp + 1 < stages;
+            tp += more;
+            pa = uniform_ptr(pa + (more ? 64 : 0));
+            pb = uniform_ptr(pb + (more ? 64 : 0));
+            backp = tp == stages - 1 ? back_last : 0u;
+            prev = at;
+          }
+          unroll<DPW>([&](auto C) __attribute__((always_inline)) {
+            if constexpr (when(C) == P + (s == 1 ? 0 : NP)) request(C, pa, pb, backp, prev);
+          });
+          if constexpr (s == 0 && P == NP - 1 - (NP > 4)) {
+            next = at + kStage == NST * kStage ? 0u : at + kStage;
+            keep = keep_of(t + 1);
+            sat = scale_at(t + 1);                       // (past the end: a place that holds something)
+          }
+          __builtin_amdgcn_sched_barrier(0);
         });
-        if constexpr (s == 0 && P == NP - 1 - (NP > 4)) {
-          next = at + kStage == NST * kStage ? 0u : at + kStage;
-          keep = keep_of(t + 1);
-          sat = scale_at(t + 1);                       // (past the end: a place that holds something)
-        }
-        __builtin_amdgcn_sched_barrier(0);
       });
-    });
 #pragma unroll
-    for (int f = 0; f < FM; ++f) sa[f] = (san[f] & keep) >> (16 * half);
+      for (int f = 0; f < FM; ++f) sa[f] = (san[f] & keep) >> (16 * half);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sb[f] = (sbn[f] & keep) >> (16 * half);
-    at = next;
-  }
+      for (int f = 0; f < FN; ++f) sb[f] = (sbn[f] & keep) >> (16 * half);
+      at = next;
+    }
   }
   wait_loads<0>();                                     // no request outlives the workgroup
 
@@ -837,9 +840,7 @@ __global__ void __launch_bounds__(1024) mx4_skinny_kernel(const Mx4MatmulArgs p)
 }
 
 // A grid holds fewer than 2^32 threads, whichever kernel is taken.
-bool mx4_matmul_fits(int64_t m, int64_t n) {
-  return ((m + 63) / 64) * ((n + 63) / 64) <= int64_t{0xffffffff} / 256 && (n + 15) / 16 <= int64_t{0xffffffff} / 1024;
-}
+bool mx4_matmul_fits(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) / 64) <= int64_t{0xffffffff} / 256; }
 
 template <int TM, int TN, int WM, int WN, int NST>
 static hipError_t run_tile(int out_dt, Mx4MatmulArgs a, hipStream_t s) {
@@ -869,22 +870,32 @@ static hipError_t run_skinny(int out_dt, const Mx4MatmulArgs& a, int waves, hipS
   return hipGetLastError();
 }
 
+// Which kernel.  Measured on products of K = 8192 (and, at a quarter to a third
+// of these times, K = 2048), in us:
+//  * skinny against 64 tiles: 1 x 2048 5 and 19, 32 x 8192 17 and 19, 8 x 28672
+//    31 and 28, 16 x 28672 35 and 29, 32 x 28672 50 and 29: up to 32 rows while
+//    each row of A is not read again by too many workgroups;
+//  * 64 tiles: 19 for up to 256 of them, 24 for 512, then in proportion;
+//  * 128 tiles: 29 for up to 256, 52 for 512, 81 for 768, 112 for 1024;
+//  * 256 tiles: 58 for 128 of them, 76 for 256, 162 for 512: whole rounds, as a
+//    CU holds one at a time.
 hipError_t launch_mx4_matmul(int out_dt, const Mx4MatmulArgs& a, hipStream_t s) {
-  if (a.m <= 64) {
+  const int64_t m = a.m, n = a.n;
+  if (m <= 32 && m * n <= (1 << 18)) {
     // waves per workgroup: enough for about 16 on every CU, none without a
     // group of 16 blocks of its own
-    const int64_t wgs = (a.n + 15) / 16, groups = (a.nb + 15) / 16;
+    const int64_t wgs = (n + 15) / 16, groups = (a.nb + 15) / 16;
     int waves = 1;
     while (waves < 16 && waves * 2 <= groups && wgs * waves < 4096) waves *= 2;
-    if (a.m <= 16) return run_skinny<1>(out_dt, a, waves, s);
-    if (a.m <= 32) return run_skinny<2>(out_dt, a, min(waves, 8), s);
-    return run_skinny<4>(out_dt, a, min(waves, 8), s);
+    return m <= 16 ? run_skinny<1>(out_dt, a, waves, s) : run_skinny<2>(out_dt, a, waves, s);
   }
   if (a.nb <= 12) return run_direct(out_dt, a, s);
-  const int64_t t256 = ((a.m + 255) / 256) * static_cast<int64_t>((a.n + 255) / 256);
-  const int64_t t128 = ((a.m + 127) / 128) * static_cast<int64_t>((a.n + 127) / 128);
-  if (t256 >= 192) return run_tile<256, 256, 2, 2, 3>(out_dt, a, s);
-  if (t128 >= 192) return run_tile<128, 128, 2, 2, 3>(out_dt, a, s);
+  auto tiles = [&](int64_t t) { return static_cast<double>((m + t - 1) / t) * static_cast<double>((n + t - 1) / t); };
+  const double t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
+  const double c64 = std::max(19.0, 24.0 * t64 / 512), c128 = std::max(29.0, 26.0 * t128 / 256);
+  const double c256 = t256 <= 128 ? 58.0 : 76.0 * std::ceil(t256 / 256);
+  if (c256 <= c128 && c256 <= c64) return run_tile<256, 256, 2, 2, 3>(out_dt, a, s);
+  if (c128 <= c64) return run_tile<128, 128, 2, 2, 3>(out_dt, a, s);
   return run_tile<64, 64, 2, 2, 3>(out_dt, a, s);
 }
 

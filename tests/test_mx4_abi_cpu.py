@@ -228,3 +228,18 @@ def test_front_checks_tokens():
         mo.token_logprobs(torch.zeros(4, 64), torch.zeros(3, dtype=torch.int64))
     with pytest.raises(mo.MuonError, match="top"):
         mo.token_logprobs(torch.zeros(4, 64), top=200)
+
+
+def test_optimizer_refuses_unknown_images():
+    with pytest.raises(ValueError, match="mx4"):
+        mo.MuonAdamW([torch.zeros(4, 4)], mx4="all")
+    with pytest.raises(RuntimeError, match="without mx4"):
+        mo.MuonAdamW([torch.zeros(4, 4)]).refresh_mx4()
+
+
+def test_product_refuses_too_many_tiles_and_too_long_rows():
+    a, b = _image(rows=1 << 18, cols=32), _image(rows=1 << 18, cols=32, at=BASE << 8)
+    assert _matmul(a, b, out=BASE << 12, ldo=1 << 18) == L.MO_EINVAL and "tiles" in L.last_error()
+    a, b = _image(rows=2, cols=(1 << 25) + 1), _image(rows=2, cols=(1 << 25) + 1, at=BASE << 8)
+    a.scales, b.scales = BASE << 4, BASE << 9
+    assert _matmul(a, b, out=BASE << 12, ldo=2) == L.MO_EINVAL and "2^25" in L.last_error()

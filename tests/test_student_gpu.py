@@ -132,3 +132,30 @@ def test_other_streams_and_long_rows():
         for a, b in zip(alone, got):
             for u, v in zip([*a[0][1:], *a[1], a[2]], [*b[0][1:], *b[1], b[2]]):
                 assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("images", ["rows", "cols", "both"])
+def test_optimizer_keeps_images_of_its_matrices(images):
+    """The images behind a step are those of the weights it wrote, in the
+    tensors that held the ones before."""
+    gen = torch.Generator().manual_seed(5)
+    shapes = [(96, 200), (200, 96), (64, 64)]
+    ps = [(torch.randn(s, generator=gen) * 0.02).cuda() for s in shapes]
+    plain = [p.clone() for p in ps]
+    opt = mo.MuonAdamW(ps, lr=1e-2, mx4=images)
+    other = mo.MuonAdamW(plain, lr=1e-2)
+    first = opt.refresh_mx4()
+    for step in range(3):
+        for p, q in zip(ps, plain):
+            p.grad = torch.randn(p.shape, generator=gen).cuda()
+            q.grad = p.grad.clone()
+        opt.step()
+        other.step()
+        want = mo.mx4_quantize(ps, images=images)
+        for p, q, a, b, f in zip(ps, plain, opt.mx4, want, first):
+            assert torch.equal(p, q)                 # the step itself is as it was
+            for x, y, z in zip(*[t if images == "both" else (t,) for t in (a, b, f)]):
+                assert x is z
+                assert torch.equal(x.codes, y.codes) and torch.equal(x.scales, y.scales)
+    with pytest.raises(RuntimeError, match="without mx4"):
+        other.refresh_mx4()
