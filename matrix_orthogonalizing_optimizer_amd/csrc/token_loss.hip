@@ -185,7 +185,8 @@ struct RowRegs {
 constexpr int kCand = 512;
 template <int NT>
 struct TopLds {
-  u64 cand[kCand], keys[kMaxTop];
+  __attribute__((aligned(16))) u64 cand[kCand];
+  u64 keys[kMaxTop];
   uint32_t upper[NT];
   int count;
   uint32_t bound;
@@ -219,10 +220,15 @@ __device__ __forceinline__ float top_bound(uint32_t mine, int n, TopLds<NT>& l) 
 
 template <int NT>
 __device__ __forceinline__ void rank_sort(int count, int n, TopLds<NT>& l) {
+  // four keys at a time, the last ones filled up with the lowest
+  if (threadIdx.x < 4 && count + threadIdx.x < kCand) l.cand[count + threadIdx.x] = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < count; i += NT) {
     const u64 k = l.cand[i];
     int rank = 0;
-    for (int j = 0; j < count; ++j) rank += l.cand[j] > k;
+    for (int j = 0; j < count; j += 4)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) rank += l.cand[j + q] > k;
     if (rank < n) l.keys[rank] = k;
   }
   __syncthreads();
@@ -539,8 +545,10 @@ Cut cut(int64_t rows, int64_t vocab, int esz, int64_t whole) {
   const int64_t bytes = vocab * esz;
   int64_t piece = bytes;
   if (bytes > whole) piece = rows * bytes < 256 * kLargePiece ? kSmallPiece : kLargePiece;
-  const int64_t len = piece / esz, n = (vocab + len - 1) / len;
-  return {static_cast<int>(n), static_cast<int>(len)};
+  const int64_t n = (bytes + piece - 1) / piece;
+  int64_t len = (vocab + n - 1) / n;                   // pieces of about equal length, in whole vectors
+  if (n > 1) len = (len + 7) / 8 * 8;
+  return {static_cast<int>((vocab + len - 1) / len), static_cast<int>(len)};
 }
 
 constexpr int64_t kLogprobsWhole = 64 << 10, kDistillWhole = 320 << 10;
