@@ -126,6 +126,10 @@ struct RowRegs {
       const int e = at(v);
       if (e + N <= n) {
         x[v] = *reinterpret_cast<const typename Row<T>::vec*>(p + e);
+      } else if (e < n && n >= N) {
+        // the row's last vector, of which the first elements belong to the one
+        // before: shifted out, with -inf behind
+        x[v] = tail(*reinterpret_cast<const typename Row<T>::vec*>(p + n - N), n - e);
       } else {
         x[v] = Row<T>::fill();
 #pragma unroll
@@ -133,6 +137,19 @@ struct RowRegs {
           if (e + j < n) Row<T>::put(x[v], j, static_cast<float>(p[e + j]));
       }
     }
+  }
+  // the last k elements of w in front, -inf behind them (0 < k < N)
+  static __device__ __forceinline__ typename Row<T>::reg tail(typename Row<T>::reg w, int k) {
+    typedef u64 u64x2 __attribute__((ext_vector_type(2)));
+    const u64x2 a = __builtin_bit_cast(u64x2, w), f = __builtin_bit_cast(u64x2, Row<T>::fill());
+    const int keep = k * static_cast<int>(sizeof(T)) * 8, out = 128 - keep;
+    u64x2 r;
+    r[0] = out >= 64 ? a[1] >> (out - 64) : (a[0] >> out) | (a[1] << (64 - out));
+    r[1] = out >= 64 ? 0 : a[1] >> out;
+    const u64 m0 = keep >= 64 ? ~u64{0} : (u64{1} << keep) - 1, m1 = keep > 64 ? (u64{1} << (keep - 64)) - 1 : 0;
+    r[0] = (r[0] & m0) | (f[0] & ~m0);
+    r[1] = (r[1] & m1) | (f[1] & ~m1);
+    return __builtin_bit_cast(typename Row<T>::reg, r);
   }
   // Makes the compiler unpack the elements again rather than keep what an
   // earlier pass unpacked (twice the registers, half the rows in flight).
