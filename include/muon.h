@@ -392,7 +392,7 @@ int mo_mx4_matmul(const mo_mx4_image* a, const mo_mx4_image* b, void* out, int o
  * logits [rows, vocab] (MO_F32 or MO_BF16), rows `ld` elements apart
  * (ld >= vocab), aligned to the element; columns vocab .. ld - 1 are never
  * read.  1 <= vocab < 2^31, 0 <= rows < 2^22.  z = logits / temperature with
- * a finite temperature > 0.  Statistics are fp32, and their sums run in a
+ * a temperature in [2^-126, 2^63].  Statistics are fp32, and their sums run in a
  * fixed order: results do not depend on the run.
  * ---------------------------------------------------------------------- */
 #define MO_MAX_TOP 128

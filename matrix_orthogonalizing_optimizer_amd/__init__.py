@@ -21,6 +21,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import threading
 from typing import Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
@@ -425,6 +426,11 @@ def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, shape: Tuple[int, ...
     return t.data_ptr()
 
 
+# Two threads on one stream share its cached workspace: a call's launches must
+# not mix with another's (the binding releases the interpreter lock).
+_SCRATCH_LOCK = threading.Lock()
+
+
 @functools.lru_cache(maxsize=1024)
 def _token_workspace(query: str, rows: int, vocab: int, top: int) -> int:
     need = ctypes.c_size_t()
@@ -650,12 +656,13 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
         tlp = torch.empty(rows, top, dtype=torch.float32, device=dev)
         tix = torch.empty(rows, top, dtype=torch.int64, device=dev)
         if rows:
-            ws = _scratch(need, handle, dev)
-            check(lib().mo_token_logprobs(ptr, dt, rows, vocab, ld, tok, temperature,
-                                          lp.data_ptr() if lp is not None else None, ent.data_ptr(), top,
-                                          tix.data_ptr() if top else None, tlp.data_ptr() if top else None,
-                                          ws.data_ptr() if ws is not None else None,
-                                          ws.numel() if ws is not None else 0, handle))
+            with _SCRATCH_LOCK:
+                ws = _scratch(need, handle, dev)
+                check(lib().mo_token_logprobs(ptr, dt, rows, vocab, ld, tok, temperature,
+                                              lp.data_ptr() if lp is not None else None, ent.data_ptr(), top,
+                                              tix.data_ptr() if top else None, tlp.data_ptr() if top else None,
+                                              ws.data_ptr() if ws is not None else None,
+                                              ws.numel() if ws is not None else 0, handle))
     return TokenLogprobs(lp, ent, tlp, tix)
 
 
@@ -693,10 +700,11 @@ def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_logit: torch
             g = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
         gp, _, _, ldg = _rows_of(g, "out_grad") if grad else (None, 0, 0, 0)
         if rows:
-            ws = _scratch(need, handle, dev)
-            check(lib().mo_distill_loss(ptr, dt, rows, vocab, ld, ti, tl, k, temperature, gl, loss.data_ptr(),
-                                        gp, ldg, ws.data_ptr() if ws is not None else None,
-                                        ws.numel() if ws is not None else 0, handle))
+            with _SCRATCH_LOCK:
+                ws = _scratch(need, handle, dev)
+                check(lib().mo_distill_loss(ptr, dt, rows, vocab, ld, ti, tl, k, temperature, gl,
+                                            loss.data_ptr(), gp, ldg, ws.data_ptr() if ws is not None else None,
+                                            ws.numel() if ws is not None else 0, handle))
     return loss, g
 
 

@@ -3,7 +3,6 @@
 #include <hip/hip_runtime.h>
 
 #include <climits>
-#include <cmath>
 #include <cstdint>
 
 #include "mo_host.h"
@@ -27,6 +26,12 @@ int check_sizes(int64_t rows, int64_t vocab, int top, int top_min) {
   if (vocab < 1 || vocab > INT32_MAX) return fail(MO_EINVAL, "vocab must be in [1, 2^31)");
   if (!token_grid_fits(rows, vocab)) return fail(MO_EINVAL, "rows times vocab is too large for one launch");
   if (top < top_min || top > MO_MAX_TOP) return fail(MO_EINVAL, "top must be in [%d, %d] (got %d)", top_min, MO_MAX_TOP, top);
+  return MO_OK;
+}
+
+// 1 / temperature times log2(e), and temperature squared, stay finite.
+int check_temperature(float t) {
+  if (!(t >= 0x1p-126f && t <= 0x1p63f)) return fail(MO_EINVAL, "temperature must be in [2^-126, 2^63]");
   return MO_OK;
 }
 
@@ -84,8 +89,7 @@ int mo_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab
   if ((rc = validate_dtype(dtype, "dtype"))) return rc;
   if ((rc = check_sizes(rows, vocab, top, 0))) return rc;
   if (top > vocab) return fail(MO_EINVAL, "top = %d exceeds vocab = %lld", top, static_cast<long long>(vocab));
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-    return fail(MO_EINVAL, "temperature must be finite and > 0");
+  if ((rc = check_temperature(temperature))) return rc;
   if (!tokens != !logprob) return fail(MO_EINVAL, "tokens and logprob: both or neither");
   if ((top > 0) != (top_index != nullptr) || (top > 0) != (top_logprob != nullptr))
     return fail(MO_EINVAL, "top_index and top_logprob must be given iff top > 0");
@@ -128,8 +132,7 @@ int mo_distill_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, 
   int rc;
   if ((rc = validate_dtype(dtype, "dtype"))) return rc;
   if ((rc = check_sizes(rows, vocab, top, 1))) return rc;
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-    return fail(MO_EINVAL, "temperature must be finite and > 0");
+  if ((rc = check_temperature(temperature))) return rc;
   if (rows == 0) return MO_OK;
   if (!loss && !grad) return fail(MO_EINVAL, "loss and grad are both NULL");
   if (!top_index || !top_logit) return fail(MO_EINVAL, "top_index and top_logit must be non-NULL");

@@ -114,7 +114,7 @@ _LP = dict(logits=BASE, dtype=L.MO_BF16, rows=8, vocab=100, ld=100, tokens=BASE 
     (dict(dtype=3), "dtype"), (dict(rows=-1), "rows"), (dict(rows=1 << 22), "rows"), (dict(vocab=0), "vocab"),
     (dict(vocab=1 << 31), "vocab"), (dict(ld=99), "stride"), (dict(logits=None), "logits"),
     (dict(logits=BASE + 1), "aligned"), (dict(tau=0.0), "temperature"), (dict(tau=-1.0), "temperature"),
-    (dict(tau=float("nan")), "temperature"), (dict(tau=float("inf")), "temperature"), (dict(tau=1e-39), "temperature"),
+    (dict(tau=float("nan")), "temperature"), (dict(tau=float("inf")), "temperature"), (dict(tau=1e-39), "temperature"), (dict(tau=1e20), "temperature"),
     (dict(tokens=None), "both"), (dict(logprob=None), "both"), (dict(top=-1), "top"), (dict(top=129), "top"),
     (dict(top=101, vocab=100), "exceeds"), (dict(top=0), "iff"), (dict(top_index=None), "iff"),
     (dict(top_index=BASE + 0x40004), "aligned"), (dict(entropy=BASE + 0x20004), "overlap"),

@@ -159,3 +159,51 @@ def test_optimizer_keeps_images_of_its_matrices(images):
                 assert torch.equal(x.codes, y.codes) and torch.equal(x.scales, y.scales)
     with pytest.raises(RuntimeError, match="without mx4"):
         other.refresh_mx4()
+
+
+def test_two_threads_on_one_stream():
+    """Calls with a workspace from two threads of one stream, over and over:
+    each gives what it gives alone."""
+    import threading
+    gen = torch.Generator().manual_seed(6)
+    zs = [torch.randn(2, 90001, generator=gen).cuda() for _ in range(2)]
+    idx = torch.randint(0, 90001, (2, 8), generator=gen).cuda()
+    val = torch.randn(2, 8, generator=gen).cuda()
+    alone = [(mo.token_logprobs(z, top=9), mo.distill_loss(z, idx, val)) for z in zs]
+    got = [[], []]
+
+    def work(i):
+        for _ in range(20):
+            got[i].append((mo.token_logprobs(zs[i], top=9), mo.distill_loss(zs[i], idx, val)))
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for a, b in got[i]:
+            assert torch.equal(a.top_logprob, alone[i][0].top_logprob) and torch.equal(a.entropy, alone[i][0].entropy)
+            assert torch.equal(b[0], alone[i][1][0]) and torch.equal(b[1], alone[i][1][1])
+
+
+def test_small_and_large_temperatures():
+    """Temperatures that make the softmax one-hot or flat."""
+    z = torch.randn(3, 5000, generator=torch.Generator().manual_seed(7)).cuda()
+    idx = torch.tensor([[1, 2], [3, 4], [5, 6]]).cuda()
+    val = torch.tensor([[1.0, 0.5]] * 3).cuda()
+    r = mo.token_logprobs(z, top=3, temperature=1e-30)
+    best = z.argmax(1)
+    assert torch.equal(r.top_index[:, 0], best)
+    assert bool((r.entropy == 0).all()) and bool((r.top_logprob[:, 0] == 0).all())
+    loss, g = mo.distill_loss(z, best[:, None].contiguous(), val[:, :1].contiguous(), temperature=1e-30)
+    assert bool((loss == 0).all()) and bool((g == 0).all())
+    r = mo.token_logprobs(z, top=3, temperature=1e18)
+    flat = float(np.log(5000.0))
+    assert bool(((r.entropy - flat).abs() <= 2.0 ** -24 * 60 * flat).all())
+    loss, g = mo.distill_loss(z, idx, val, temperature=1e6)
+    want = od.distill(_f64(z), _f64(idx).astype(np.int64), _f64(val), 1e6)[1]
+    # g = tau (q - p): q and p are off by about 60 roundings
+    assert np.max(np.abs(_f64(g) - want)) <= 1e6 * 60 * 2.0 ** -24
