@@ -84,22 +84,23 @@ def _shape2(t: torch.Tensor) -> Tuple[int, int]:
 _WS: dict = {}
 
 
-def _workspace(device: torch.device, nbytes: int, stream_handle: int) -> torch.Tensor:
+def _workspace(device: torch.device, nbytes: int, stream_handle: int, cache: Optional[dict] = None) -> torch.Tensor:
     """A cached byte buffer of at least ``nbytes`` for one (device, stream).
     Calls queued on different streams never share it, and it is allocated on
     that stream, so torch's allocator orders any reuse of its memory after
     the work queued there."""
+    cache = _WS if cache is None else cache
     key = (device.type, device.index, int(stream_handle or 0))
-    ws = _WS.get(key)
+    ws = cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        _WS.pop(key, None)
+        cache.pop(key, None)
         n = max(nbytes, 256)
         if stream_handle and stream_handle != torch.cuda.current_stream(device).cuda_stream:
             with torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=device)):
                 ws = torch.empty(n, dtype=torch.uint8, device=device)
         else:
             ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _WS[key] = ws
+        cache[key] = ws
     return ws
 
 
@@ -427,7 +428,9 @@ def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, shape: Tuple[int, ...
 
 
 # Two threads on one stream share its cached workspace: a call's launches must
-# not mix with another's (the binding releases the interpreter lock).
+# not mix with another's (the binding releases the interpreter lock). Optimizer
+# steps have workspaces of their own.
+_TOKEN_WS: dict = {}
 _SCRATCH_LOCK = threading.Lock()
 
 
@@ -445,7 +448,7 @@ def _scratch(nbytes: int, handle: int, device: torch.device) -> Optional[torch.T
         return None
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return _workspace(device, nbytes, handle)
+    return _workspace(device, nbytes, handle, _TOKEN_WS)
 
 
 class Mx4Matrix:
@@ -600,7 +603,7 @@ def mx4_linear(x: torch.Tensor, w: Mx4Matrix, *, out_dtype: torch.dtype = torch.
                save: bool = False, stream=None):
     """``y = x W^T`` with W [N, K] held in 4 bits and x [..., K] (fp32 or
     bf16) quantised on the way.  ``save=True`` also returns the image of x^T
-    that :func:`mx4_linear_backward` takes."""
+    that :func:`mx4_linear_backward` takes (and needs one token at least)."""
     x2 = _flat2(x)
     if x2.shape[1] != w.cols:
         raise ValueError(f"x has {x2.shape[1]} features, the weights {w.cols}")
@@ -754,7 +757,8 @@ class MuonAdamW:
         self.muon_params: List[torch.Tensor] = list(muon_params)
         self.adamw_params: List[torch.Tensor] = list(adamw_params)
         for p in self.muon_params:
-            _shape2(p)
+            if 0 in _shape2(p) and mx4 is not None:
+                raise ValueError(f"an image has at least one row and one column, got {list(p.shape)}")
         self.lr, self.wd, self.mu, self.nesterov = lr, wd, mu, nesterov
         self.ns_steps, self.ns_dtype, self.betas, self.adam_eps = ns_steps, ns_dtype, betas, adam_eps
         self.momentum = [torch.zeros_like(p, dtype=mom_dtype) for p in self.muon_params]

@@ -243,3 +243,11 @@ def test_product_refuses_too_many_tiles_and_too_long_rows():
     a, b = _image(rows=2, cols=(1 << 25) + 1), _image(rows=2, cols=(1 << 25) + 1, at=BASE << 8)
     a.scales, b.scales = BASE << 4, BASE << 9
     assert _matmul(a, b, out=BASE << 12, ldo=2) == L.MO_EINVAL and "2^25" in L.last_error()
+
+
+def test_images_of_empty_matrices_are_refused():
+    import torch
+    import matrix_orthogonalizing_optimizer_amd as mo
+    with pytest.raises(ValueError, match="at least one row"):
+        mo.MuonAdamW([torch.empty(0, 8)], mx4="rows")
+    mo.MuonAdamW([torch.empty(0, 8)])
