@@ -147,7 +147,7 @@ int dequant_group(const mo_mx4_image* images, void* const* dst, int64_t count, i
     double bytes = 0;
     while (i < count && a.count < G) {
       const mo_mx4_image& x = images[i];
-      const int64_t t = mx4_dequant_tiles(x.rows, x.cols);
+      const int64_t t = mx4_dequant_tiles(dtype, x.rows, x.cols);
       if (a.count && tiles + t > kMaxTiles) break;
       a.item[a.count++] = {static_cast<const uint8_t*>(x.codes), static_cast<const uint8_t*>(x.scales), dst[i],
                            static_cast<int32_t>(x.rows), static_cast<int32_t>(x.cols), tiles};
@@ -173,7 +173,7 @@ int dequantize(const mo_mx4_image* images, void* const* dst, int64_t count, int 
     const mo_mx4_image& x = images[i];
     if ((rc = check_image(x, "image", i))) return rc;
     if (!dst[i] || !aligned16(dst[i])) return fail(MO_EINVAL, "image %lld: dst must be non-NULL and 16-byte aligned", ll(i));
-    if (mx4_dequant_tiles(x.rows, x.cols) > kMaxTiles) return fail(MO_EINVAL, "image %lld: too large for one launch", ll(i));
+    if (mx4_dequant_tiles(dtype, x.rows, x.cols) > kMaxTiles) return fail(MO_EINVAL, "image %lld: too large for one launch", ll(i));
     add_range(ranges, x.codes, code_bytes(x.rows, x.cols), i, false);
     add_range(ranges, x.scales, scale_bytes(x.rows, x.cols), i, false);
     add_range(ranges, dst[i], view_bytes(x.rows, x.cols, x.cols, esz), i, true);

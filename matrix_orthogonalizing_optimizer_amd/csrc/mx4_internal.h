@@ -55,7 +55,7 @@ constexpr int64_t kMx4MaxCols = int64_t{1} << 25;
 bool mx4_matmul_fits(int64_t m, int64_t n);
 
 int64_t mx4_quant_tiles(int64_t rows, int64_t cols, bool cols_image);
-int64_t mx4_dequant_tiles(int64_t rows, int64_t cols);
+int64_t mx4_dequant_tiles(int dt, int64_t rows, int64_t cols);
 template <int G>
 hipError_t launch_mx4_quant(int dt, bool cols_image, const Mx4QuantArgs<G>& a, int64_t tiles, hipStream_t s);
 template <int G>
