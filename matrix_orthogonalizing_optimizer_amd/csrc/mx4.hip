@@ -719,20 +719,26 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
 }
 
 // Direct kernel, for contractions of at most 12 blocks (whose rows of scale
-// bytes are shorter than the tile kernel's requests): one wave per 32 x 32
-// outputs (2 x 2 tiles of 16 x 16), four waves per workgroup, no LDS.  The
-// scaled 16 x 16 x 128 instruction takes from lane l the 32 codes and the scale
-// byte of row l % 16, block l / 16 of a step.
+// bytes are shorter than the tile kernel's requests): 4 x 4 tiles of 16 x 16
+// outputs per wave, 2 x 2 waves per workgroup, no LDS.  The scaled 16 x 16 x
+// 128 instruction takes from lane l the 32 codes and the scale byte of row l %
+// 16, block l / 16 of a step; the operands are given in reverse, so that a lane
+// ends with four consecutive outputs of a row.  Bound by its stores and by the
+// rows that each request of codes and scale bytes looks up: 8192 x 8192 x 128
+// 45 us, x 384 72 us (2 x 2 tiles: 51 and 107; nothing either way up to 1024 x
+// 1024).
+constexpr int kDirectTiles = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_direct_kernel(const Mx4MatmulArgs p) {
+  constexpr int F = kDirectTiles, kWave = 16 * F, kTile = 2 * kWave;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t tn = (static_cast<uint32_t>(p.n) + 63u) / 64u;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / tn) * 64 + (wave >> 1) * 32;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x % tn) * 64 + (wave & 1) * 32;
+  const uint32_t tn = (static_cast<uint32_t>(p.n) + kTile - 1u) / kTile;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / tn) * kTile + (wave >> 1) * kWave;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x % tn) * kTile + (wave & 1) * kWave;
   const int r16 = lane & 15, kb = lane >> 4;
-  const uint8_t *ac[2], *as[2], *bc[2], *bs[2];
+  const uint8_t *ac[F], *as[F], *bc[F], *bs[F];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < F; ++i) {
     // rows past the end read the last row; their products are not stored
     const int64_t ar = min(m0 + 16 * i + r16, static_cast<int64_t>(p.m) - 1);
     const int64_t br = min(n0 + 16 * i + r16, static_cast<int64_t>(p.n) - 1);
@@ -741,46 +747,34 @@ __global__ void __launch_bounds__(256) mx4_direct_kernel(const Mx4MatmulArgs p) 
     bc[i] = p.b + br * p.nb * 16;
     bs[i] = p.sb + br * p.sp;
   }
-  f32x4v acc[2][2] = {};
+  f32x4v acc[F][F] = {};
   for (int k = 0; k < p.nb; k += 4) {
     const int b = k + kb;
-    i32x8v av[2] = {}, bv[2] = {};
-    int asv[2] = {}, bsv[2] = {};
+    u32x4v av[F] = {}, bv[F] = {};
+    int asv[F] = {}, bsv[F] = {};
     if (b < p.nb) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const u32x4v x = *reinterpret_cast<const u32x4v*>(ac[i] + static_cast<int64_t>(b) * 16);
-        const u32x4v y = *reinterpret_cast<const u32x4v*>(bc[i] + static_cast<int64_t>(b) * 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          av[i][j] = static_cast<int>(x[j]);
-          bv[i][j] = static_cast<int>(y[j]);
-        }
+      for (int i = 0; i < F; ++i) {
+        av[i] = *reinterpret_cast<const u32x4v*>(ac[i] + static_cast<int64_t>(b) * 16);
+        bv[i] = *reinterpret_cast<const u32x4v*>(bc[i] + static_cast<int64_t>(b) * 16);
         asv[i] = as[i][b];
         bsv[i] = bs[i][b];
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av[i], bv[j], acc[i][j], 4, 4, 0, asv[i], 0, bsv[j]);
+      for (int j = 0; j < F; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(bv[j]), codes8(av[i]), acc[i][j], 4, 4, 0, bsv[j], 0, asv[i]);
   }
   T* out = static_cast<T*>(p.out);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t r = m0 + 16 * i + 4 * kb + q, c = n0 + 16 * j + r16;
-        if (r < p.m && c < p.n) {
-          T* o = out + r * p.ldo + c;
-          float v = acc[i][j][q];
-          if (p.accumulate) v += to_f(*o);
-          *o = static_cast<T>(v);
-        }
-      }
+    for (int j = 0; j < F; ++j) {
+      const int64_t r = m0 + 16 * i + r16, c = n0 + 16 * j + 4 * kb;
+      if (r < p.m && c < p.n) store4_out(out + r * p.ldo + c, acc[i][j], static_cast<int>(min(p.n - c, int64_t{4})), p.accumulate);
+    }
 }
 
 // Skinny kernel: MT x 16 rows of A (all of them), 16 rows of B per
@@ -882,7 +876,8 @@ static hipError_t run_tile(int out_dt, Mx4MatmulArgs a, hipStream_t s) {
 }
 
 static hipError_t run_direct(int out_dt, const Mx4MatmulArgs& a, hipStream_t s) {
-  const int64_t tn = (a.n + 63) / 64, tm = (a.m + 63) / 64;
+  constexpr int kTile = 32 * kDirectTiles;
+  const int64_t tn = (static_cast<int64_t>(a.n) + kTile - 1) / kTile, tm = (static_cast<int64_t>(a.m) + kTile - 1) / kTile;
   const dim3 g(static_cast<uint32_t>(tn * tm));
   if (out_dt == F32) mx4_direct_kernel<float><<<g, 256, 0, s>>>(a);
   else mx4_direct_kernel<__bf16><<<g, 256, 0, s>>>(a);
