@@ -15,11 +15,12 @@
 // near each other, and logits of the type's lowest value do not overflow.
 // All sums are fp32, in a fixed order.
 //
-// HBM bound.  Log probabilities, bf16: 4096 x 32000 44 us for the statistics
-// (6 TB/s), 66 with 64 alternatives (the search overlaps other rows' loads in
-// part); 501 x 129283 with 32 alternatives 35 + 5 us for the join.
-// Distillation, loss and gradient, bf16: 8192 x 32000 (1.05 GB) 230 us, 4.6
-// TB/s.  With few rows the launches bound both: 8 x 48000 fp32 7 + 5 us.
+// HBM bound.  Log probabilities, bf16: 4096 x 32000 43 us for the statistics
+// (6.1 TB/s), 67 with 32 alternatives and 75 with 64 (the search overlaps other
+// rows' loads in part); 501 x 129283 with 8 alternatives 35 + 5 us for the join.
+// Distillation, loss and gradient, bf16: 8192 x 32000 (1.05 GB) 233 us, 4.5
+// TB/s.  With few rows the launches bound both: 3 x 32000 fp32 with 20
+// alternatives 7 + 5 us.
 #include <type_traits>
 
 #include "mo_internal.h"
