@@ -193,18 +193,24 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const Mx4QuantArgs<
 // column's block then lies in 4 lanes of a wave (l, l ^ 16, l ^ 32, l ^ 48),
 // each with 8 consecutive codes of it, and a row's block in 4 neighbours.  The
 // columns' codes go through LDS so that they leave as whole 128-byte lines.
-// HBM bound: 8192 x 8192 bf16 28 us for the transpose alone, 40.5 us with both
-// (3.06 bytes an element, 5.1 TB/s); fp32 51 and 70 us.  Two workgroups of 8
+// HBM bound: 8192 x 8192 bf16 29 us for the transpose alone, 39 us with both
+// (3.06 bytes an element, 5.2 TB/s); fp32 53 and 70 us.  Two workgroups of 8
 // waves fill a CU.
-constexpr int kColTileRows = 256, kColTileCols = 128;
+constexpr int kColTileRows = 256, kColTileCols = 128, kRun = 16;
 template <typename T, int G>
 __global__ void __launch_bounds__(512, 4) mx4_quant_cols_kernel(const Mx4QuantArgs<G> a) {
   __shared__ uint32_t codes[kColTileCols][33];     // 128 bytes a column, and a dword against bank conflicts
   __shared__ __attribute__((aligned(8))) uint8_t bytes[kColTileCols][8];
   const Mx4QuantItem& it = a.item[G == 1 ? 0 : find_item(a, blockIdx.x)];
   const T* src = static_cast<const T*>(it.src);
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) - it.tile0;
+  // each XCD (workgroup index mod 8) takes runs of kRun neighbours, so that
+  // lines that two tiles share meet in its L2 (the last ones as they come):
+  // 8192 x 28672 bf16, both images, 185 to 171 us; whole matrices in eight
+  // ranges 168, but fp32 8192 x 8192 77 instead of 70
   const int64_t tiles_c = (it.cols + kColTileCols - 1) / kColTileCols;
+  const int64_t tiles = (it.rows + kColTileRows - 1) / kColTileRows * tiles_c;
+  const uint32_t b = blockIdx.x - static_cast<uint32_t>(it.tile0), g = b / (8 * kRun) * (8 * kRun);
+  const int64_t tile = g + 8 * kRun <= tiles ? g + (b % 8) * kRun + (b - g) / 8 : b;
   const int64_t row0 = tile / tiles_c * kColTileRows, col0 = tile % tiles_c * kColTileCols;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t r0 = row0 + wave * 32 + (lane >> 4) * 8, c0 = col0 + (lane & 15) * 8;
