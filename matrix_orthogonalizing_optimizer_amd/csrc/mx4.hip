@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1
           if constexpr (s == 0 && P == NP - 1 - (NP > 4)) {
             next = at + kStage == NST * kStage ? 0u : at + kStage;
             keep = keep_of(t + 1);
-            sat = scale_at(t + 1);                       // (past the end: a place that holds something)
+            sat = scale_at(min(t + 1, stages - 1));      // past the end: the last stage's again, unused
           }
           __builtin_amdgcn_sched_barrier(0);
         });
