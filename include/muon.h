@@ -409,7 +409,8 @@ int mo_distill_loss_workspace_size(int64_t rows, int64_t vocab, int top, size_t*
  *   top_index[r, i], top_logprob[r, i], i < top: the columns with the
  *       largest logits, largest first, ties to the lower column (NaN above
  *       everything, -0 equal to +0), and their l_j.
- * -inf logits are tokens of probability zero.  A row that holds a NaN or
+ * -inf logits are tokens of probability zero, and an l_j below fp32's range
+ * is -inf.  A row that holds a NaN or
  * +inf, or only -inf, has NaN logprob (scored tokens), entropy and
  * top_logprob.
  * tokens: device int64 [rows], logprob: fp32 [rows]: both or neither NULL.
@@ -437,7 +438,8 @@ int mo_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab
  * zero gradient whatever the logits.  A present slot with an index >= vocab
  * or a NaN or +inf top_logit makes the row's loss and gradient NaN; so does,
  * in a row that is not skipped, a NaN or +inf logit or a row of -inf only.
- * A teacher's token at logit -inf makes its row's loss +inf.
+ * A teacher's token at logit -inf makes its row's loss +inf, as does a loss
+ * beyond fp32's range; g_r temperature must lie within that range.
  * loss: fp32 [rows] or NULL.  grad: [rows, vocab] in the logits' dtype, rows
  * ld_grad elements apart, or NULL (then grad_loss is not read); columns
  * vocab .. ld_grad - 1 are left as they were.  One of the two is needed.

@@ -29,7 +29,8 @@ int check_sizes(int64_t rows, int64_t vocab, int top, int top_min) {
   return MO_OK;
 }
 
-// 1 / temperature times log2(e), and temperature squared, stay finite.
+// 1 / temperature times log2(e) is finite, and temperature squared, the scale
+// of the loss at high temperatures.
 int check_temperature(float t) {
   if (!(t >= 0x1p-126f && t <= 0x1p63f)) return fail(MO_EINVAL, "temperature must be in [2^-126, 2^63]");
   return MO_OK;

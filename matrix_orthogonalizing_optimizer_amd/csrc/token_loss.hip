@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(256) logprobs_join_kernel(const LogprobArgs a)
 // The teacher's side of a row: softmax over its present slots, slot k in
 // thread k of the first two waves.
 struct Teacher {
-  float p, logp;
+  float p, tau_logp;     // (tau log p stays finite where log p does not)
   int col;               // -1: absent, of no weight, or not a column
   bool skip, bad;
 };
@@ -450,19 +450,21 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, int64_t r, floa
   if (q.bad) t = -INFINITY;
   const float m = block_reduce<NT>(t, red, Max());
   q.skip = m == -INFINITY && !q.bad;
-  const float x = (t - (m == -INFINITY ? 0.0f : m)) * a.inv_tau, e = exp2_(x * kLog2e), s = block_reduce<NT>(e, red, Sum());
+  const float x = t - (m == -INFINITY ? 0.0f : m), e = exp2_(x * a.inv_tau * kLog2e), s = block_reduce<NT>(e, red, Sum());
   q.p = s > 0.0f ? e / s : 0.0f;
-  q.logp = x - log2_(s) * kLn2;
+  q.tau_logp = x - log2_(s) * (kLn2 * a.tau);
   q.col = q.p > 0.0f ? static_cast<int>(idx) : -1;
   return q;
 }
 
-// tau^2 sum p (log p - log q), in every thread.
+// tau^2 sum p (log p - log q) as tau sum p (tau log p - tau log q), in every
+// thread: tau^2 underflows below tau = 2^-75, and a logit's distance from the
+// largest over tau overflows there, where the loss itself does neither.
 template <int NT, typename T>
 __device__ __forceinline__ float distill_value(const DistillArgs& a, const Teacher& q, const T* z, Stats st, float* red) {
-  const float lq = q.col >= 0 ? (static_cast<float>(z[q.col]) - st.ref) * a.inv_tau - log2_(st.s) * kLn2 : 0.0f;
-  const float l = block_reduce<NT>(q.col >= 0 ? q.p * (q.logp - lq) : 0.0f, red, Sum());
-  return q.bad || st.ref == -INFINITY || st.s != st.s ? NAN : a.tau * a.tau * l;
+  const float lq = q.col >= 0 ? (static_cast<float>(z[q.col]) - st.ref) - log2_(st.s) * (kLn2 * a.tau) : 0.0f;
+  const float l = block_reduce<NT>(q.col >= 0 ? q.p * (q.tau_logp - lq) : 0.0f, red, Sum());
+  return q.bad || st.ref == -INFINITY || st.s != st.s ? NAN : a.tau * l;
 }
 
 template <int NT>
