@@ -629,6 +629,12 @@ def mx4_linear_backward(dy: torch.Tensor, x_t: Mx4Matrix, w_t: Mx4Matrix, *,
     d2 = _flat2(dy)
     if d2.shape[0] != x_t.cols or d2.shape[1] != w_t.cols:
         raise ValueError(f"dy is {tuple(d2.shape)}, the images want [{x_t.cols}, {w_t.cols}]")
+    if x_t.rows != w_t.rows:
+        raise ValueError(f"x has {x_t.rows} features, the weights {w_t.rows}")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    if dw is not None and tuple(dw.shape) != (w_t.cols, x_t.rows):
+        raise ValueError(f"dw must be [{w_t.cols}, {x_t.rows}], got {tuple(dw.shape)}")
     dq, dq_t = mx4_quantize(d2, images="both", stream=stream)
     dx = mx4_matmul(dq, w_t, out_dtype=dx_dtype, stream=stream)
     dw = mx4_matmul(dq_t, x_t, out_dtype=torch.float32, out=dw, accumulate=accumulate, stream=stream)
