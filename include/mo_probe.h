@@ -10,7 +10,7 @@
  * streaming kernels, so that the fractions can also be read against
  * achieved ceilings.  Not part of the optimizer's ABI.
  *
- * Both calls allocate and free their own device memory, synchronise the
+ * All calls allocate and free their own device memory, synchronise the
  * device and time with HIP events on an internal stream.  They return
  * 0 on success and a negative value on a HIP error (the message is then
  * available from mo_probe_last_error()).
@@ -38,6 +38,13 @@ int mo_probe_mfma_bf16(int iters, int reps, double* tflops);
  * is what the matrix cores sustain within the chip's power budget on real
  * data, still with no memory traffic.  Same units and outputs. */
 int mo_probe_mfma_bf16_random(int iters, int reps, double* tflops);
+
+/* The same grid and issue pattern for the scaled 4-bit instruction
+ * v_mfma_scale_f32_32x32x64_f8f6f4 (unit scales) of the products of MX4
+ * images: on random codes, eight operands per side cycled (random_codes !=
+ * 0), or on zero codes, which the power limit does not slow.
+ * *tflops = 131072 flop x MFMAs / seconds; best of `reps` launches. */
+int mo_probe_mfma_fp4(int random_codes, int iters, int reps, double* tflops);
 
 /* HBM rates over a buffer of `bytes` (rounded down to 64 KiB):
  * *read_gbs: a read-only reduction of the whole buffer (16-byte loads);

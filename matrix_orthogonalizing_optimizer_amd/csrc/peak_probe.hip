@@ -1,5 +1,5 @@
-// Roofline probes (declared in include/mo_probe.h): the bf16 matrix-core
-// rate and the HBM streaming rates the chip sustains on their own.
+// Roofline probes (declared in include/mo_probe.h): the bf16 and 4-bit matrix-core
+// rates and the HBM streaming rates the chip sustains on their own.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -101,6 +101,37 @@ __global__ __launch_bounds__(256) void mfma_random_probe_kernel(float* out, int 
   out[blockIdx.x * blockDim.x + threadIdx.x] = s;
 }
 
+// The scaled 4-bit instruction on register operands, four independent
+// accumulators, unit scales: eight A and eight B operands of random codes per
+// lane, cycled as above (kRandom), or codes that are all zero.
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+constexpr int kUnitScale = 0x7f7f7f7f;
+template <bool kRandom>
+__global__ __launch_bounds__(256) void mfma_fp4_probe_kernel(float* out, int iters) {
+  const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
+  i32x8_t a[kOps] = {}, b[kOps] = {};
+#pragma unroll
+  for (int o = 0; o < kOps; ++o)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[o][k] = kRandom ? static_cast<int>(probe_hash(t * 64u + o * 8u + k)) : 0;
+      b[o][k] = kRandom ? static_cast<int>(probe_hash(t * 64u + o * 8u + 4u + k) ^ 0x9e3779b9u) : 0;
+    }
+  f32x16_t acc[kChains];
+  for (int c = 0; c < kChains; ++c)
+    for (int r = 0; r < 16; ++r) acc[c][r] = 0.0f;
+  for (int i = 0; i < iters; ++i) {
+#pragma unroll
+    for (int k = 0; k < kPerIter; ++k)
+      acc[k % kChains] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          a[k % kOps], b[(3 * k + 1) % kOps], acc[k % kChains], 4, 4, 0, kUnitScale, 0, kUnitScale);
+  }
+  float s = 0.0f;
+  for (int c = 0; c < kChains; ++c)
+    for (int r = 0; r < 16; ++r) s += acc[c][r];
+  out[blockIdx.x * blockDim.x + threadIdx.x] = s;
+}
+
 // Streaming kernels: each pass of the grid covers gridDim.x * 256 * U
 // consecutive 16-byte words, thread t of a block taking words t, t + 256,
 // .. t + 256 (U - 1) of its block's span (coalesced), U loads in flight
@@ -171,7 +202,8 @@ int cu_count(int* cus) {
   return e == hipSuccess ? 0 : probe_fail(e, "device query");
 }
 
-int mfma_probe(bool random_operands, int iters, int reps, double* tflops) {
+// Rate of a probe kernel whose instruction does `flops` operations.
+int mfma_probe(void (*kernel)(float*, int), double flops, int iters, int reps, double* tflops) {
   if (iters < 1 || reps < 1 || !tflops) {
     g_probe_err = "iters and reps must be >= 1, tflops non-NULL";
     return -2;
@@ -188,10 +220,7 @@ int mfma_probe(bool random_operands, int iters, int reps, double* tflops) {
   for (int r = 0; r <= reps && e == hipSuccess; ++r) {   // the first launch warms up
     e = hipEventRecord(e0, nullptr);
     if (e == hipSuccess) {
-      if (random_operands)
-        hipLaunchKernelGGL(mfma_random_probe_kernel, dim3(blocks), dim3(256), 0, nullptr, out, iters);
-      else
-        hipLaunchKernelGGL(mfma_probe_kernel, dim3(blocks), dim3(256), 0, nullptr, out, iters);
+      hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, nullptr, out, iters);
       e = hipGetLastError();
     }
     if (e == hipSuccess) e = hipEventRecord(e1, nullptr);
@@ -199,8 +228,8 @@ int mfma_probe(bool random_operands, int iters, int reps, double* tflops) {
     float ms = 0.0f;
     if (e == hipSuccess) e = hipEventElapsedTime(&ms, e0, e1);
     if (e == hipSuccess && r > 0 && ms > 0.0f) {
-      const double flops = 32768.0 * kPerIter * static_cast<double>(iters) * blocks * 4.0;
-      best = std::max(best, flops / (ms * 1e-3) / 1e12);
+      const double work = flops * kPerIter * static_cast<double>(iters) * blocks * 4.0;
+      best = std::max(best, work / (ms * 1e-3) / 1e12);
     }
   }
   const hipError_t run = e;
@@ -218,10 +247,16 @@ extern "C" {
 
 const char* mo_probe_last_error(void) { return g_probe_err.c_str(); }
 
-int mo_probe_mfma_bf16(int iters, int reps, double* tflops) { return mfma_probe(false, iters, reps, tflops); }
+int mo_probe_mfma_bf16(int iters, int reps, double* tflops) {
+  return mfma_probe(mfma_probe_kernel, 32768.0, iters, reps, tflops);
+}
 
 int mo_probe_mfma_bf16_random(int iters, int reps, double* tflops) {
-  return mfma_probe(true, iters, reps, tflops);
+  return mfma_probe(mfma_random_probe_kernel, 32768.0, iters, reps, tflops);
+}
+
+int mo_probe_mfma_fp4(int random_codes, int iters, int reps, double* tflops) {
+  return mfma_probe(random_codes ? mfma_fp4_probe_kernel<true> : mfma_fp4_probe_kernel<false>, 131072.0, iters, reps, tflops);
 }
 
 int mo_probe_hbm(size_t bytes, int reps, double* read_gbs, double* copy_gbs) {
