@@ -11,6 +11,10 @@ weights needs: microscaled 4-bit images of matrices and their products
 (``mx4_*``), token log probabilities with the top alternatives, and the
 distillation loss with its gradient.
 
+No function here takes part in autograd: results carry no graph, also where
+an argument requires a gradient.  The backward passes are calls of their own
+(``mx4_linear_backward``, the gradient that ``distill_loss`` returns).
+
 This module only marshals torch tensors into the C ABI of ``libmuon.so``
 (``include/muon.h``); PyTorch provides device memory and streams.  Every
 arithmetic step runs in the HIP library, and there is no fallback.
@@ -603,7 +607,8 @@ def mx4_linear(x: torch.Tensor, w: Mx4Matrix, *, out_dtype: torch.dtype = torch.
                save: bool = False, stream=None):
     """``y = x W^T`` with W [N, K] held in 4 bits and x [..., K] (fp32 or
     bf16) quantised on the way.  ``save=True`` also returns the image of x^T
-    that :func:`mx4_linear_backward` takes (and needs one token at least)."""
+    that :func:`mx4_linear_backward` takes (and needs one token at least).
+    Not seen by autograd."""
     x2 = _flat2(x)
     if x2.shape[1] != w.cols:
         raise ValueError(f"x has {x2.shape[1]} features, the weights {w.cols}")
@@ -687,7 +692,8 @@ def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_logit: torch
     is skipped) and ``top_logit`` fp32 [rows, k] -- ``top_index`` and
     ``top_logprob`` of :func:`token_logprobs` on the teacher serve as they
     are.  ``grad_loss`` fp32 [rows]: the gradient that reaches each row's
-    loss (1 when None).  ``out_grad``: written instead of a new tensor."""
+    loss (1 when None).  ``out_grad``: written instead of a new tensor.  Not
+    seen by autograd: pass the gradient on yourself."""
     ptr, rows, vocab, ld = _rows_of(logits, "logits")
     dt, dev = _dtype_code(logits.dtype, "logits"), logits.device
     if top_index.dim() != 2:

@@ -461,11 +461,15 @@ __device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate
 // Blocks past the end load the last block's codes under zero scale bytes in
 // both operands: 2^-254 of a value of at most 36 is zero in fp32.
 //
-// 8192 x 28672 x 8192, operands quantised from normal values: 0.99 to 1.06 ms,
-// 3.6 to 3.9 PFLOP/s.  A loop of nothing but this instruction on random codes
-// runs at 6.6, both at the clock that the power limit leaves: 8192^3 takes 220
-// us with zero codes, 282 with normal values and 335 with random codes.  The
-// larger the tile, the fewer bytes each product takes from the caches (64
+// 8192 x 28672 x 8192, operands quantised from normal values: 0.95 to 1.08 ms
+// by box, 3.6 to 4.0 PFLOP/s.  A loop of nothing but this instruction runs at
+// 6.1 to 6.6 on random codes, at the clock that the power limit leaves, and at
+// 9.9 on zero codes.  8192^3 takes 220 us with zero codes (5.0 PFLOP/s), 282
+// with normal values and 335 with random codes: the power limit costs a
+// quarter, and even without it the matrix cores wait half of the time, though
+// neither LDS nor the cache path is full: with one wave per SIMD and no second
+// workgroup, nothing covers the wait at each stage's barrier, nor the first
+// requests and the stores of a tile.  The larger the tile, the fewer bytes each product takes from the caches (64
 // bytes a clock and CU): 256 x 256 with four waves of 128 x 128 outputs, one
 // workgroup to a CU, takes half of that path's time; two workgroups of 128 x
 // 256 took three quarters of it and 14% longer.  Eight waves in the 256 tile
@@ -900,10 +904,13 @@ static hipError_t run_skinny(int out_dt, const Mx4MatmulArgs& a, int waves, hipS
 }
 
 // Which kernel.  Measured on products of K = 8192 (and, at a quarter to a third
-// of these times, K = 2048), in us:
+// of these times, K = 2048), in us.  K is not in the rule: where the number of
+// stages differs much from 64, the fixed part of each tile weighs differently
+// than these figures say.
 //  * skinny against 64 tiles: 1 x 2048 5 and 19, 32 x 8192 17 and 19, 8 x 28672
 //    31 and 28, 16 x 28672 35 and 29, 32 x 28672 50 and 29: up to 32 rows while
-//    each row of A is not read again by too many workgroups;
+//    each row of A is not read again by too many workgroups (one bound on the
+//    outputs; near it, at 8 x 28672, the 64 tiles would be a tenth faster);
 //  * 64 tiles: 19 for up to 256 of them, 24 for 512, then in proportion;
 //  * 128 tiles: 29 for up to 256, 52 for 512, 81 for 768, 112 for 1024;
 //  * 256 tiles: 58 for 128 of them, 76 for 256, 162 for 512: whole rounds, as a

@@ -4,9 +4,10 @@
 //
 // Both read a row of logits once into registers: a workgroup's registers
 // hold up to 320 KiB, so the maximum, the sum against it, the alternatives
-// and the gradient all come from one reading.  Rows that are longer, or too
-// few to fill the chip, are cut into pieces of one workgroup each, whose
-// statistics a second launch joins.
+// and the gradient all come from one reading.  Longer rows (over 64 KiB for
+// the log probabilities, over 320 KiB for the loss) are cut into pieces of one
+// workgroup each, whose statistics a second launch joins; shorter ones are one
+// workgroup each, however few they are.
 //
 // With m the largest logit of the row (or piece) and x_j = logit_j - m, the
 // sums are S = sum exp(x_j / tau) and U = sum exp(x_j / tau) x_j, and
@@ -19,8 +20,9 @@
 // (6.1 TB/s), 67 with 32 alternatives and 75 with 64 (the search overlaps other
 // rows' loads in part); 501 x 129283 with 8 alternatives 35 + 5 us for the join.
 // Distillation, loss and gradient, bf16: 8192 x 32000 (1.05 GB) 233 us, 4.5
-// TB/s.  With few rows the launches bound both: 3 x 32000 fp32 with 20
-// alternatives 7 + 5 us.
+// TB/s; rows of 128 to 320 KiB, where one workgroup fills a CU, 2048 x 128256
+// 306 us and 1024 x 151936 189 us, 3.3 to 3.4 TB/s.  With few rows the launches
+// bound both: 3 x 32000 fp32 with 20 alternatives 7 + 5 us.
 #include <type_traits>
 
 #include "mo_internal.h"
@@ -204,8 +206,11 @@ struct RowRegs {
 // search looks at the upper half of the keys and rounds down); the elements
 // that reach it, little more than n unless many are equal, go to a list, and
 // each takes its place by counting the larger ones.  A list that overflows
-// (plateaus, rows with few columns) is replaced by an exact search for the
-// n-th key over all elements, a bit at a time.
+// (plateaus; rows whose mask leaves fewer threads with a token than n) is
+// replaced by an exact search for the n-th key over all elements, a bit at a
+// time, each of which reads the row again: 4096 x 32000 bf16 with 64
+// alternatives takes 10.9 ms instead of 75 us when every row comes to that
+// (one column in a thousand left, or all equal), 3 rows 136 us instead of 16.
 constexpr int kCand = 512;
 template <int NT>
 struct TopLds {
@@ -559,9 +564,9 @@ __global__ void __launch_bounds__(NT, waves_for(NT, NV)) distill_kernel(const Di
 }  // namespace
 
 // -------------------------------------------------------------------- launches
-// Pieces of a row: a row that a workgroup's registers hold (`whole`) is not
-// cut.  Longer ones are cut into 64 KiB, or, where that leaves most of the
-// chip idle, into 16 KiB.
+// Pieces of a row: a row of at most `whole` bytes, which a workgroup's
+// registers hold, is not cut, however few rows there are.  Longer ones are cut
+// into 64 KiB, or, where that leaves most of the chip idle, into 16 KiB.
 namespace {
 constexpr int64_t kSmallPiece = 16 << 10, kLargePiece = 64 << 10;
 
