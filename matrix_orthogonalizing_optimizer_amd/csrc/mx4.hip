@@ -469,12 +469,13 @@ __device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate
 // quarter, and even without it the matrix cores wait half of the time, though
 // neither LDS nor the cache path is full: with one wave per SIMD and no second
 // workgroup, nothing covers the wait at each stage's barrier, nor the first
-// requests and the stores of a tile.  The larger the tile, the fewer bytes each product takes from the caches (64
-// bytes a clock and CU): 256 x 256 with four waves of 128 x 128 outputs, one
-// workgroup to a CU, takes half of that path's time; two workgroups of 128 x
-// 256 took three quarters of it and 14% longer.  Eight waves in the 256 tile
-// read twice the LDS bytes per product (6% longer).  Rings of six and ten
-// stages for the 64 tile, and bands of 2, 8 and 16 tile rows, gain nothing.
+// requests and the stores of a tile.  The larger the tile, the fewer bytes each
+// product takes from the caches (64 bytes a clock and CU): 256 x 256 with four
+// waves of 128 x 128 outputs, one workgroup to a CU, takes half of that path's
+// time; two workgroups of 128 x 256 took three quarters of it and 14% longer.
+// Eight waves in the 256 tile read twice the LDS bytes per product (6% longer).
+// Rings of six and ten stages for the 64 tile, and bands of 2, 8 and 16 tile
+// rows, gain nothing.
 constexpr int kStageRow = 64;          // bytes of a row in one stage
 
 // A wave-uniform address, said to be one.

@@ -464,7 +464,7 @@ __device__ __forceinline__ Teacher teacher(const DistillArgs& a, int64_t r, floa
 
 // tau^2 sum p (log p - log q) as tau sum p (tau log p - tau log q), in every
 // thread: tau^2 underflows below tau = 2^-75, and a logit's distance from the
-// largest over tau overflows there, where the loss itself does neither.
+// largest, over tau, overflows near 2^-126, where the loss itself does neither.
 template <int NT, typename T>
 __device__ __forceinline__ float distill_value(const DistillArgs& a, const Teacher& q, const T* z, Stats st, float* red) {
   const float lq = q.col >= 0 ? (static_cast<float>(z[q.col]) - st.ref) - log2_(st.s) * (kLn2 * a.tau) : 0.0f;

@@ -22,14 +22,13 @@ def _images(m, n, k):
     return a, b, _np(mo.mx4_dequantize(a, dtype=torch.float32)), _np(mo.mx4_dequantize(b, dtype=torch.float32))
 
 
-@pytest.mark.parametrize("k", [2049, 2176, 2200, 2432, 6273, 6528])
-@pytest.mark.parametrize("tile", TILES)
+# (the longer ones reach the same place as the shorter, at a long oracle's cost in the largest tile)
+@pytest.mark.parametrize("tile,k", [(t, k) for t in TILES for k in (2049, 2176, 2200, 2432, 6273, 6528)
+                                    if t != "256" or k <= 2432])
 def test_scales_that_end_inside_a_request(tile, k):
     """One to three stages into an odd group of sixteen, whole and partial:
     the place after the last scale dword is then the end of the kernel's
     shared memory, which nothing may read."""
-    if tile == "256" and k > 2432:
-        pytest.skip("the same place as the shorter ones, and a long oracle")
     m, n = TILES[tile]
     a, b, av, bv = _images(m, n, k)
     for dt in DTYPES:
