@@ -7,19 +7,13 @@
 
 #include "mo_internal.h"
 #include "mx4_internal.h"
-#include "ns_common.h"
+#include "product.h"
 
 namespace mo {
 
 namespace {
 
-typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 typedef int i32x8v __attribute__((ext_vector_type(8)));
-typedef float f32x4v __attribute__((ext_vector_type(4)));
-
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f<__bf16>(__bf16 v) { return static_cast<float>(v); }
 
 // Scale byte of a block from the bits of its largest magnitude: the biased
 // exponent less 2 (the list's largest binade starts at 4 = 2^2), 255 for a
@@ -30,92 +24,20 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   return e > 2u ? e - 2u : 0u;
 }
 
-// Sixteen bytes, aligned to the element only: rows may start anywhere, and the
-// hardware's unaligned access costs less than peeling.
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x4u2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
-typedef float f32x2v __attribute__((ext_vector_type(2)));
-
-// Eight consecutive elements of a row.
-template <typename T> struct Oct;
-template <> struct Oct<float> {
-  f32x4v lo, hi;
-  __device__ __forceinline__ void load(const float* p, int n) {        // n > 0 present, the others 0
-    if (n >= 8) {
-      lo = *reinterpret_cast<const f32x4u*>(p);
-      hi = *reinterpret_cast<const f32x4u*>(p + 4);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        lo[j] = j < n ? p[j] : 0.0f;
-        hi[j] = j + 4 < n ? p[j + 4] : 0.0f;
-      }
-    }
-  }
-  __device__ __forceinline__ void clear() { lo = hi = f32x4v{0.0f, 0.0f, 0.0f, 0.0f}; }
-  __device__ __forceinline__ float get(int j) const { return j < 4 ? lo[j] : hi[j - 4]; }
-  __device__ __forceinline__ uint32_t bits(int j) const { return __float_as_uint(get(j)) & 0x7fffffffu; }
-  // bits of the largest magnitude
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, bits(j));
-    return m;
-  }
-  // the eight codes, element 0 lowest
-  __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo[0], lo[1], s, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo[2], lo[3], s, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, hi[0], hi[1], s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, hi[2], hi[3], s, 3);
-  }
-};
-template <> struct Oct<__bf16> {
-  u32x4v v;
-  __device__ __forceinline__ void load(const __bf16* p, int n) {
-    if (n >= 8) {
-      v = *reinterpret_cast<const u32x4u2*>(p);
-    } else {
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = (2 * j < n ? q[2 * j] : 0u) | (2 * j + 1 < n ? static_cast<uint32_t>(q[2 * j + 1]) << 16 : 0u);
-    }
-  }
-  __device__ __forceinline__ void clear() { v = u32x4v{0u, 0u, 0u, 0u}; }
-  __device__ __forceinline__ bf16x2v pair(int i) const {
-    const uint32_t w = v[i];             // a bit cast of the vector's element itself reads element 0
-    return __builtin_bit_cast(bf16x2v, w);
-  }
-  __device__ __forceinline__ float get(int j) const {
-    return __uint_as_float((j & 1) ? (v[j / 2] & 0xffff0000u) : (v[j / 2] << 16));
-  }
-  __device__ __forceinline__ uint32_t bits(int j) const { return __float_as_uint(get(j)) & 0x7fffffffu; }
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, bits(j));
-    return m;
-  }
-  __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(0), s, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(1), s, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(2), s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, pair(3), s, 3);
-  }
-};
-
-// The scale of a block as the conversions take it: only its exponent counts,
-// and an exponent of 0 means 2^-127.
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
-
-// Largest of a quad of lanes.
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
-  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true)));   // lanes 1 0 3 2
-  return max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true)));   // lanes 2 3 0 1
+// The eight codes, element 0 lowest.
+__device__ __forceinline__ uint32_t fp4_codes(const Oct<float>& o, float s) {
+  uint32_t r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o.lo[0], o.lo[1], s, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o.lo[2], o.lo[3], s, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o.hi[0], o.hi[1], s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, o.hi[2], o.hi[3], s, 3);
+}
+__device__ __forceinline__ uint32_t fp4_codes(const Oct<__bf16>& o, float s) {
+  uint32_t r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, o.pair(0), s, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, o.pair(1), s, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, o.pair(2), s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, o.pair(3), s, 3);
 }
 
 // Codes of the lane's eighth of a row's block, whose scale byte it also gives:
@@ -123,21 +45,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
 template <typename T>
 __device__ __forceinline__ uint32_t row_codes(const Oct<T>& o, uint32_t& byte) {
   byte = scale_byte(quad_max(o.amax()));
-  const uint32_t c = o.codes(scale_of(byte));
+  const uint32_t c = fp4_codes(o, scale_of(byte));
   return byte == 255u ? 0u : c;
-}
-
-// The matrix that workgroup `b` belongs to: the last whose first one is not
-// past it.
-template <typename A>
-__device__ __forceinline__ int find_item(const A& a, int64_t b) {
-  int lo = 0, hi = a.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.item[mid].tile0 <= b) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 }  // namespace
@@ -403,45 +312,6 @@ __device__ __forceinline__ f32x16v mfma32(u32x4v a, u32x4v b, f32x16v c, uint32_
                                                          static_cast<int>(sb));
 }
 
-// Waits until at most `kLeft` of this wave's loads are outstanding, and for
-// its LDS reads.
-template <int kLeft>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(kLeft < 64, "the counter has 6 bits");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLeft) & (kWaitLgkm0 | (63 & 15) | (3 << 14)));
-  asm volatile("" ::: "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ void store_out(T* o, float v, int accumulate) {
-  if (accumulate) v += to_f(*o);
-  *o = static_cast<T>(v);
-}
-
-// Four consecutive outputs, n of them inside.
-template <typename T>
-__device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate) {
-  if (n >= 4) {
-    if constexpr (sizeof(T) == 4) {
-      if (accumulate) v += *reinterpret_cast<const f32x4u*>(o);
-      *reinterpret_cast<f32x4u*>(o) = v;
-    } else {
-      typedef uint32_t u32x2u2 __attribute__((ext_vector_type(2), aligned(2)));
-      if (accumulate) {
-        const u32x2u2 w = *reinterpret_cast<const u32x2u2*>(o);
-        v += f32x4v{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
-                    __uint_as_float(w[1] & 0xffff0000u)};
-      }
-      *reinterpret_cast<u32x2u2*>(o) = u32x2u2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < n) store_out(o + k, v[k], accumulate);
-  }
-}
-
 // Tile kernel.  The contraction runs in stages of 4 blocks (128 columns):
 // two instructions per output fragment, lanes 0..31 of a wave taking the
 // stage's first two blocks and lanes 32..63 the others (any order of blocks
@@ -477,23 +347,6 @@ __device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate
 // Rings of six and ten stages for the 64 tile, and bands of 2, 8 and 16 tile
 // rows, gain nothing.
 constexpr int kStageRow = 64;          // bytes of a row in one stage
-
-// A wave-uniform address, said to be one.
-__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
-  return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
-}
-
-// lds_dma16 to lds_base + kPlus.
-template <int kPlus>
-__device__ __forceinline__ void lds_dma16_at(const void* sbase, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(voff), "s"(sbase), "s"(lds_base), "n"(kPlus)
-               : "memory", "m0", "scc");
-}
 
 template <int TM, int TN, int WM, int WN, int NST, typename T>
 __global__ void __launch_bounds__(64 * WM * WN, TM * TN / (WM * WN) >= 16384 ? 1 : 2) mx4_tile_kernel(const Mx4MatmulArgs p) {
