@@ -449,6 +449,150 @@ int mo_distill_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, 
                     float temperature, const float* grad_loss, float* loss, void* grad,
                     int64_t ld_grad, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floating point matrices ("FP8") with a scale for each block of 128.
+ *
+ * The image of a matrix X [rows, cols] holds each element as an e4m3 number
+ * (sign, 4 exponent bits of bias 7, 3 mantissa bits, subnormals, largest 448,
+ * 0x7f and 0xff NaN) times a power of two shared by 128 consecutive elements
+ * of a row (block b: columns 128 b .. 128 b + 127; the last block may be
+ * short).  With nb = ceil(cols / 128):
+ *   codes   uint8 [rows][128 nb]: element (r, c) is byte c.
+ *   scales  uint8 [rows][16 ceil(nb / 16)]: byte b of a row is e + 127 for
+ *           the block's scale 2^e; 255 makes the block NaN.
+ * Padding (codes of columns >= cols, scales of blocks >= nb) is zero.
+ * codes and scales are 16-byte aligned.  A matrix without rows or columns has
+ * an empty image, whose pointers may be NULL.
+ *
+ * Quantisation: a = the block's largest |x|; e = the smallest integer with a
+ * <= 448 2^e, at least -127 (byte 0 for a = 0); code = x 2^-e rounded to
+ * nearest, halfway cases to even.  With square scales a is the largest of 128
+ * rows x 128 columns (rows 128 i .. 128 i + 127), so that the image of the
+ * transpose holds the same values: the form for weights, whose gradients then
+ * belong to the values that the forward pass multiplied.  A block that holds a
+ * NaN or an infinity gets scale byte 255 and zero codes: its values read back
+ * as NaN, and so does every product they enter.
+ * ---------------------------------------------------------------------- */
+typedef struct mo_fp8_image {
+    const void* codes;
+    const void* scales;
+    int64_t     rows;
+    int64_t     cols;
+} mo_fp8_image;
+
+/* One matrix to quantise.  src [rows, cols], rows `ld` elements apart
+ * (ld >= cols), aligned to its element.  codes / scales: the image of src,
+ * or both NULL.  codes_t / scales_t: the image of its transpose [cols,
+ * rows] (blocks run along src's columns), or both NULL.  One of the two is
+ * needed. */
+typedef struct mo_fp8_item {
+    const void* src;
+    void*       codes;
+    void*       scales;
+    void*       codes_t;
+    void*       scales_t;
+    int64_t     rows;
+    int64_t     cols;
+    int64_t     ld;
+} mo_fp8_item;
+
+/* Bytes of an image's two arrays.  0 <= rows, cols < 2^31 and rows * cols
+ * <= 2^40.  Host-only. */
+int mo_fp8_image_size(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
+
+/* Quantises `count` matrices of one dtype (MO_F32 or MO_BF16) on `stream`,
+ * grouped into few launches; square != 0: square scales.  An output may not
+ * overlap a source or another output.  Results do not depend on the grouping. */
+int mo_fp8_quantize(const mo_fp8_item* items, int64_t count, int dtype, int square, void* stream);
+
+/* The values that `count` images stand for: dst[i] contiguous [rows, cols]
+ * in dtype, 16-byte aligned.  Exact in fp32, and in bf16 but for steps below
+ * 2^-133, which only blocks below 2^-116 have and which are rounded; values of
+ * 2^128 and more, which only images of another origin hold, become inf. */
+int mo_fp8_dequantize(const mo_fp8_image* images, void* const* dst, int64_t count, int dtype,
+                      void* stream);
+
+/* out[m, n] = sum_k a[m, k] b[n, k] over the values of two images with the
+ * same cols (a [M, K], b [N, K]), + out[m, n] when accumulate != 0.
+ * Products enter fp32 sums on the matrix cores; the result (after the
+ * accumulation) is rounded once to out_dtype (MO_F32 or MO_BF16).  out: rows
+ * ldo elements apart (ldo >= N), aligned to its element; columns N .. ldo - 1
+ * are left as they were.  out may not overlap an image.  Results do not
+ * depend on the run (no atomics).  K <= 2^23 (K = 0: zeros) and ceil(M / 64)
+ * ceil(N / 64) < 2^24. */
+int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int out_dtype,
+                  int64_t ldo, int accumulate, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Cross entropy of a linear layer's logits, without keeping the logits.
+ *
+ * x [rows, hidden], w [vocab, hidden], z = x w^T.  Per row t with target y_t:
+ *   loss[t] = log sum_v exp(z_tv) - z_{t, y_t},
+ *   dz_tv   = g_t (exp(z_tv) / sum_v exp(z_tv) - [v = y_t]),
+ *   dx = dz w,   dw = dz^T x  (+ dw when accumulate != 0).
+ * The products take bf16 operands: x and w given in fp32 are rounded to bf16
+ * on the way.  Sums and the softmax's statistics are fp32.  dz enters the
+ * products for a bf16 gradient rounded to bf16 (relative to the largest |g|),
+ * for an fp32 gradient as a sum of three bf16 terms.  Each gradient is rounded
+ * once to its type (after the accumulation).  Results do not depend on the run
+ * (no atomics).
+ *
+ * A row with a negative target takes no part: loss 0, dx 0 and nothing in dw,
+ * whatever its x holds.  g_t = 0 does the same to the row's gradients.  A
+ * target >= vocab makes the row's loss and dx and all of dw NaN; so does, in a
+ * row that takes part, a NaN or +inf logit or a row of -inf only (infinite or
+ * NaN weights therefore reach every row that takes part).  Logits are the fp32
+ * sums.
+ * ---------------------------------------------------------------------- */
+
+/* Workspace of mo_linear_ce.  want_dx, want_dw: whether the call gives dx and
+ * dw; dx has x's dtype.  Host-only. */
+int mo_linear_ce_workspace_size(int64_t rows, int64_t hidden, int64_t vocab, int x_dtype,
+                                int dw_dtype, int want_dx, int want_dw, size_t* bytes);
+
+/* x: rows ldx elements apart (ldx >= hidden), w: ldw, dx [rows, hidden]: ld_dx,
+ * dw [vocab, hidden]: ld_dw; all aligned to their elements (columns past
+ * hidden are neither read nor written).  targets: int64 [rows]; grad_loss: fp32
+ * [rows], the gradient that reaches each loss, 1 when NULL; loss: fp32 [rows].
+ * dx (x's dtype) and dw (dw_dtype) may each be NULL: then it is not computed.
+ * 0 <= rows <= 2^20, 1 <= hidden <= 2^22, 1 <= vocab < 2^31.  With rows = 0 dw
+ * is zeros (or left as it was with accumulate).  Outputs may not overlap each
+ * other, an input or the workspace. */
+int mo_linear_ce(const void* x, int x_dtype, int64_t ldx, const void* w, int w_dtype, int64_t ldw,
+                 int64_t rows, int64_t hidden, int64_t vocab, const int64_t* targets,
+                 const float* grad_loss, float* loss, void* dx, int64_t ld_dx, void* dw,
+                 int dw_dtype, int64_t ld_dw, int accumulate, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Balance loss of a router, its experts' counts and the gradient.
+ *
+ * logits [tokens, experts] (MO_F32 or MO_BF16), rows ld elements apart; index
+ * int64 [tokens, top]: the experts that each token chose; a negative one is a
+ * choice that was not made or was dropped.  A token without any choice (padding
+ * behind a sequence) takes no part, whatever its logits.  With p_t the softmax
+ * of token t's logits, n the number of tokens that take part, counts[e] the
+ * choices of expert e (an expert named twice counts twice), f_e = experts
+ * counts[e] / sum counts and P_e the mean of p_te over those n tokens:
+ *   loss = weight sum_e f_e P_e   (weight for perfect balance; 0 for n = 0),
+ *   grad[t, j] = g weight / n p_tj (f_j - sum_e f_e p_te)   (+ grad[t, j] when
+ *       accumulate != 0; 0 in rows that take no part),
+ * g = grad_loss (one fp32, the gradient that reaches the loss), 1 when NULL.
+ * No gradient passes through the counts.  An index >= experts is not counted
+ * and makes the loss and the gradient of every row that takes part NaN; so does
+ * a NaN or +inf logit, or a row of -inf only, to the loss and its own row.
+ * loss: one fp32; counts: int64 [experts]; grad: [tokens, experts] in the
+ * logits' dtype, rows ld_grad elements apart, or NULL.  Sums are fp32 in a fixed
+ * order: results do not depend on the run.  0 <= tokens < 2^31, 1 <= experts,
+ * top <= 4096, weight finite.  Outputs may not overlap each other, an input or
+ * the workspace.
+ * ---------------------------------------------------------------------- */
+int mo_balance_loss_workspace_size(int64_t tokens, int64_t experts, size_t* bytes);
+int mo_balance_loss(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                    const int64_t* index, int64_t top, float weight, const float* grad_loss,
+                    float* loss, int64_t* counts, void* grad, int64_t ld_grad, int accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Kernel classes for the timing counters below. */
 typedef enum mo_kernel_class {
     MO_K_MOMENTUM = 0,     /* momentum + Nesterov + norm partials + X_0 copy */
@@ -470,7 +614,13 @@ typedef enum mo_kernel_class {
     MO_K_MX4_MATMUL = 16,  /* MX4 product (flops)                            */
     MO_K_LOGPROBS = 17,    /* token log probabilities (bytes moved)          */
     MO_K_DISTILL = 18,     /* distillation loss and gradient (bytes moved)   */
-    MO_K_COUNT = 19
+    MO_K_FP8_QUANT = 19,   /* FP8 quantisation (bytes moved)                 */
+    MO_K_FP8_DEQUANT = 20, /* FP8 images read back (bytes moved)             */
+    MO_K_FP8_MATMUL = 21,  /* FP8 product (flops)                            */
+    MO_K_LINEAR_CE = 22,   /* linear cross entropy, all launches (flops of
+                              the logits and of each gradient, once)         */
+    MO_K_BALANCE = 23,     /* balance loss, all launches (bytes moved)       */
+    MO_K_COUNT = 24
 } mo_kernel_class;
 
 /* Timing counters.  mo_profile_enable(mask): for every class k with bit k

@@ -9,11 +9,15 @@ the same learning rate and decay for non-matrix parameters.
 Next to the step stand the operators that a 4-bit student of the trained
 weights needs: microscaled 4-bit images of matrices and their products
 (``mx4_*``), token log probabilities with the top alternatives, and the
-distillation loss with its gradient.
+distillation loss with its gradient.  For training in 8 bits: 8-bit floating
+point images with a scale per block of 128 and their products (``fp8_*``), the
+cross entropy of an LM head without its logits, and a router's balance loss
+with its experts' counts.
 
 No function here takes part in autograd: results carry no graph, also where
 an argument requires a gradient.  The backward passes are calls of their own
-(``mx4_linear_backward``, the gradient that ``distill_loss`` returns).
+(``mx4_linear_backward``, ``fp8_linear_backward``, the gradients that the
+losses return).
 
 This module only marshals torch tensors into the C ABI of ``libmuon.so``
 (``include/muon.h``); PyTorch provides device memory and streams.  Every
@@ -30,13 +34,15 @@ from typing import Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
-from ._lib import (KERNEL_CLASS_NAMES, MO_BF16, MO_F32, MO_MAX_TOP, MoMatrix, MoMx4Image,  # noqa: F401
-                   MoMx4Item, MoTensor, MuonError, check, last_error, lib)
+from ._lib import (KERNEL_CLASS_NAMES, MO_BF16, MO_F32, MO_MAX_TOP, MoFp8Image,  # noqa: F401
+                   MoFp8Item, MoMatrix, MoMx4Image, MoMx4Item, MoTensor, MuonError, check, last_error, lib)
 
 __all__ = ["muon_step", "adamw_step", "newton_schulz", "muon_workspace_size",
            "newton_schulz_workspace_size", "svd_entropy", "svd_entropy_workspace_size",
            "Mx4Matrix", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear",
-           "mx4_linear_backward", "TokenLogprobs", "token_logprobs", "distill_loss",
+           "mx4_linear_backward", "Fp8Matrix", "fp8_quantize", "fp8_dequantize", "fp8_matmul",
+           "fp8_linear", "fp8_linear_backward", "linear_cross_entropy", "BalanceLoss", "balance_loss",
+           "TokenLogprobs", "token_logprobs", "distill_loss",
            "MuonPlan", "MuonAdamW", "profile_enable", "profile_read", "profile_reset",
            "MuonError", "KERNEL_CLASS_NAMES"]
 
@@ -646,6 +652,192 @@ def mx4_linear_backward(dy: torch.Tensor, x_t: Mx4Matrix, w_t: Mx4Matrix, *,
     return dx if dy.dim() == 2 else dx.view(*dy.shape[:-1], w_t.rows), dw
 
 
+# ---------------------------------------------------------------- 8-bit matrices
+class Fp8Matrix:
+    """The 8-bit image of a [rows, cols] matrix with a scale per block of 128:
+    ``codes`` uint8 [rows, 128 nb] (e4m3) and ``scales`` uint8 [rows, 16 ceil(nb
+    / 16)] with nb = ceil(cols / 128) blocks per row, as ``include/muon.h`` lays
+    them out.  Rows or columns may be none."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        if codes.dim() != 2:
+            raise ValueError("codes must be 2-D")
+        rows, nb = int(codes.shape[0]), -(-int(cols) // 128)
+        if cols < 0:
+            raise ValueError("cols must not be negative")
+        for t, w, what in ((codes, 128 * nb, "codes"), (scales, -(-nb // 16) * 16, "scales")):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (rows, w) or not t.is_contiguous():
+                raise ValueError(f"{what} of a [{rows}, {cols}] image must be contiguous uint8 "
+                                 f"[{rows}, {w}], got {t.dtype} {tuple(t.shape)}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must share a device")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, int(cols)
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.rows, self.cols
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "Fp8Matrix":
+        """An image whose contents are still to be written."""
+        if rows < 0 or cols < 0:
+            raise ValueError(f"rows and columns must not be negative, got [{rows}, {cols}]")
+        nb = -(-cols // 128)
+        q = object.__new__(cls)                 # right by construction: no checks
+        q.codes = torch.empty((rows, 128 * nb), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, -(-nb // 16) * 16), dtype=torch.uint8, device=device)
+        q.rows, q.cols = rows, cols
+        return q
+
+    def _struct(self) -> MoFp8Image:
+        return MoFp8Image(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+
+    def __repr__(self) -> str:
+        return f"Fp8Matrix([{self.rows}, {self.cols}], device={self.device})"
+
+
+def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str = "rows",
+                 square: bool = False, out=None, stream=None):
+    """8-bit images of a 2-D matrix or of a list of them (``mo_fp8_quantize``;
+    fp32 or bf16, one dtype; rows may be strided).
+
+    ``images``: "rows" -- the image of x (blocks of 128 along its rows); "cols"
+    -- the image of x^T (blocks along x's columns); "both" -- the pair of them,
+    from one reading of x.  ``square``: one scale for 128 x 128 elements, so
+    that both images hold the same values -- for weights.  A list gives a list.
+    ``out``: images of an earlier call (same form) to overwrite.
+    """
+    if images not in _IMAGES:
+        raise ValueError(f"images must be one of {_IMAGES}")
+    single = isinstance(x, torch.Tensor)
+    xs = [x] if single else list(x)
+    if not xs:
+        return []
+    outs = None if out is None else ([out] if single else list(out))
+    if outs is not None and len(outs) != len(xs):
+        raise ValueError(f"out has {len(outs)} entries for {len(xs)} matrices")
+    dt = _dtype_code(_common_dtype(xs, "x"), "x")
+    dev = xs[0].device
+    views = [_rows_of(t, "x") for t in xs]
+    given = []                                   # (image, transposed image) of each matrix
+    if outs is not None:
+        for (_, r, c, _), o in zip(views, outs):
+            pair = tuple(o) if images == "both" else (o, None) if images == "rows" else (None, o)
+            if len(pair) != 2:
+                raise ValueError('out must hold pairs for images="both"')
+            for q, shape in zip(pair, ((r, c), (c, r))):
+                if q is not None and not isinstance(q, Fp8Matrix):
+                    raise TypeError("out must hold Fp8Matrix")
+                if q is not None and q.shape != shape:
+                    raise ValueError(f"out: expected an image of {shape}, got {q.shape}")
+            if (images != "cols" and pair[0] is None) or (images != "rows" and pair[1] is None):
+                raise ValueError("out lacks an image")
+            given.append(pair)
+    used = xs + [t for p in given for q in p if q is not None for t in (q.codes, q.scales)]
+    with _launch_on(dev, stream, used) as handle:
+        if outs is None:
+            given = [(Fp8Matrix.empty(r, c, dev) if images != "cols" else None,
+                      Fp8Matrix.empty(c, r, dev) if images != "rows" else None) for _, r, c, _ in views]
+        arr = (MoFp8Item * len(xs))()
+        for it, (ptr, r, c, ld), (q, qt) in zip(arr, views, given):
+            it.src, it.rows, it.cols, it.ld = ptr, r, c, ld
+            if q is not None:
+                it.codes, it.scales = q.codes.data_ptr(), q.scales.data_ptr()
+            if qt is not None:
+                it.codes_t, it.scales_t = qt.codes.data_ptr(), qt.scales.data_ptr()
+        check(lib().mo_fp8_quantize(arr, len(xs), dt, int(square), handle))
+    res = [p if images == "both" else p[0] if images == "rows" else p[1] for p in given]
+    return res[0] if single else res
+
+
+def fp8_dequantize(q: Union[Fp8Matrix, Sequence[Fp8Matrix]], *, dtype: torch.dtype = torch.bfloat16,
+                   stream=None):
+    """The values that an image, or each of a list, stands for (``mo_fp8_dequantize``)."""
+    single = isinstance(q, Fp8Matrix)
+    qs = [q] if single else list(q)
+    dt = _dtype_code(dtype, "dtype")
+    if not qs:
+        return []
+    dev = qs[0].device
+    with _launch_on(dev, stream, [t for i in qs for t in (i.codes, i.scales)]) as handle:
+        res = [torch.empty(i.shape, dtype=dtype, device=dev) for i in qs]
+        arr = (MoFp8Image * len(qs))(*[i._struct() for i in qs])
+        ptrs = (ctypes.c_void_p * len(qs))(*[t.data_ptr() for t in res])
+        check(lib().mo_fp8_dequantize(arr, ptrs, len(qs), dt, handle))
+    return res[0] if single else res
+
+
+def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """``a b^T`` over the values of two images with equal columns
+    (``mo_fp8_matmul``): a [M, K], b [N, K] give [M, N], fp32 sums rounded
+    once.  ``out``: written instead of a new tensor (its dtype counts, rows
+    may be strided); with ``accumulate`` the product is added to it."""
+    if not isinstance(a, Fp8Matrix) or not isinstance(b, Fp8Matrix):
+        raise TypeError("a and b must be Fp8Matrix")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    dt = _dtype_code(out_dtype if out is None else out.dtype, "out")
+    used = [a.codes, a.scales, b.codes, b.scales, out]
+    with _launch_on(a.device, stream, used) as handle:
+        if out is None:
+            out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.device)
+        ptr, r, c, ld = _rows_of(out, "out")
+        if (r, c) != (a.rows, b.rows):
+            raise ValueError(f"out must be [{a.rows}, {b.rows}], got [{r}, {c}]")
+        sa, sb = a._struct(), b._struct()
+        check(lib().mo_fp8_matmul(ctypes.byref(sa), ctypes.byref(sb), ptr, dt, ld, int(accumulate), handle))
+    return out
+
+
+def fp8_linear(x: torch.Tensor, w: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
+               save: bool = False, stream=None):
+    """``y = x W^T`` with W [N, K] held in 8 bits and x [..., K] (fp32 or
+    bf16) quantised on the way, a scale per 128 of a row.  ``save=True`` also
+    returns the image of x^T that :func:`fp8_linear_backward` takes.  x may
+    have no tokens.  Not seen by autograd."""
+    x2 = _flat2(x)
+    if x2.shape[1] != w.cols:
+        raise ValueError(f"x has {x2.shape[1]} features, the weights {w.cols}")
+    if save:
+        xq, x_t = fp8_quantize(x2, images="both", stream=stream)
+    else:
+        xq = fp8_quantize(x2, stream=stream)
+    y = fp8_matmul(xq, w, out_dtype=out_dtype, stream=stream)
+    y = y if x.dim() == 2 else y.view(*x.shape[:-1], w.rows)
+    return (y, x_t) if save else y
+
+
+def fp8_linear_backward(dy: torch.Tensor, x_t: Fp8Matrix, w_t: Fp8Matrix, *,
+                        dx_dtype: torch.dtype = torch.bfloat16, dw: Optional[torch.Tensor] = None,
+                        accumulate: bool = False, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dW) of ``y = x W^T`` from dy [..., N] (fp32 or bf16), the image of
+    x^T [K, tokens] and the image of W^T [K, N]: dy is quantised along both of
+    its axes, dx = dy W contracts over N and dW = dy^T x over the tokens.  The
+    rounding of x and W passes gradients straight through.  dW is fp32 [N, K]
+    unless ``dw`` gives it; ``accumulate`` adds to ``dw``.  Without tokens dW
+    is zeros (or stays as it was)."""
+    d2 = _flat2(dy)
+    if d2.shape[0] != x_t.cols or d2.shape[1] != w_t.cols:
+        raise ValueError(f"dy is {tuple(d2.shape)}, the images want [{x_t.cols}, {w_t.cols}]")
+    if x_t.rows != w_t.rows:
+        raise ValueError(f"x has {x_t.rows} features, the weights {w_t.rows}")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    if dw is not None and tuple(dw.shape) != (w_t.cols, x_t.rows):
+        raise ValueError(f"dw must be [{w_t.cols}, {x_t.rows}], got {tuple(dw.shape)}")
+    dq, dq_t = fp8_quantize(d2, images="both", stream=stream)
+    dx = fp8_matmul(dq, w_t, out_dtype=dx_dtype, stream=stream)
+    dw = fp8_matmul(dq_t, x_t, out_dtype=torch.float32, out=dw, accumulate=accumulate, stream=stream)
+    return dx if dy.dim() == 2 else dx.view(*dy.shape[:-1], w_t.rows), dw
+
+
 # ------------------------------------------------- log probabilities, distillation
 class TokenLogprobs(NamedTuple):
     logprob: Optional[torch.Tensor]       # fp32 [rows], None without tokens
@@ -723,6 +915,124 @@ def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_logit: torch
     return loss, g
 
 
+# ------------------------------------------------- cross entropy, router balance
+_GRADS = (True, False, "x", "weight")
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
+                         grad_loss: Optional[torch.Tensor] = None, grad: Union[bool, str] = True,
+                         dw: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None):
+    """Cross entropy of the logits ``x weight^T``, which are never kept
+    (``mo_linear_ce``): (loss fp32 [rows], dx, dW).  x [..., hidden] and weight
+    [vocab, hidden] are fp32 or bf16 (rows may be strided) and are multiplied
+    in bf16; ``targets`` int64, one per row of x (negative: the row is skipped).
+
+    ``grad_loss`` fp32 [rows]: the gradient that reaches each row's loss (1
+    when None).  ``grad``: True for both gradients, "x" or "weight" for one,
+    False for the loss alone; what is not asked for is None.  dx has x's dtype
+    and shape, dW the weights' dtype unless ``dw`` [vocab, hidden] gives it;
+    ``accumulate`` adds to ``dw``.  Not seen by autograd: pass the gradients on
+    yourself."""
+    if grad not in _GRADS:
+        raise ValueError(f"grad must be one of {_GRADS}")
+    x2 = _flat2(x)
+    xp, rows, hidden, ldx = _rows_of(x2, "x")
+    wp, vocab, wh, ldw = _rows_of(weight, "weight")
+    if hidden != wh:
+        raise ValueError(f"x has {hidden} features, the weights {wh}")
+    x_dt, w_dt, dev = _dtype_code(x.dtype, "x"), _dtype_code(weight.dtype, "weight"), x.device
+    tp = _vector(targets.view(-1) if targets.is_contiguous() else targets, torch.int64, (rows,), "targets")
+    gp = _vector(grad_loss, torch.float32, (rows,), "grad_loss")
+    want_dx, want_dw = grad in (True, "x"), grad in (True, "weight")
+    if dw is not None and not want_dw:
+        raise ValueError(f"dw given with grad={grad!r}")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    if dw is not None and tuple(dw.shape) != (vocab, hidden):
+        raise ValueError(f"dw must be [{vocab}, {hidden}], got {tuple(dw.shape)}")
+    dw_dt = w_dt if dw is None else _dtype_code(dw.dtype, "dw")
+    need = _linear_ce_workspace(rows, hidden, vocab, x_dt, dw_dt, want_dx, want_dw)
+    with _launch_on(dev, stream, [x2, weight, targets, grad_loss, dw]) as handle:
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        dx = torch.empty(rows, hidden, dtype=x.dtype, device=dev) if want_dx else None
+        if want_dw and dw is None:
+            dw = torch.empty(vocab, hidden, dtype=weight.dtype, device=dev)
+        wgp, _, _, ld_dw = _rows_of(dw, "dw") if want_dw else (None, 0, 0, 0)
+        with _SCRATCH_LOCK:
+            ws = _scratch(need, handle, dev)
+            check(lib().mo_linear_ce(xp, x_dt, ldx, wp, w_dt, ldw, rows, hidden, vocab, tp, gp, loss.data_ptr(),
+                                     dx.data_ptr() if want_dx else None, hidden, wgp, dw_dt, ld_dw, int(accumulate),
+                                     ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                                     handle))
+    return loss, dx if dx is None or x.dim() == 2 else dx.view(x.shape), dw
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_ce_workspace(rows: int, hidden: int, vocab: int, x_dt: int, dw_dt: int, dx: bool, dw: bool) -> int:
+    need = ctypes.c_size_t()
+    check(lib().mo_linear_ce_workspace_size(rows, hidden, vocab, x_dt, dw_dt, int(dx), int(dw), ctypes.byref(need)))
+    return need.value
+
+
+class BalanceLoss(NamedTuple):
+    loss: torch.Tensor                    # fp32, no dimensions
+    counts: torch.Tensor                  # int64 [experts]
+    grad: Optional[torch.Tensor]          # [tokens, experts] in the logits' dtype, None with grad=False
+
+
+@functools.lru_cache(maxsize=1024)
+def _balance_workspace(tokens: int, experts: int) -> int:
+    need = ctypes.c_size_t()
+    check(lib().mo_balance_loss_workspace_size(tokens, experts, ctypes.byref(need)))
+    return need.value
+
+
+def balance_loss(logits: torch.Tensor, index: torch.Tensor, *, weight: float = 1.0,
+                 grad_loss: Optional[torch.Tensor] = None, grad: bool = True,
+                 out_grad: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> BalanceLoss:
+    """Balance loss of a router (``mo_balance_loss``): ``weight`` times the sum
+    over experts of f_e, their share of the choices times their number, and
+    P_e, the mean of softmax(logits)_e over the tokens that made a choice.
+    logits fp32 or bf16 [tokens, experts] (rows may be strided), ``index``
+    int64 [tokens, top]: the experts that each token chose (negative: none; a
+    token without any is skipped).  ``counts`` are the choices of each expert:
+    the rows that its layers will see.
+
+    ``grad_loss``: one fp32 value, the gradient that reaches the loss (1 when
+    None).  The gradient is for the logits, in their dtype; ``out_grad`` is
+    written instead of a new tensor, and with ``accumulate`` added to.  Not
+    seen by autograd: pass the gradient on yourself."""
+    ptr, tokens, experts, ld = _rows_of(logits, "logits")
+    dt, dev = _dtype_code(logits.dtype, "logits"), logits.device
+    if index.dim() != 2:
+        raise ValueError("index must be [tokens, top]")
+    top = int(index.shape[1])
+    ip = _vector(index, torch.int64, (tokens, top), "index")
+    if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
+        raise ValueError("grad_loss must be one float32 value")
+    if out_grad is not None:
+        if not grad:
+            raise ValueError("out_grad given with grad=False")
+        if out_grad.dtype != logits.dtype or tuple(out_grad.shape) != (tokens, experts):
+            raise ValueError(f"out_grad must be {logits.dtype} [{tokens}, {experts}]")
+    if accumulate and out_grad is None:
+        raise ValueError("accumulate needs out_grad")
+    need = _balance_workspace(tokens, experts)
+    with _launch_on(dev, stream, [logits, index, grad_loss, out_grad]) as handle:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        counts = torch.empty(experts, dtype=torch.int64, device=dev)
+        g = out_grad
+        if grad and g is None:
+            g = torch.empty(tokens, experts, dtype=logits.dtype, device=dev)
+        gp, _, _, ldg = _rows_of(g, "out_grad") if grad else (None, 0, 0, 0)
+        with _SCRATCH_LOCK:
+            ws = _scratch(need, handle, dev)
+            check(lib().mo_balance_loss(ptr, dt, tokens, experts, ld, ip, top, weight,
+                                        grad_loss.data_ptr() if grad_loss is not None else None, loss.data_ptr(),
+                                        counts.data_ptr(), gp, ldg, int(accumulate), ws.data_ptr(), ws.numel(), handle))
+    return BalanceLoss(loss, counts, g)
+
+
 def profile_enable(classes: Iterable[str] = ()) -> None:
     """Time every later launch of the named kernel classes with HIP events."""
     mask = 0
@@ -755,7 +1065,9 @@ class MuonAdamW:
     matrices in ``self.mx4`` (as :func:`mx4_quantize` gives them, in the
     matrices' order), rewritten in place behind every step, so that 4-bit
     layers always multiply the current weights.  ``refresh_mx4()`` makes them
-    before the first step, or after weights were loaded.
+    before the first step, or after weights were loaded.  ``fp8`` keeps 8-bit
+    images in ``self.fp8`` in the same way, with square scales
+    (``refresh_fp8()``).
     """
 
     def __init__(self, muon_params: Sequence[torch.Tensor],
@@ -763,9 +1075,11 @@ class MuonAdamW:
                  wd: float = 0.1, mu: float = 0.95, nesterov: bool = True,
                  ns_steps: int = 5, mom_dtype: torch.dtype = torch.bfloat16,
                  ns_dtype: torch.dtype = torch.bfloat16, betas=(0.9, 0.999),
-                 adam_eps: float = 1e-8, mx4: Optional[str] = None):
+                 adam_eps: float = 1e-8, mx4: Optional[str] = None, fp8: Optional[str] = None):
         if mx4 is not None and mx4 not in _IMAGES:
             raise ValueError(f"mx4 must be None or one of {_IMAGES}")
+        if fp8 is not None and fp8 not in _IMAGES:
+            raise ValueError(f"fp8 must be None or one of {_IMAGES}")
         self.muon_params: List[torch.Tensor] = list(muon_params)
         self.adamw_params: List[torch.Tensor] = list(adamw_params)
         for p in self.muon_params:
@@ -781,6 +1095,8 @@ class MuonAdamW:
         self.plans_created = 0
         self._mx4_images = mx4
         self.mx4: Optional[list] = None
+        self._fp8_images = fp8
+        self.fp8: Optional[list] = None
 
     def refresh_mx4(self) -> list:
         """Rewrite the 4-bit images from the matrices as they are now."""
@@ -788,6 +1104,14 @@ class MuonAdamW:
             raise RuntimeError('MuonAdamW was made without mx4="rows", "cols" or "both"')
         self.mx4 = mx4_quantize([p.detach() for p in self.muon_params], images=self._mx4_images, out=self.mx4)
         return self.mx4
+
+    def refresh_fp8(self) -> list:
+        """Rewrite the 8-bit images from the matrices as they are now."""
+        if self._fp8_images is None:
+            raise RuntimeError('MuonAdamW was made without fp8="rows", "cols" or "both"')
+        self.fp8 = fp8_quantize([p.detach() for p in self.muon_params], images=self._fp8_images, square=True,
+                                out=self.fp8)
+        return self.fp8
 
     def _grads(self, ps):
         gs = [p.grad for p in ps]
@@ -823,6 +1147,8 @@ class MuonAdamW:
             self._plan.release_grads()
             if self._mx4_images is not None:
                 self.refresh_mx4()
+            if self._fp8_images is not None:
+                self.refresh_fp8()
         if self.adamw_params:
             adamw_step(self.adamw_params, self._grads(self.adamw_params), self.exp_avg,
                        self.exp_avg_sq, lr=lr, step=self.t, wd=self.wd, beta1=self.betas[0],

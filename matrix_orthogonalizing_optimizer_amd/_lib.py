@@ -19,12 +19,14 @@ MO_SCALE_SHAPE, MO_SCALE_HIDDEN, MO_SCALE_UPDATE_NORM = 0, 1, 2
 (MO_K_MOMENTUM, MO_K_NORM, MO_K_GRAM, MO_K_POLY, MO_K_UPDATE, MO_K_APPLY,
  MO_K_APPLY_X0, MO_K_RMS, MO_K_ADAMW, MO_K_SVD_GRAM, MO_K_SVD_REDUCE,
  MO_K_SVD_COLUMN, MO_K_SVD_EIG, MO_K_SVD_PANEL, MO_K_MX4_QUANT, MO_K_MX4_DEQUANT,
- MO_K_MX4_MATMUL, MO_K_LOGPROBS, MO_K_DISTILL) = range(19)
+ MO_K_MX4_MATMUL, MO_K_LOGPROBS, MO_K_DISTILL, MO_K_FP8_QUANT, MO_K_FP8_DEQUANT,
+ MO_K_FP8_MATMUL, MO_K_LINEAR_CE, MO_K_BALANCE) = range(24)
 MO_MAX_TOP = 128
 KERNEL_CLASS_NAMES = ["momentum", "norm", "gram", "poly", "update", "apply",
                       "apply_x0", "rms", "adamw", "svd_gram", "svd_reduce",
                       "svd_column", "svd_eig", "svd_panel", "mx4_quant", "mx4_dequant",
-                      "mx4_matmul", "logprobs", "distill"]
+                      "mx4_matmul", "logprobs", "distill", "fp8_quant", "fp8_dequant",
+                      "fp8_matmul", "linear_ce", "balance"]
 
 STATUS_NAMES = {MO_OK: "MO_OK", MO_EINVAL: "MO_EINVAL",
                 MO_EUNSUPPORTED: "MO_EUNSUPPORTED",
@@ -50,6 +52,14 @@ class MoMx4Item(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("codes_t", ctypes.c_void_p), ("scales_t", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64)]
+
+
+class MoFp8Image(ctypes.Structure):
+    _fields_ = MoMx4Image._fields_
+
+
+class MoFp8Item(ctypes.Structure):
+    _fields_ = MoMx4Item._fields_
 
 
 class MuonError(RuntimeError):
@@ -106,6 +116,20 @@ _SIGS = {
                                      _P, _P, _c.c_int, _P, _P, _P, _c.c_size_t, _P]),
     "mo_distill_loss": (_c.c_int, [_P, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _P, _P, _c.c_int,
                                    _c.c_float, _P, _P, _P, _c.c_int64, _P, _c.c_size_t, _P]),
+    "mo_fp8_image_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.POINTER(_c.c_size_t),
+                                     _c.POINTER(_c.c_size_t)]),
+    "mo_fp8_quantize": (_c.c_int, [_c.POINTER(MoFp8Item), _c.c_int64, _c.c_int, _c.c_int, _P]),
+    "mo_fp8_dequantize": (_c.c_int, [_c.POINTER(MoFp8Image), _c.POINTER(_P), _c.c_int64, _c.c_int, _P]),
+    "mo_fp8_matmul": (_c.c_int, [_c.POINTER(MoFp8Image), _c.POINTER(MoFp8Image), _P, _c.c_int,
+                                 _c.c_int64, _c.c_int, _P]),
+    "mo_linear_ce_workspace_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int,
+                                               _c.c_int, _c.c_int, _c.POINTER(_c.c_size_t)]),
+    "mo_linear_ce": (_c.c_int, [_P, _c.c_int, _c.c_int64, _P, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64,
+                                _c.c_int64, _P, _P, _P, _P, _c.c_int64, _P, _c.c_int, _c.c_int64, _c.c_int,
+                                _P, _c.c_size_t, _P]),
+    "mo_balance_loss_workspace_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.POINTER(_c.c_size_t)]),
+    "mo_balance_loss": (_c.c_int, [_P, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _P, _c.c_int64,
+                                   _c.c_float, _P, _P, _P, _P, _c.c_int64, _c.c_int, _P, _c.c_size_t, _P]),
     "mo_profile_enable": (_c.c_int, [_c.c_uint]),
     "mo_profile_read": (_c.c_int, [_c.c_int, _c.POINTER(_c.c_int64), _c.POINTER(_c.c_double),
                                    _c.POINTER(_c.c_double)]),

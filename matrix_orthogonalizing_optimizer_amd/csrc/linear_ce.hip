@@ -1,0 +1,498 @@
+// Cross entropy of logits z = x W^T that are never kept, with the gradients for
+// x and W (gfx950).
+//
+//   loss_t = log sum_v exp z_tv - z_{t, target}
+//   dz_tv = g_t (exp(z_tv - log sum exp z_t) - [v = target]),  dx = dz W,  dW = dz^T x
+//
+// The products run on the matrix cores in bf16 with fp32 sums, in pieces of the
+// vocabulary.  A first product's tiles leave only each row's largest logit and
+// sum of exponentials per wave of columns; a second one, with the row's
+// statistics known, turns its sums into dz, which two further products contract
+// with the piece's weights and with x while it is the only piece that exists.
+#include <algorithm>
+#include <cmath>
+
+#include "linear_ce_internal.h"
+#include "mo_internal.h"
+#include "tile_product.h"
+
+namespace mo {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// dz enters its products as a sum of bf16 terms: one where the gradient is
+// bf16 itself (its rounding, 2^-9 of a value, is of the size of the result's
+// own), three where it is fp32 (2^-26: x and W are exact in bf16, so that the
+// fp32 sums are the only other error).
+constexpr int terms_of(int dt) { return dt == F32 ? 3 : 1; }
+
+// LDS that only one wave uses: the hardware keeps the wave's accesses in order,
+// and the compiler keeps them so here.
+__device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
+
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+// ------------------------------------------------------------ rows and packing
+// Per row: its factor in dz, relative to the largest |g| (so that equal g do
+// not add a rounding of their own to dz's): 0 for a row that takes no part, NaN
+// for a target that is no column.  scale[0] is that largest |g|, or 1.
+__global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, const float* g, int rows, int vocab, float* factor, float* scale) {
+  __shared__ float most[16];
+  float m = 0.0f;
+  if (g)
+    for (int t = threadIdx.x; t < rows; t += 1024)
+      if (targets[t] >= 0) m = fmaxf(m, fabsf(g[t]));       // NaN is left out
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = most[0];
+  for (int i = 1; i < 16; ++i) m = fmaxf(m, most[i]);
+  const float s = m > 0.0f && m < INFINITY ? m : 1.0f;
+  if (threadIdx.x == 0) *scale = s;
+  for (int t = threadIdx.x; t < rows; t += 1024) {
+    const int64_t y = targets[t];
+    const float r = g ? g[t] : 1.0f;
+    factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= vocab ? NAN : r / s;
+  }
+}
+
+// bf16 copies of a [rows, cols] matrix: dst [rows][pitch] (columns past `cols`
+// zero) and its transpose dst_t [cols][pitch_t] (rows past `rows` zero, and
+// those whose factor is 0, so that whatever they hold takes no part).  Tiles of
+// 64 x 64 through LDS.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
+                                                      uint16_t* dst_t, int64_t pitch_t, const float* factor) {
+  __shared__ uint16_t tile[64][66];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
+  const int cl = (threadIdx.x & 15) * 4, rl = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + rl + 16 * i;
+    float v[4] = {};
+    if (r < rows) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + cl + k < cols) v[k] = to_f(src[r * ld + c0 + cl + k]);
+    }
+    const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+    if (dst && r < rows && c0 + cl < pitch) *reinterpret_cast<uint2*>(dst + r * pitch + c0 + cl) = make_uint2(lo, hi);
+    const bool out = factor && r < rows && factor[r] == 0.0f;
+    tile[rl + 16 * i][cl] = out ? 0 : static_cast<uint16_t>(lo);
+    tile[rl + 16 * i][cl + 1] = out ? 0 : static_cast<uint16_t>(lo >> 16);
+    tile[rl + 16 * i][cl + 2] = out ? 0 : static_cast<uint16_t>(hi);
+    tile[rl + 16 * i][cl + 3] = out ? 0 : static_cast<uint16_t>(hi >> 16);
+  }
+  if (!dst_t) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t c = c0 + rl + 16 * i, r = r0 + cl;
+    if (c >= cols || r >= pitch_t) continue;
+    const uint32_t lo = tile[cl][rl + 16 * i] | static_cast<uint32_t>(tile[cl + 1][rl + 16 * i]) << 16;
+    const uint32_t hi = tile[cl + 2][rl + 16 * i] | static_cast<uint32_t>(tile[cl + 3][rl + 16 * i]) << 16;
+    *reinterpret_cast<uint2*>(dst_t + c * pitch_t + r) = make_uint2(lo, hi);
+  }
+}
+
+hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch, uint16_t* dst_t, int64_t pitch_t,
+                const float* factor, hipStream_t s) {
+  const dim3 g(static_cast<uint32_t>((cols + 63) / 64), static_cast<uint32_t>((rows + 63) / 64));
+  if (dt == F32) ce_pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
+  else ce_pack_kernel<__bf16><<<g, 256, 0, s>>>(static_cast<const __bf16*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ statistics
+struct CeStatsArgs {
+  const int64_t* targets;
+  int64_t col0;                 // the piece's first column
+  float2* part;                 // [rows][tiles_n WN]: largest logit, sum of exp(z - it)
+  float* target_logit;          // written by the tile that holds the row's target
+};
+
+template <class C>
+__device__ __forceinline__ float col_mask(const TilePlace& q, int j, int g, int k, float v) {
+  const int c = q.wn * (C::TN / C::WN) + 32 * j + 8 * g + 4 * q.half + k;
+  return c <= q.nlast ? v : -INFINITY;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads) ce_stats_kernel(const ProductArgs p, const CeStatsArgs e) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
+  const TilePlace q = tile_place<C>(p);
+  f32x16v acc[C::FM][C::FN];
+  tile_sums<C>(p, q, smem, acc);
+  const bool edge = (q.wn + 1) * (C::TN / C::WN) > q.nlast + 1;
+  const int64_t cols = static_cast<int64_t>(p.tiles_n) * C::WN, col = static_cast<int64_t>(q.tn) * C::WN + q.wn;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    if (edge) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = col_mask<C>(q, j, r / 4, r % 4, acc[i][j][r]);
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
+    m = fmaxf(m, __uint_as_float(lane_xor32(__float_as_uint(m))));
+    const float ref = m == -INFINITY ? 0.0f : m;            // columns of -inf alone: a sum of zero
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * kLog2e);
+    s += __uint_as_float(lane_xor32(__float_as_uint(s)));
+    const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
+    const bool in = row <= q.mlast;
+    const int64_t t = q.m0 + row;
+    if (in && q.half == 0) e.part[t * cols + col] = make_float2(m, s);
+    // the target's logit, where these columns hold it
+    const int64_t y = in ? e.targets[t] - e.col0 - q.n0 - q.wn * (C::TN / C::WN) : -1;
+    const bool mine = y >= 0 && y < C::TN / C::WN && ((y >> 2) & 1) == q.half && y + q.wn * (C::TN / C::WN) <= q.nlast;
+    if (__any(mine)) {
+      float z = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (y == 32 * j + 8 * (r / 4) + 4 * q.half + r % 4) z = acc[i][j][r];
+      if (mine) e.target_logit[t] = z;
+    }
+  }
+}
+
+// Joins a piece's statistics with those of the pieces before it, a wave per
+// row; after the last piece the row's {m, 1 / sum} and its loss.
+__global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int64_t cols, int rows, int vocab, int first, int last,
+                                                      const int64_t* targets, const float* target_logit, float2* stat, float* loss) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= rows) return;
+  float m = -INFINITY, s = 0.0f;
+  auto add = [&](float m2, float s2) __attribute__((always_inline)) {
+    const float n = fmaxf(m, m2), ref = n == -INFINITY ? 0.0f : n;
+    s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - ref) * kLog2e);
+    m = n;
+  };
+  for (int64_t c = lane; c < cols; c += 64) {
+    const float2 v = part[t * cols + c];
+    add(v.x, v.y);
+  }
+  for (int o = 1; o < 64; o <<= 1) {
+    const float m2 = __shfl_xor(m, o, 64), s2 = __shfl_xor(s, o, 64);
+    const float a = m, b = s;
+    // both lanes of a pair add in the same order
+    const bool low = (lane & o) == 0;
+    m = low ? a : m2;
+    s = low ? b : s2;
+    add(low ? m2 : a, low ? s2 : b);
+  }
+  if (!first) {
+    const float2 v = stat[t];
+    const float a = m, b = s;
+    m = v.x;
+    s = v.y;
+    add(a, b);
+  }
+  if (lane) return;
+  if (!last) {
+    stat[t] = make_float2(m, s);
+    return;
+  }
+  // -inf alone, or a NaN or +inf anywhere, gives NaN
+  const bool none = m == -INFINITY;
+  stat[t] = make_float2(m, none ? NAN : 1.0f / s);
+  const int64_t y = targets[t];
+  loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + (m - target_logit[t]);
+}
+
+// ------------------------------------------------------------ dz
+struct CeGradArgs {
+  const int64_t* targets;
+  int64_t col0;
+  const float2* stat;
+  const float* factor;
+  uint16_t* dz;                 // [rows][terms_x][vp], or null
+  uint16_t* dz_t;               // [columns][terms_w][tp], or null
+  int terms_x, terms_w;
+  int vp, tp;                   // the piece's columns and the rows, padded (zeros)
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads) ce_grad_kernel(const ProductArgs p, const CeGradArgs e) {
+  constexpr int W = C::TN / C::WN, kPitch = C::kTurnPitch, kLanes = W / 4;
+  // columns of 32 rows' bf16, with padding against bank conflicts
+  constexpr int kPitchT = 80;
+  static_assert(W * kPitchT <= 32 * kPitch, "the wave's place holds the transpose too");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
+  const TilePlace q = tile_place<C>(p);
+  f32x16v acc[C::FM][C::FN];
+  tile_sums<C>(p, q, smem, acc);
+  uint8_t* turn = smem + (q.wm * C::WN + q.wn) * 32 * kPitch;
+  const bool edge = (q.wn + 1) * W > q.nlast + 1;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
+    const bool in = row <= q.mlast;
+    const int64_t t = q.m0 + (in ? row : 0);
+    const float f = in ? e.factor[t] : 0.0f;
+    const float2 st = e.stat[t];
+    const int64_t y = e.targets[t] - e.col0 - q.n0 - q.wn * W;
+    const int hot = y >= 0 && y < W ? static_cast<int>(y) : -1;
+    const float inv = f == 0.0f ? 0.0f : st.y;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
+        float v = __builtin_amdgcn_exp2f((acc[i][j][r] - st.x) * kLog2e) * inv;
+        v = f * (c == hot ? v - 1.0f : v);
+        if (f == 0.0f || (edge && q.wn * W + c > q.nlast)) v = 0.0f;
+        acc[i][j][r] = v;
+      }
+    for (int term = 0; term < max(e.terms_x, e.terms_w); ++term) {
+      // bf16 terms, largest first: what is left goes to the next
+      if (e.dz && term < e.terms_x) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4v*>(turn + q.r32 * kPitch + (32 * j + 8 * g + 4 * q.half) * 4) =
+                f32x4v{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        wave_order();
+#pragma unroll
+        for (int k = 0; k < 32 * kLanes / 64; ++k) {
+          const int lr = k * (64 / kLanes) + q.lane / kLanes, lc = q.lane % kLanes * 4;
+          const f32x4v v = *reinterpret_cast<const f32x4v*>(turn + lr * kPitch + lc * 4);
+          const int64_t rr = q.wm * (C::TM / C::WM) + 32 * i + lr, cc = q.n0 + q.wn * W + lc;
+          if (rr <= q.mlast && cc < e.vp)
+            *reinterpret_cast<uint2*>(e.dz + ((q.m0 + rr) * e.terms_x + term) * e.vp + cc) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+        wave_order();
+      }
+      if (e.dz_t && term < e.terms_w) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
+            *reinterpret_cast<uint16_t*>(turn + c * kPitchT + q.r32 * 2) = static_cast<uint16_t>(pack_bf16x2(acc[i][j][r], acc[i][j][r]));
+          }
+        wave_order();
+#pragma unroll
+        for (int k = 0; k < W * 4 / 64; ++k) {
+          const int c = k * 16 + q.lane / 4, ch = q.lane % 4;
+          const u32x4v v = *reinterpret_cast<const u32x4v*>(turn + c * kPitchT + ch * 16);
+          const int64_t cc = q.wn * W + c, rr = q.m0 + q.wm * (C::TM / C::WM) + 32 * i + ch * 8;
+          if (cc <= q.nlast && rr < e.tp)
+            *reinterpret_cast<u32x4v*>(e.dz_t + ((q.n0 + cc) * e.terms_w + term) * e.tp + rr) = v;
+        }
+        wave_order();
+      }
+      if (term + 1 < max(e.terms_x, e.terms_w)) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] -= bf2f(static_cast<uint16_t>(pack_bf16x2(acc[i][j][r], acc[i][j][r])));
+      }
+    }
+  }
+}
+
+// dx = scale times the sum of the splits' parts, 0 in rows that take no part.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t n, int rows, int hidden, const float* scale,
+                                                        const float* factor, T* dx, int64_t ld) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (u >= n) return;
+  const int64_t t = u / hidden, c = u - t * hidden;
+  float v = 0.0f;
+  for (int s = 0; s < splits; ++s) v += part[s * n + u];
+  dx[t * ld + c] = static_cast<T>(factor[t] == 0.0f ? 0.0f : v * *scale);
+}
+
+// ------------------------------------------------------------ the plan
+// Pieces of the vocabulary, and the places of everything in the workspace.
+struct Plan {
+  int64_t hp, tp;              // hidden size and rows, padded to whole pairs of stages
+  int64_t vf, vb;              // columns of a forward and of a backward piece
+  int splits;                  // of the product for dx
+  int terms_x, terms_w;
+  size_t part, stat, zt, factor, scale, x, w, x_t, w_t, dz, dz_t, dxp, total;
+};
+
+// Pieces of at most `most` columns, of about equal length, in whole tiles.
+int64_t piece_of(int64_t vocab, int64_t most) {
+  const int64_t n = (vocab + most - 1) / most;
+  return std::min(up((vocab + n - 1) / n, 256), up(vocab, 256));
+}
+
+typedef TileCfgT<OpBf16, 64, 64, 2, 2> CfgSmall;
+
+Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt, bool dx, bool dw) {
+  Plan p{};
+  p.hp = up(hidden, 64);
+  p.tp = up(rows, 64);
+  p.terms_x = terms_of(x_dt);
+  p.terms_w = terms_of(dw_dt);
+  // dz and its transpose stay near 2^26 elements each and a piece's weights
+  // within 2^27
+  const int64_t fit = std::min((int64_t{1} << 26) / std::max<int64_t>(rows, 1), (int64_t{1} << 27) / p.hp);
+  p.vb = piece_of(vocab, std::min(std::max(fit / 256 * 256, int64_t{1024}), int64_t{1} << 20));
+  p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
+  const int64_t tiles = ((rows + 63) / 64) * ((hidden + 63) / 64);
+  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), p.vb / 256)));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t t = static_cast<size_t>(rows);
+  p.part = take(t * static_cast<size_t>(up(std::max(p.vf, p.vb), 256) / 32) * 8);
+  p.stat = take(t * 8);
+  p.zt = take(t * 4);
+  p.factor = take(t * 4);
+  p.scale = take(4);
+  p.x = take(t * p.hp * 2);
+  p.w = take(static_cast<size_t>(p.vb) * p.hp * 2);
+  if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.tp * 2);
+  if (dx) p.w_t = take(static_cast<size_t>(hidden) * p.vb * 2);
+  if (dx) p.dz = take(t * p.vb * 2 * p.terms_x);
+  if (dw) p.dz_t = take(static_cast<size_t>(p.vb) * p.tp * 2 * p.terms_w);
+  if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * hidden * 4);
+  p.total = rows ? at : 0;
+  return p;
+}
+
+template <class C>
+dim3 tiles_of(ProductArgs& p) {
+  p.tiles_m = (p.m + C::TM - 1) / C::TM;
+  p.tiles_n = (p.n + C::TN - 1) / C::TN;
+  return dim3(static_cast<uint32_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n), 1u);
+}
+
+}  // namespace
+
+size_t linear_ce_workspace(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt, bool dx, bool dw) {
+  return make_plan(rows, hidden, vocab, x_dt, dw_dt, dx, dw).total;
+}
+
+#define MO_TRY(e)                          \
+  do {                                     \
+    const hipError_t err_ = (e);           \
+    if (err_ != hipSuccess) return err_;   \
+  } while (0)
+
+hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
+  if (a.rows == 0)                   // accumulating calls and those without dw do not come here
+    return a.dw_dt == F32 ? run_product_zero(static_cast<float*>(a.dw), a.ld_dw, a.vocab, a.hidden, s)
+                          : run_product_zero(static_cast<__bf16*>(a.dw), a.ld_dw, a.vocab, a.hidden, s);
+  const bool want_dx = a.dx != nullptr, want_dw = a.dw != nullptr, grad = want_dx || want_dw;
+  const Plan pl = make_plan(a.rows, a.hidden, a.vocab, a.x_dt, a.dw_dt, want_dx, want_dw);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  float2* part = reinterpret_cast<float2*>(base + pl.part);
+  float2* stat = reinterpret_cast<float2*>(base + pl.stat);
+  float* zt = reinterpret_cast<float*>(base + pl.zt);
+  float* factor = reinterpret_cast<float*>(base + pl.factor);
+  float* scale = reinterpret_cast<float*>(base + pl.scale);
+  uint16_t* xb = reinterpret_cast<uint16_t*>(base + pl.x);
+  uint16_t* wb = reinterpret_cast<uint16_t*>(base + pl.w);
+  uint16_t* x_t = want_dw ? reinterpret_cast<uint16_t*>(base + pl.x_t) : nullptr;
+  uint16_t* w_t = want_dx ? reinterpret_cast<uint16_t*>(base + pl.w_t) : nullptr;
+  uint16_t* dz = want_dx ? reinterpret_cast<uint16_t*>(base + pl.dz) : nullptr;
+  uint16_t* dz_t = want_dw ? reinterpret_cast<uint16_t*>(base + pl.dz_t) : nullptr;
+  float* dxp = want_dx ? reinterpret_cast<float*>(base + pl.dxp) : nullptr;
+
+  // operands that the products can read in place
+  auto plain = [&](const void* q, int dt, int64_t ld) {
+    return dt == BF16 && a.hidden % 64 == 0 && ld % 8 == 0 && ld <= kCeMaxHidden && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+  };
+  const bool plain_x = plain(a.x, a.x_dt, a.ldx), plain_w = plain(a.w, a.w_dt, a.ldw);
+  const int esz_w = a.w_dt == F32 ? 4 : 2, esz_dw = a.dw_dt == F32 ? 4 : 2;
+
+  if (grad) ce_rows_kernel<<<1, 1024, 0, s>>>(a.targets, a.grad_loss, a.rows, a.vocab, factor, scale);
+  MO_TRY(hipGetLastError());
+  if (!plain_x || want_dw) MO_TRY(pack(a.x_dt, a.x, a.ldx, a.rows, a.hidden, plain_x ? nullptr : xb, pl.hp, x_t, pl.tp, factor, s));
+
+  ProductArgs logits{};
+  logits.a = static_cast<const uint8_t*>(plain_x ? a.x : xb);
+  logits.pitch_a = static_cast<uint32_t>((plain_x ? a.ldx : pl.hp) * 2);
+  logits.pitch_b = static_cast<uint32_t>((plain_w ? a.ldw : pl.hp) * 2);
+  logits.m = a.rows;
+  logits.stages = logits.stages_b = static_cast<int>(pl.hp / 32);
+  logits.splits = 1;
+  typedef CfgSmall C;
+
+  auto weights = [&](int64_t v0) { return static_cast<const uint8_t*>(a.w) + v0 * a.ldw * esz_w; };
+  const int64_t vf = plain_w ? pl.vf : pl.vb;
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += vf) {
+    const int v = static_cast<int>(std::min<int64_t>(vf, a.vocab - v0));
+    if (!plain_w) MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, wb, pl.hp, nullptr, 0, nullptr, s));
+    logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
+    logits.n = v;
+    const dim3 g = tiles_of<C>(logits);
+    ce_stats_kernel<C><<<g, C::kThreads, 0, s>>>(logits, {a.targets, v0, part, zt});
+    MO_TRY(hipGetLastError());
+    ce_join_kernel<<<(a.rows + 3) / 4, 256, 0, s>>>(part, static_cast<int64_t>(logits.tiles_n) * C::WN, a.rows, a.vocab, v0 == 0,
+                                                    v0 + v >= a.vocab, a.targets, zt, stat, a.loss);
+    MO_TRY(hipGetLastError());
+  }
+  if (!grad) return hipSuccess;
+
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += pl.vb) {
+    const int v = static_cast<int>(std::min<int64_t>(pl.vb, a.vocab - v0));
+    const int64_t vp = up(v, 64);
+    if (!plain_w || want_dx) MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb, pl.hp, w_t, vp, nullptr, s));
+    logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
+    logits.n = v;
+    const dim3 g = tiles_of<C>(logits);
+    ce_grad_kernel<C><<<g, C::kThreads, 0, s>>>(logits, {a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp),
+                                                        static_cast<int>(pl.tp)});
+    MO_TRY(hipGetLastError());
+    if (want_dx) {
+      ProductArgs p{};
+      p.a = reinterpret_cast<const uint8_t*>(dz);
+      p.b = reinterpret_cast<const uint8_t*>(w_t);
+      p.pitch_a = static_cast<uint32_t>(vp * 2 * pl.terms_x);
+      p.pitch_b = static_cast<uint32_t>(vp * 2);
+      p.m = a.rows;
+      p.n = a.hidden;
+      p.stages_b = static_cast<int>(vp / 32);
+      p.stages = p.stages_b * pl.terms_x;
+      p.splits = pl.splits;
+      MO_TRY((run_product_store<C, float>(p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0, nullptr}, s)));
+    }
+    if (want_dw) {
+      ProductArgs p{};
+      p.a = reinterpret_cast<const uint8_t*>(dz_t);
+      p.b = reinterpret_cast<const uint8_t*>(x_t);
+      p.pitch_a = static_cast<uint32_t>(pl.tp * 2 * pl.terms_w);
+      p.pitch_b = static_cast<uint32_t>(pl.tp * 2);
+      p.m = v;
+      p.n = a.hidden;
+      p.stages_b = static_cast<int>(pl.tp / 32);
+      p.stages = p.stages_b * pl.terms_w;
+      p.splits = 1;
+      uint8_t* out = static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * esz_dw;
+      if (a.dw_dt == F32) MO_TRY((run_product_store<C, float>(p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+      else MO_TRY((run_product_store<C, __bf16>(p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+    }
+  }
+  if (want_dx) {
+    const int64_t n = static_cast<int64_t>(a.rows) * a.hidden;
+    const uint32_t g = static_cast<uint32_t>((n + 255) / 256);
+    if (a.x_dt == F32) ce_finish_kernel<float><<<g, 256, 0, s>>>(dxp, pl.splits, n, a.rows, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
+    else ce_finish_kernel<__bf16><<<g, 256, 0, s>>>(dxp, pl.splits, n, a.rows, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
+    MO_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+}  // namespace mo

@@ -5,9 +5,9 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
-#include <exception>
 #include <vector>
 
+#include "checks.h"
 #include "mo_host.h"
 #include "mo_internal.h"
 #include "muon.h"
@@ -16,8 +16,6 @@
 namespace {
 
 using namespace mo;
-
-long long ll(int64_t x) { return static_cast<long long>(x); }
 
 int check_shape(int64_t rows, int64_t cols, const char* what, int64_t i) {
   if (rows < 1 || cols < 1 || rows > INT32_MAX || cols > INT32_MAX || rows > (int64_t{1} << 40) / cols)
@@ -28,36 +26,6 @@ int check_shape(int64_t rows, int64_t cols, const char* what, int64_t i) {
 size_t code_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows * mx4_blocks(cols) * 16); }
 size_t scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows * mx4_scale_pitch(cols)); }
 
-// Bytes that a [rows, cols] view with rows `ld` elements apart touches.
-size_t view_bytes(int64_t rows, int64_t cols, int64_t ld, int esz) {
-  return (static_cast<size_t>(rows - 1) * static_cast<size_t>(ld) + static_cast<size_t>(cols)) * static_cast<size_t>(esz);
-}
-
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-  int64_t idx;
-  bool out;
-};
-
-void add_range(std::vector<Range>& v, const void* p, size_t n, int64_t idx, bool out) {
-  if (p && n) v.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + n, idx, out});
-}
-
-// No output may share a byte with any other range; inputs may share.
-int check_overlap(std::vector<Range>& v, const char* what) {
-  std::sort(v.begin(), v.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  uintptr_t end_any = 0, end_out = 0;   // furthest end of the ranges so far
-  for (const Range& r : v) {
-    if (r.lo < end_out || (r.out && r.lo < end_any))
-      return fail(MO_EINVAL, "%s %lld: an output overlaps another buffer of the call", what, ll(r.idx));
-    end_any = std::max(end_any, r.hi);
-    if (r.out) end_out = std::max(end_out, r.hi);
-  }
-  return MO_OK;
-}
-
 int check_image(const mo_mx4_image& x, const char* what, int64_t i) {
   if (int rc = check_shape(x.rows, x.cols, what, i)) return rc;
   if (!x.codes || !x.scales) return fail(MO_EINVAL, "%s %lld: codes and scales must be non-NULL", what, ll(i));
@@ -65,8 +33,6 @@ int check_image(const mo_mx4_image& x, const char* what, int64_t i) {
     return fail(MO_EINVAL, "%s %lld: codes must be 16-byte and scales 4-byte aligned", what, ll(i));
   return MO_OK;
 }
-
-int esz_of(int dt) { return dt == MO_F32 ? 4 : 2; }
 
 // Launches are limited by kMx4Group matrices and by a grid of fewer than
 // 2^32 threads.
@@ -217,16 +183,6 @@ int matmul(const mo_mx4_image* a, const mo_mx4_image* b, void* out, int out_dtyp
   g.accumulate = accumulate != 0;
   ProfScope ps(MO_K_MX4_MATMUL, s, 2.0 * static_cast<double>(a->rows) * b->rows * a->cols);
   return checked(launch_mx4_matmul(out_dtype, g, s), s, "mx4 matmul");
-}
-
-// No C++ exception may leave a C entry point.
-template <typename F>
-int guarded(F f) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    return fail(MO_EINVAL, "host memory: %s", e.what());
-  }
 }
 
 }  // namespace
