@@ -466,7 +466,8 @@ int mo_distill_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, 
  *
  * Quantisation: a = the block's largest |x|; e = the smallest integer with a
  * <= 448 2^e, at least -127 (byte 0 for a = 0); code = x 2^-e rounded to
- * nearest, halfway cases to even.  With square scales a is the largest of 128
+ * nearest, halfway cases to even (what would round to 2^128, beyond fp32, to
+ * 248 2^120).  With square scales a is the largest of 128
  * rows x 128 columns (rows 128 i .. 128 i + 127), so that the image of the
  * transpose holds the same values: the form for weights, whose gradients then
  * belong to the values that the forward pass multiplied.  A block that holds a

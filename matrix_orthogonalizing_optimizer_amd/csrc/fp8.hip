@@ -25,11 +25,15 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   return e > 8u ? e - 8u : 0u;
 }
 
+// The largest magnitude that does not round to 2^128 (under the largest scale,
+// 2^120, codes are steps of 8 here).
+__device__ __forceinline__ float clip(float x) { return __builtin_amdgcn_fmed3f(x, -0x1.fp127f, 0x1.fp127f); }
+
 // Four codes from four elements under the scale, element 0 lowest.
 __device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, float s) {
   i16x2v r = {0, 0};
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, s, false);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, s, true);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, clip(a), clip(b), s, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, clip(c), clip(d), s, true);
   return __builtin_bit_cast(uint32_t, r);
 }
 template <typename T>
@@ -321,8 +325,12 @@ hipError_t launch_fp8_matmul(int out_dt, const Fp8MatmulArgs& a, hipStream_t s) 
   p.n = a.n;
   p.stages = p.stages_b = 2 * a.nb;
   p.splits = 1;
-  typedef TileCfgT<OpFp8, 64, 64, 2, 2> C64;
-  return out_dt == F32 ? run<C64, float>(p, a, s) : run<C64, __bf16>(p, a, s);
+  if (a.m >= 1024 && a.n >= 1024) {
+    if (out_dt == F32) return run<TileCfgT<OpFp8Exact, 256, 256, 2, 4, 4>, float>(p, a, s);
+    return run<TileCfgT<OpFp8, 256, 256, 2, 2, 4>, __bf16>(p, a, s);
+  }
+  if (out_dt == F32) return run<TileCfgT<OpFp8Exact, 64, 64, 2, 2, 6>, float>(p, a, s);
+  return run<TileCfgT<OpFp8, 64, 64, 2, 2, 6>, __bf16>(p, a, s);
 }
 
 }  // namespace mo

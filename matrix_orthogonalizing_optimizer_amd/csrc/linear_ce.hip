@@ -120,7 +120,7 @@ __device__ __forceinline__ float col_mask(const TilePlace& q, int j, int g, int 
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads) ce_stats_kernel(const ProductArgs p, const CeStatsArgs e) {
+__global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(const ProductArgs p, const CeStatsArgs e) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
   const TilePlace q = tile_place<C>(p);
   f32x16v acc[C::FM][C::FN];
@@ -224,7 +224,7 @@ struct CeGradArgs {
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads) ce_grad_kernel(const ProductArgs p, const CeGradArgs e) {
+__global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(const ProductArgs p, const CeGradArgs e) {
   constexpr int W = C::TN / C::WN, kPitch = C::kTurnPitch, kLanes = W / 4;
   // columns of 32 rows' bf16, with padding against bank conflicts
   constexpr int kPitchT = 80;
@@ -333,7 +333,8 @@ int64_t piece_of(int64_t vocab, int64_t most) {
   return std::min(up((vocab + n - 1) / n, 256), up(vocab, 256));
 }
 
-typedef TileCfgT<OpBf16, 64, 64, 2, 2> CfgSmall;
+typedef TileCfgT<OpBf16, 64, 64, 2, 2, 6> CfgSmall;
+typedef TileCfgT<OpBf16, 256, 256, 2, 2, 4> CfgLarge;
 
 Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt, bool dx, bool dw) {
   Plan p{};
@@ -371,11 +372,34 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   return p;
 }
 
+// Whether the product fills the chip with tiles of 256.
+bool large(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 128; }
+
+template <typename T>
+hipError_t store(const ProductArgs& p, const StoreArgs<T>& e, hipStream_t s) {
+  return large(p.m, p.n) ? run_product_store<CfgLarge, T>(p, e, s) : run_product_store<CfgSmall, T>(p, e, s);
+}
+
 template <class C>
 dim3 tiles_of(ProductArgs& p) {
   p.tiles_m = (p.m + C::TM - 1) / C::TM;
   p.tiles_n = (p.n + C::TN - 1) / C::TN;
   return dim3(static_cast<uint32_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n), 1u);
+}
+
+template <class C>
+hipError_t run_stats(ProductArgs p, const CeStatsArgs& e, int64_t& cols, hipStream_t s) {
+  const dim3 g = tiles_of<C>(p);
+  cols = static_cast<int64_t>(p.tiles_n) * C::WN;
+  ce_stats_kernel<C><<<g, C::kThreads, 0, s>>>(p, e);
+  return hipGetLastError();
+}
+
+template <class C>
+hipError_t run_grad(ProductArgs p, const CeGradArgs& e, hipStream_t s) {
+  const dim3 g = tiles_of<C>(p);
+  ce_grad_kernel<C><<<g, C::kThreads, 0, s>>>(p, e);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -428,7 +452,6 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   logits.m = a.rows;
   logits.stages = logits.stages_b = static_cast<int>(pl.hp / 32);
   logits.splits = 1;
-  typedef CfgSmall C;
 
   auto weights = [&](int64_t v0) { return static_cast<const uint8_t*>(a.w) + v0 * a.ldw * esz_w; };
   const int64_t vf = plain_w ? pl.vf : pl.vb;
@@ -437,10 +460,11 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     if (!plain_w) MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, wb, pl.hp, nullptr, 0, nullptr, s));
     logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
     logits.n = v;
-    const dim3 g = tiles_of<C>(logits);
-    ce_stats_kernel<C><<<g, C::kThreads, 0, s>>>(logits, {a.targets, v0, part, zt});
-    MO_TRY(hipGetLastError());
-    ce_join_kernel<<<(a.rows + 3) / 4, 256, 0, s>>>(part, static_cast<int64_t>(logits.tiles_n) * C::WN, a.rows, a.vocab, v0 == 0,
+    const CeStatsArgs e{a.targets, v0, part, zt};
+    int64_t cols;
+    if (large(a.rows, v)) MO_TRY(run_stats<CfgLarge>(logits, e, cols, s));
+    else MO_TRY(run_stats<CfgSmall>(logits, e, cols, s));
+    ce_join_kernel<<<(a.rows + 3) / 4, 256, 0, s>>>(part, cols, a.rows, a.vocab, v0 == 0,
                                                     v0 + v >= a.vocab, a.targets, zt, stat, a.loss);
     MO_TRY(hipGetLastError());
   }
@@ -452,10 +476,8 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     if (!plain_w || want_dx) MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb, pl.hp, w_t, vp, nullptr, s));
     logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
     logits.n = v;
-    const dim3 g = tiles_of<C>(logits);
-    ce_grad_kernel<C><<<g, C::kThreads, 0, s>>>(logits, {a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp),
-                                                        static_cast<int>(pl.tp)});
-    MO_TRY(hipGetLastError());
+    const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp)};
+    MO_TRY(large(a.rows, v) ? run_grad<CfgLarge>(logits, e, s) : run_grad<CfgSmall>(logits, e, s));
     if (want_dx) {
       ProductArgs p{};
       p.a = reinterpret_cast<const uint8_t*>(dz);
@@ -467,7 +489,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.stages_b = static_cast<int>(vp / 32);
       p.stages = p.stages_b * pl.terms_x;
       p.splits = pl.splits;
-      MO_TRY((run_product_store<C, float>(p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0, nullptr}, s)));
+      MO_TRY((store<float>(p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0, nullptr}, s)));
     }
     if (want_dw) {
       ProductArgs p{};
@@ -481,8 +503,8 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.stages = p.stages_b * pl.terms_w;
       p.splits = 1;
       uint8_t* out = static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * esz_dw;
-      if (a.dw_dt == F32) MO_TRY((run_product_store<C, float>(p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
-      else MO_TRY((run_product_store<C, __bf16>(p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+      if (a.dw_dt == F32) MO_TRY((store<float>(p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+      else MO_TRY((store<__bf16>(p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
     }
   }
   if (want_dx) {

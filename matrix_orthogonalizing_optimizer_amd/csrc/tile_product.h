@@ -24,18 +24,22 @@ struct ProductArgs {
   int splits;                    // workgroups that share a tile's contraction
 };
 
-// 32 x 32 outputs, 64 bytes of each row: lane l gives row l & 31 and two
-// chunks of 16 bytes, at 32 (l / 32) bytes of the stage.  (Any order of the
+// A wave's 32 x 32 outputs from 64 bytes of each row: lane l gives row l & 31 and
+// two chunks of 16 bytes, at 32 (l / 32) bytes of the stage.  (Any order of the
 // contraction is right as long as both operands agree.)
 struct OpBf16 {
-  static constexpr bool kScaled = false;
+  static constexpr bool kScaled = false, kDecoded = false;
   static __device__ __forceinline__ f32x16v mma(const u32x4v (&a)[2], const u32x4v (&b)[2], f32x16v c, uint32_t, uint32_t) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[0]), __builtin_bit_cast(bf16x8_t, b[0]), c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[1]), __builtin_bit_cast(bf16x8_t, b[1]), c, 0, 0, 0);
   }
 };
+// 8-bit codes as they are: the instruction adds groups of products after
+// aligning them to the largest, and drops what lies about 2^-16 below it.  The
+// sums are off by 1.4e-5 of their size (2-norm) for normal values, 8e-5 where a
+// few values are a thousand times the others: enough for bf16 outputs.
 struct OpFp8 {
-  static constexpr bool kScaled = true;
+  static constexpr bool kScaled = true, kDecoded = false;
   static __device__ __forceinline__ i32x8v codes(const u32x4v (&x)[2]) {
     return i32x8v{static_cast<int>(x[0][0]), static_cast<int>(x[0][1]), static_cast<int>(x[0][2]), static_cast<int>(x[0][3]),
                   static_cast<int>(x[1][0]), static_cast<int>(x[1][1]), static_cast<int>(x[1][2]), static_cast<int>(x[1][3])};
@@ -44,16 +48,41 @@ struct OpFp8 {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes(a), codes(b), c, 0, 0, 0, static_cast<int>(sa), 0, static_cast<int>(sb));
   }
 };
+// 8-bit codes turned into the bf16 numbers that they stand for, exactly, on
+// their way from LDS to the matrix cores: exact products in fp32 sums, at half
+// the rate.
+struct OpFp8Exact {
+  static constexpr bool kScaled = true, kDecoded = true;
+};
 
-template <class OpT, int TMv, int TNv, int WMv, int WNv>
+// 16 codes under a scale as two operands of 8 bf16.
+__device__ __forceinline__ void decode16(u32x4v x, float s, u32x4v& lo, u32x4v& hi) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    lo[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[w], s, false));
+    lo[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[w], s, true));
+    hi[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 + w], s, false));
+    hi[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 + w], s, true));
+  }
+}
+__device__ __forceinline__ f32x16v mma_bf16(u32x4v a, u32x4v b, f32x16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// TM x TN outputs, WM x WN waves, a ring of NST stages in LDS.
+template <class OpT, int TMv, int TNv, int WMv, int WNv, int NSTv>
 struct TileCfgT {
   typedef OpT Op;
-  static constexpr int TM = TMv, TN = TNv, WM = WMv, WN = WNv, NW = WM * WN;
+  static constexpr int TM = TMv, TN = TNv, WM = WMv, WN = WNv, NST = NSTv, NW = WM * WN;
   static constexpr int FM = TM / (32 * WM), FN = TN / (32 * WN);
   static constexpr int kThreads = 64 * NW;
-  // LDS: what the epilogues need to turn 32 rows per wave
+  static constexpr int kMinWaves = FM * FN >= 16 ? 1 : 2;        // per SIMD: 256 sums a lane leave room for one
+  static constexpr int kStage = (TM + TN) * 64, kScaleGroup = Op::kScaled ? (TM + TN) * 16 : 0;
+  // what the epilogues need to turn 32 rows per wave
   static constexpr int kTurnPitch = TN / WN * 4 + 16;
-  static constexpr int kLds = NW * 32 * kTurnPitch;
+  static constexpr int kRing = NST * kStage + 2 * kScaleGroup, kTurn = NW * 32 * kTurnPitch;
+  static constexpr int kLds = kRing > kTurn ? kRing : kTurn;
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
 };
 
 // Where a workgroup's tile is: its first row and column, the last ones inside
@@ -72,8 +101,19 @@ __device__ __forceinline__ TilePlace tile_place(const ProductArgs& p) {
   q.wn = wave % C::WN;
   q.r32 = q.lane & 31;
   q.half = q.lane >> 5;
-  q.tm = blockIdx.x % p.tiles_m;
-  q.tn = blockIdx.x / p.tiles_m;
+  {
+    // each XCD (workgroup index mod 8) takes a contiguous range of tiles,
+    // walked in bands of 4 tile rows so that its L2 shares panels of both
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles_m) * static_cast<uint32_t>(p.tiles_n);
+    const uint32_t x = blockIdx.x % 8, y = blockIdx.x / 8;
+    const uint32_t t = x * (tiles / 8) + min(x, tiles % 8) + y;
+    constexpr uint32_t kBand = 4;
+    const uint32_t band = t / (kBand * p.tiles_n);
+    const uint32_t rows = min(kBand, p.tiles_m - band * kBand);
+    const uint32_t in = t - band * kBand * p.tiles_n;
+    q.tm = __builtin_amdgcn_readfirstlane(static_cast<int>(band * kBand + in % rows));
+    q.tn = __builtin_amdgcn_readfirstlane(static_cast<int>(in / rows));
+  }
   q.m0 = static_cast<int64_t>(q.tm) * C::TM;
   q.n0 = static_cast<int64_t>(q.tn) * C::TN;
   q.mlast = static_cast<int>(min(static_cast<int64_t>(C::TM), p.m - q.m0)) - 1;
@@ -90,50 +130,185 @@ __device__ __forceinline__ void split_range(const ProductArgs& p, int s, int& k0
 
 // acc[i][j]: lane (r32, half), element 4 e + k of the tile's row
 // wm TM / WM + 32 i + r32, column wn TN / WN + 32 j + 8 e + 4 half + k.
-// Straight from memory: every wave reads its own rows of both operands.
+//
+// LDS holds NST stages of 64 bytes of every row of both operands, filled by
+// loads that bypass the registers:
+//   * a row of a stage is 4 chunks of 16 bytes, stored at chunk ^ ((row / 4) &
+//     3): the 16 rows that a 16-byte read serves at a time then touch each of
+//     the 64 banks once;
+//   * scale bytes come for 16 blocks (32 stages) of a row at a time;
+//   * at stage t, whose fragments are in registers, the wave waits for its
+//     requests of stage t + 1, the workgroup meets, and then stage t's place is
+//     requested again for stage t + NST while the fragments of t + 1 are read.
+//     Products, reads and requests are interleaved one by one.
+// Past the end the last stage is requested again, unused, so that the number of
+// loads in flight is the same at every wait.  Rows past the end repeat the last
+// row; what comes of them is not stored.
 template <class C>
-__device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace& q, uint8_t*, f32x16v (&acc)[C::FM][C::FN]) {
+__device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace& q, uint8_t* smem, f32x16v (&acc)[C::FM][C::FN]) {
   typedef typename C::Op Op;
-  const uint8_t *a[C::FM], *b[C::FN], *sa[C::FM], *sb[C::FN];
+  constexpr int TM = C::TM, TN = C::TN, NW = C::NW, FM = C::FM, FN = C::FN, NST = C::NST, kStage = C::kStage;
+  constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW), DPW = DA + DB;      // requests of a wave and stage
+  constexpr int DS = Op::kScaled ? ((TM + TN) / 64 + NW - 1) / NW : 0;        // and of a group of scales
+  constexpr int kScales = NST * kStage;
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i) {
-    const int64_t r = q.m0 + min(q.wm * (C::TM / C::WM) + 32 * i + q.r32, q.mlast);   // rows past the end: the last again
-    a[i] = p.a + r * p.pitch_a + q.half * 32;
-    if constexpr (Op::kScaled) sa[i] = p.sa + r * p.sp;
-  }
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-  for (int j = 0; j < C::FN; ++j) {
-    const int64_t r = q.n0 + min(q.wn * (C::TN / C::WN) + 32 * j + q.r32, q.nlast);
-    b[j] = p.b + r * p.pitch_b + q.half * 32;
-    if constexpr (Op::kScaled) sb[j] = p.sb + r * p.sp;
-  }
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x16v{};
   int k0, k1;
   split_range(p, blockIdx.y, k0, k1);
+  const int stages = __builtin_amdgcn_readfirstlane(k1 - k0);
+  if (stages <= 0) return;                                // the same for the whole workgroup
+  const int wave = q.wm * C::WN + q.wn, lane = q.lane;
+  const uint8_t* a0 = uniform_ptr(p.a + q.m0 * p.pitch_a + static_cast<int64_t>(k0) * 64);
+  const uint8_t* b00 = uniform_ptr(p.b + q.n0 * p.pitch_b);
+
+  // Requests.  Lane l copies chunk l & 3 of row l / 4 of 16 rows, so it fetches
+  // the chunk that is stored there.
+  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+  uint32_t arow[DA], brow[DB];
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i)
+  for (int i = 0; i < DA; ++i) arow[i] = min(16 * (wave * DA + i) + lane / 4, q.mlast) * p.pitch_a + chunk * 16;
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x16v{};
-  for (int t = k0; t < k1; ++t) {
-    u32x4v av[C::FM][2], bv[C::FN][2];
-    uint32_t as[C::FM] = {}, bs[C::FN] = {};
-    const int64_t ka = static_cast<int64_t>(t) * 64, kb = static_cast<int64_t>(t % p.stages_b) * 64;
+  for (int i = 0; i < DB; ++i) brow[i] = min(16 * (wave * DB + i) + lane / 4, q.nlast) * p.pitch_b + chunk * 16;
+  const uint32_t lds0 = lds_addr(smem);
+  const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * 64 + wave * DB * 1024;
+  int tp = 0, kb = __builtin_amdgcn_readfirstlane(k0 % p.stages_b);           // the stage being requested, and b's
+  const uint8_t *pa = a0, *pb = uniform_ptr(b00 + static_cast<int64_t>(kb) * 64);
+  auto advance = [&]() __attribute__((always_inline)) {
+    const bool more = tp + 1 < stages;
+    tp += more;
+    pa = uniform_ptr(pa + (more ? 64 : 0));
+    const bool wrap = more && kb + 1 == p.stages_b;
+    kb = wrap ? 0 : kb + more;
+    pb = uniform_ptr(wrap ? b00 : pb + (more ? 64 : 0));
+  };
+  auto request = [&](auto I, uint32_t to) __attribute__((always_inline)) {
+    constexpr int i = I;
+    if constexpr (i < DA) lds_dma16_at<i * 1024>(pa, arow[i], dst + to);
+    else lds_dma16_at<(i - DA) * 1024>(pb, brow[i - DA], dstb + to);
+  };
+  // Scale bytes: 64 rows a request, 16 bytes of each; two groups in turn.
+  const int blocks = stages / 2, groups = (blocks + 15) / 16;
+  auto request_scales = [&](int g) __attribute__((always_inline)) {
+    if constexpr (Op::kScaled) {
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-      av[i][0] = *reinterpret_cast<const u32x4v*>(a[i] + ka);
-      av[i][1] = *reinterpret_cast<const u32x4v*>(a[i] + ka + 16);
-      if constexpr (Op::kScaled) as[i] = sa[i][t >> 1];
+      for (int i = 0; i < DS; ++i) {
+        const int r = (wave * DS + i) % ((TM + TN) / 64);                     // small tiles: some twice, the same bytes
+        const bool is_a = r < TM / 64;
+        const int row = is_a ? min(r * 64 + lane, q.mlast) : min((r - TM / 64) * 64 + lane, q.nlast);
+        const uint8_t* base = uniform_ptr(is_a ? p.sa + q.m0 * p.sp : p.sb + q.n0 * p.sp);
+        lds_dma16_at<0>(base, static_cast<uint32_t>(row) * p.sp + g * 16, lds0 + kScales + (g & 1) * C::kScaleGroup + r * 1024);
+      }
     }
+  };
+
+  // Fragments: 32 rows, lane l holds row l & 31.
+  const uint8_t* abase = smem + (q.wm * (TM / C::WM) + q.r32) * 64;
+  const uint8_t* bbase = smem + TM * 64 + (q.wn * (TN / C::WN) + q.r32) * 64;
+  const uint8_t* asbase = smem + kScales + (q.wm * (TM / C::WM) + q.r32) * 16;
+  const uint8_t* bsbase = smem + kScales + (TM + q.wn * (TN / C::WN) + q.r32) * 16;
+  uint32_t xs[2];
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      bv[j][0] = *reinterpret_cast<const u32x4v*>(b[j] + kb);
-      bv[j][1] = *reinterpret_cast<const u32x4v*>(b[j] + kb + 16);
-      if constexpr (Op::kScaled) bs[j] = sb[j][t >> 1];
+  for (int s = 0; s < 2; ++s) xs[s] = static_cast<uint32_t>(((q.half * 2 + s) ^ ((q.r32 >> 2) & 3)) * 16);
+  u32x4v af[2][FM][2], bf[2][FN][2];
+  uint32_t sa[FM] = {}, sb[FN] = {}, san[FM] = {}, sbn[FN] = {};
+  // reading r of a stage's 2 (FM + FN), in the order of need: A's first rows, B, the rest of A
+  constexpr int NR = 2 * (FM + FN);
+  auto read = [&](auto R, auto set, uint32_t at) __attribute__((always_inline)) {
+    constexpr int f = R / 2, s = R % 2, S = set;
+    constexpr int fa = f == 0 ? 0 : f > FN ? f - FN : -1, fb = f >= 1 && f <= FN ? f - 1 : -1;
+    if constexpr (fa >= 0) af[S][fa][s] = *reinterpret_cast<const u32x4v*>(abase + (at + xs[s]) + fa * 32 * 64);
+    if constexpr (fb >= 0) bf[S][fb][s] = *reinterpret_cast<const u32x4v*>(bbase + (at + xs[s]) + fb * 32 * 64);
+  };
+  auto read_scales = [&](int block) __attribute__((always_inline)) {
+    if constexpr (Op::kScaled) {
+      const int b = min(block, blocks - 1);                                   // past the end: the last again, unused
+      const uint32_t off = ((b >> 4) & 1) * C::kScaleGroup + (b & 15);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) san[i] = asbase[off + i * 512];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sbn[j] = bsbase[off + j * 512];
     }
+  };
+  auto take_scales = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+    for (int i = 0; i < FM; ++i) sa[i] = san[i];
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) acc[i][j] = Op::mma(bv[j], av[i], acc[i][j], bs[j], as[i]);
+    for (int j = 0; j < FN; ++j) sb[j] = sbn[j];
+  };
+  auto meet = [&]() __attribute__((always_inline)) {       // no memory fence: it would drain the loads
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  request_scales(0);
+  unroll<NST>([&](auto Q) __attribute__((always_inline)) {
+    if constexpr (Q > 0) advance();
+    unroll<DPW>([&](auto I) __attribute__((always_inline)) { request(I, static_cast<uint32_t>(Q * kStage)); });
+  });
+  wait_loads<(NST - 1) * DPW>();
+  meet();
+  unroll<NR>([&](auto R) __attribute__((always_inline)) { read(R, std::integral_constant<int, 0>{}, 0u); });
+  read_scales(0);
+  take_scales();
+
+  constexpr int NP = FM * FN;
+  uint32_t at = 0;                                         // place of the stage in registers
+  for (int t = 0; t < stages; t += 2) {
+    unroll<2>([&](auto S) __attribute__((always_inline)) {
+      constexpr int cur = S, nxt = cur ^ 1;
+      // this wave's reads of the stage are done, its part of the next has come
+      wait_loads<(NST - 2) * DPW>();
+      meet();
+      const uint32_t next = at + kStage == NST * kStage ? 0u : at + kStage;
+      if constexpr (Op::kScaled && cur == 0)
+        if ((t & 31) == 0 && (t >> 5) + 1 < groups) request_scales((t >> 5) + 1);
+      advance();
+      auto besides = [&](auto P, auto N) __attribute__((always_inline)) {     // what goes with product P of N
+        constexpr int n = N, r0 = P * NR / n, r1 = (P + 1) * NR / n, l0 = P * DPW / n, l1 = (P + 1) * DPW / n;
+        unroll<r1 - r0>([&](auto R) __attribute__((always_inline)) {
+          read(std::integral_constant<int, r0 + decltype(R)::value>{}, std::integral_constant<int, nxt>{}, next);
+        });
+        unroll<l1 - l0>([&](auto L) __attribute__((always_inline)) { request(std::integral_constant<int, l0 + decltype(L)::value>{}, at); });
+        if constexpr (cur == 1 && P == n - 1) read_scales(t / 2 + 1);
+      };
+      if constexpr (Op::kDecoded) {
+        float fa[FM], fb[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[i] = scale_of(sa[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = scale_of(sb[j]);
+        unroll<2>([&](auto H) __attribute__((always_inline)) {
+          constexpr int s = H;
+          u32x4v a[FM][2], b[FN][2];
+#pragma unroll
+          for (int j = 0; j < FN; ++j) decode16(bf[cur][j][s], fb[j], b[j][0], b[j][1]);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) decode16(af[cur][i][s], fa[i], a[i][0], a[i][1]);
+          unroll<NP>([&](auto P) __attribute__((always_inline)) {
+            constexpr int i = P / FN, j = P % FN;
+            acc[i][j] = mma_bf16(b[j][0], a[i][0], acc[i][j]);
+            acc[i][j] = mma_bf16(b[j][1], a[i][1], acc[i][j]);
+            besides(std::integral_constant<int, s * NP + decltype(P)::value>{}, std::integral_constant<int, 2 * NP>{});
+          });
+        });
+      } else {
+        // a product at a time, and behind each a little of everything else
+        unroll<NP>([&](auto P) __attribute__((always_inline)) {
+          constexpr int i = P / FN, j = P % FN;
+          acc[i][j] = Op::mma(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+          besides(P, std::integral_constant<int, NP>{});
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      }
+      if constexpr (cur == 1) take_scales();
+      at = next;
+    });
   }
+  wait_loads<0>();                                         // no request outlives the workgroup
+  __syncthreads();
 }
 
 // Stores the sums, times a factor in device memory where one is given.  Each
@@ -183,7 +358,7 @@ hipError_t run_product_zero(T* out, int64_t ldo, int64_t rows, int64_t cols, hip
 }
 
 template <class C, typename T>
-__global__ void __launch_bounds__(C::kThreads) product_store_kernel(const ProductArgs p, const StoreArgs<T> e) {
+__global__ void __launch_bounds__(C::kThreads, C::kMinWaves) product_store_kernel(const ProductArgs p, const StoreArgs<T> e) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
   const TilePlace q = tile_place<C>(p);
   f32x16v acc[C::FM][C::FN];
