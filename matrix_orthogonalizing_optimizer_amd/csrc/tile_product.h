@@ -141,9 +141,9 @@ __device__ __forceinline__ void split_range(const ProductArgs& p, int s, int& k0
 //     requests of stage t + 1, the workgroup meets, and then stage t's place is
 //     requested again for stage t + NST while the fragments of t + 1 are read.
 //     Products, reads and requests are interleaved one by one.
-// Past the end the last stage is requested again, unused, so that the number of
-// loads in flight is the same at every wait.  Rows past the end repeat the last
-// row; what comes of them is not stored.
+// Past the end no lane requests, and the number of loads in flight is still the
+// same at every wait.  Rows past the end repeat the last row; what comes of them
+// is not stored.
 template <class C>
 __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace& q, uint8_t* smem, f32x16v (&acc)[C::FM][C::FN]) {
   typedef typename C::Op Op;
@@ -151,6 +151,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW), DPW = DA + DB;      // requests of a wave and stage
   constexpr int DS = Op::kScaled ? ((TM + TN) / 64 + NW - 1) / NW : 0;        // and of a group of scales
   constexpr int kScales = NST * kStage;
+  static_assert(NST % 2 == 0, "stages come in pairs");
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -175,18 +176,20 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * 64 + wave * DB * 1024;
   int tp = 0, kb = __builtin_amdgcn_readfirstlane(k0 % p.stages_b);           // the stage being requested, and b's
   const uint8_t *pa = a0, *pb = uniform_ptr(b00 + static_cast<int64_t>(kb) * 64);
+  int lanes = -1;                                          // which of them request, each half of the wave
   auto advance = [&]() __attribute__((always_inline)) {
-    const bool more = tp + 1 < stages;
-    tp += more;
-    pa = uniform_ptr(pa + (more ? 64 : 0));
-    const bool wrap = more && kb + 1 == p.stages_b;
-    kb = wrap ? 0 : kb + more;
-    pb = uniform_ptr(wrap ? b00 : pb + (more ? 64 : 0));
+    ++tp;
+    ++kb;
+    pa = uniform_ptr(pa + 64);
+    const bool wrap = kb == p.stages_b;
+    kb = wrap ? 0 : kb;
+    pb = uniform_ptr(wrap ? b00 : pb + 64);
+    lanes = __builtin_amdgcn_readfirstlane(tp < stages ? -1 : 0);
   };
   auto request = [&](auto I, uint32_t to) __attribute__((always_inline)) {
     constexpr int i = I;
-    if constexpr (i < DA) lds_dma16_at<i * 1024>(pa, arow[i], dst + to);
-    else lds_dma16_at<(i - DA) * 1024>(pb, brow[i - DA], dstb + to);
+    if constexpr (i < DA) lds_dma16_masked<i * 1024>(pa, arow[i], dst + to, lanes);
+    else lds_dma16_masked<(i - DA) * 1024>(pb, brow[i - DA], dstb + to, lanes);
   };
   // Scale bytes: 64 rows a request, 16 bytes of each; two groups in turn.
   const int blocks = stages / 2, groups = (blocks + 15) / 16;
