@@ -42,15 +42,18 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// The softmax of a row; columns past the last are 0.
 template <typename T, int L, int C>
-__device__ __forceinline__ void softmax_row(const T* z, int experts, int l, float (&p)[C]) {
+__device__ __forceinline__ void load_row(const T* z, int experts, int l, float (&p)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) p[c] = l + L * c < experts ? to_f(z[l + L * c]) : -INFINITY;
+}
+
+// The softmax of a row, in place; columns past the last are 0.
+template <int L, int C>
+__device__ __forceinline__ void softmax_row(int experts, int l, float (&p)[C]) {
   float m = -INFINITY;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    p[c] = l + L * c < experts ? to_f(z[l + L * c]) : -INFINITY;
-    m = fmaxf(m, p[c]);
-  }
+  for (int c = 0; c < C; ++c) m = fmaxf(m, p[c]);
   m = lanes_max<L>(m);
   float s = 0.0f;
 #pragma unroll
@@ -85,19 +88,41 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(const BalanceArgs a, 
   const int l = threadIdx.x % L, r = threadIdx.x / L;
   float sum[C] = {};
   int live = 0, wrong = 0;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + r; t < a.tokens; t += static_cast<int64_t>(w.groups) * kRows) {
-    const int64_t* index = a.index + t * a.top;
-    if (!has_choice<L>(index, a.top, l)) continue;
-    for (int k = l; k < a.top; k += L) {
-      const int64_t e = index[k];
-      if (e >= a.experts) wrong = 1;
-      else if (e >= 0) atomicAdd(&count[e], 1);
-    }
-    if (l == 0) ++live;
-    float p[C];
-    softmax_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p);
+  // kDeep rows at a time, whose loads are all in flight before the first is used
+  constexpr int kDeep = C <= 4 ? 4 : C <= 8 ? 2 : 1;
+  const int64_t step = static_cast<int64_t>(w.groups) * kRows;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows + r; t0 < a.tokens; t0 += step * kDeep) {
+    float p[kDeep][C];
+    int64_t first[kDeep];
 #pragma unroll
-    for (int c = 0; c < C; ++c) sum[c] += p[c];
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t t = t0 + d * step;
+      first[d] = -1;
+      if (t < a.tokens) {
+        load_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p[d]);
+        if (l < a.top) first[d] = a.index[t * a.top + l];
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t t = t0 + d * step;
+      if (t >= a.tokens) continue;                          // the same for the row's lanes
+      int any = 0;
+      int64_t e = first[d];
+      for (int k = l; k < a.top; k += L) {
+        if (k >= L) e = a.index[t * a.top + k];
+        any |= e >= 0;
+        if (e >= a.experts) wrong = 1;
+        else if (e >= 0) atomicAdd(&count[e], 1);
+      }
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) any |= __shfl_xor(any, o, 64);
+      if (!any) continue;
+      if (l == 0) ++live;
+      softmax_row<L, C>(a.experts, l, p[d]);
+#pragma unroll
+      for (int c = 0; c < C; ++c) sum[c] += p[d][c];
+    }
   }
   if (live) atomicAdd(&seen[0], live);
   if (wrong) seen[1] = 1;
@@ -123,10 +148,14 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
   return t;
 }
 
-// One workgroup: totals over the groups, f, the loss.
+// One workgroup: totals over the groups, f, the loss.  A wave takes 64 experts
+// and every 16th group; the waves' sums are added in their order.
 __global__ void __launch_bounds__(1024) balance_join_kernel(const BalanceArgs a, const Partials w) {
+  __shared__ float psum[16][64];
+  __shared__ int csum[16][64];
+  __shared__ float mean[kMaxExperts];          // sum of p, then its share of the loss
   __shared__ int64_t red[16];
-  __shared__ float redf[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t live = 0, wrong = 0, choices = 0;
   for (int g = threadIdx.x; g < w.groups; g += 1024) {
     live += w.tokens[g * 2];
@@ -134,29 +163,45 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const BalanceArgs a,
   }
   live = block_sum(live, red);
   wrong = block_sum(wrong, red);
-  for (int e = threadIdx.x; e < a.experts; e += 1024) {
-    int64_t c = 0;
-    for (int g = 0; g < w.groups; ++g) c += w.count[static_cast<int64_t>(g) * a.experts + e];
-    a.counts[e] = c;
-    choices += c;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    const int e = e0 + lane;
+    float p = 0.0f;
+    int c = 0;
+    if (e < a.experts) {
+#pragma unroll 8
+      for (int g = wave; g < w.groups; g += 16) {
+        p += w.p[static_cast<int64_t>(g) * a.experts + e];
+        c += w.count[static_cast<int64_t>(g) * a.experts + e];
+      }
+    }
+    psum[wave][lane] = p;
+    csum[wave][lane] = c;
+    __syncthreads();
+    if (wave == 0 && e < a.experts) {
+      float v = 0.0f;
+      int64_t n = 0;
+      for (int i = 0; i < 16; ++i) {
+        v += psum[i][lane];
+        n += csum[i][lane];
+      }
+      mean[e] = v;
+      a.counts[e] = n;
+      choices += n;
+    }
+    __syncthreads();
   }
   choices = block_sum(choices, red);
   float loss = 0.0f;
-  for (int e = threadIdx.x; e < a.experts; e += 1024) {
-    float p = 0.0f;
-    for (int g = 0; g < w.groups; ++g) p += w.p[static_cast<int64_t>(g) * a.experts + e];
-    const float f = choices ? static_cast<float>(a.counts[e]) * static_cast<float>(a.experts) / static_cast<float>(choices) : 0.0f;
-    w.f[e] = f;
-    loss += f * p;
-  }
+  if (wave == 0)
+    for (int e = lane; e < a.experts; e += 64) {              // the lane's own counts and sums
+      const float f = choices ? static_cast<float>(a.counts[e]) * static_cast<float>(a.experts) / static_cast<float>(choices) : 0.0f;
+      w.f[e] = f;
+      loss += f * mean[e];
+    }
   for (int o = 32; o > 0; o >>= 1) loss += __shfl_xor(loss, o, 64);
-  if ((threadIdx.x & 63) == 0) redf[threadIdx.x >> 6] = loss;
-  __syncthreads();
   if (threadIdx.x) return;
-  float t = 0.0f;
-  for (int i = 0; i < 16; ++i) t += redf[i];
   const float n = live ? static_cast<float>(live) : 1.0f;
-  *a.loss = wrong ? NAN : a.weight * (t / n);
+  *a.loss = wrong ? NAN : a.weight * (loss / n);
   w.f[a.experts] = wrong ? NAN : a.weight * (a.grad_loss ? *a.grad_loss : 1.0f) / n;
 }
 
@@ -174,7 +219,8 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a, 
     float p[C];
     float mean = 0.0f;
     if (live) {
-      softmax_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p);
+      load_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p);
+      softmax_row<L, C>(a.experts, l, p);
 #pragma unroll
       for (int c = 0; c < C; ++c) mean += p[c] * f[c];
       mean = lanes_sum<L>(mean);
@@ -190,7 +236,8 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a, 
   }
 }
 
-int groups_of(int64_t tokens) { return static_cast<int>(std::min<int64_t>(256, (tokens + 63) / 64)); }
+// Workgroups of the first launch: what they leave is read by one workgroup.
+int groups_of(int64_t tokens) { return static_cast<int>(std::min<int64_t>(512, (tokens + 63) / 64)); }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 

@@ -310,6 +310,20 @@ static hipError_t run(const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t 
   return run_product_store<C, T>(p, {static_cast<T*>(a.out), a.ldo, 0, a.accumulate, nullptr}, s);
 }
 
+// Measured (see tile_us), in tiles of 64, 128 and 256: 1024 x 1024 x 8192 26, 2048
+// x 2048 x 8192 44, 4096 x 4096 x 8192 114 us from codes, 40, 76 and 201 decoded.
+constexpr TileCost kCostCodes[3] = {{64, 3, 4.0, 0.15, 0.15}, {128, 2, 7.0, 0.25, 0.29}, {256, 1, 13.0, 0.60, 0.78}};
+constexpr TileCost kCostExact[3] = {{64, 3, 5.0, 0.25, 0.20}, {128, 2, 7.0, 0.52, 0.43}, {256, 1, 16.0, 1.10, 1.45}};
+
+template <class Op, typename T>
+static hipError_t run_op(const TileCost (&cost)[3], const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t s) {
+  double us[3];
+  for (int i = 0; i < 3; ++i) us[i] = tile_us(cost[i], a.m, a.n, p.stages, 1);
+  if (us[2] <= us[1] && us[2] <= us[0]) return run<TileCfgT<Op, 256, 256, 2, 4, 4>, T>(p, a, s);
+  if (us[1] <= us[0]) return run<TileCfgT<Op, 128, 128, 2, 2, 4>, T>(p, a, s);
+  return run<TileCfgT<Op, 64, 64, 2, 2, 6>, T>(p, a, s);
+}
+
 hipError_t launch_fp8_matmul(int out_dt, const Fp8MatmulArgs& a, hipStream_t s) {
   if (a.nb == 0)                     // accumulating calls do not come here
     return out_dt == F32 ? run_product_zero(static_cast<float*>(a.out), a.ldo, a.m, a.n, s)
@@ -325,12 +339,7 @@ hipError_t launch_fp8_matmul(int out_dt, const Fp8MatmulArgs& a, hipStream_t s) 
   p.n = a.n;
   p.stages = p.stages_b = 2 * a.nb;
   p.splits = 1;
-  if (a.m >= 1024 && a.n >= 1024) {
-    if (out_dt == F32) return run<TileCfgT<OpFp8Exact, 256, 256, 2, 4, 4>, float>(p, a, s);
-    return run<TileCfgT<OpFp8, 256, 256, 2, 2, 4>, __bf16>(p, a, s);
-  }
-  if (out_dt == F32) return run<TileCfgT<OpFp8Exact, 64, 64, 2, 2, 6>, float>(p, a, s);
-  return run<TileCfgT<OpFp8, 64, 64, 2, 2, 6>, __bf16>(p, a, s);
+  return out_dt == F32 ? run_op<OpFp8Exact, float>(kCostExact, p, a, s) : run_op<OpFp8, __bf16>(kCostCodes, p, a, s);
 }
 
 }  // namespace mo

@@ -60,46 +60,50 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, c
 
 // bf16 copies of a [rows, cols] matrix: dst [rows][pitch] (columns past `cols`
 // zero) and its transpose dst_t [cols][pitch_t] (rows past `rows` zero, and
-// those whose factor is 0, so that whatever they hold takes no part).  Tiles of
-// 64 x 64 through LDS.
+// those whose factor is 0, so that whatever they hold takes no part).  64 rows
+// x 128 columns per workgroup, through LDS; HBM bound.
+constexpr int kPackRows = 64, kPackCols = 128;
 template <typename T>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
                                                       uint16_t* dst_t, int64_t pitch_t, const float* factor) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int cl = (threadIdx.x & 15) * 4, rl = threadIdx.x >> 4;
+  __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];       // pairs of columns; odd rows of dwords: columns spread over the banks
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kPackRows, c0 = static_cast<int64_t>(blockIdx.x) * kPackCols;
+  const int cl = (threadIdx.x & 15) * 8, rl = threadIdx.x >> 4;
+  const int left = static_cast<int>(min(int64_t{8}, cols - c0 - cl));
+  Oct<T> o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i].clear();
+    if (r0 + rl + 16 * i < rows && left > 0) o[i].load(src + (r0 + rl + 16 * i) * ld + c0 + cl, left);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + rl + 16 * i;
-    float v[4] = {};
-    if (r < rows) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c0 + cl + k < cols) v[k] = to_f(src[r * ld + c0 + cl + k]);
-    }
-    const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
-    if (dst && r < rows && c0 + cl < pitch) *reinterpret_cast<uint2*>(dst + r * pitch + c0 + cl) = make_uint2(lo, hi);
+    const u32x4v v = {pack_bf16x2(o[i].get(0), o[i].get(1)), pack_bf16x2(o[i].get(2), o[i].get(3)),
+                      pack_bf16x2(o[i].get(4), o[i].get(5)), pack_bf16x2(o[i].get(6), o[i].get(7))};
+    if (dst && r < rows && c0 + cl < pitch) *reinterpret_cast<u32x4v*>(dst + r * pitch + c0 + cl) = v;
     const bool out = factor && r < rows && factor[r] == 0.0f;
-    tile[rl + 16 * i][cl] = out ? 0 : static_cast<uint16_t>(lo);
-    tile[rl + 16 * i][cl + 1] = out ? 0 : static_cast<uint16_t>(lo >> 16);
-    tile[rl + 16 * i][cl + 2] = out ? 0 : static_cast<uint16_t>(hi);
-    tile[rl + 16 * i][cl + 3] = out ? 0 : static_cast<uint16_t>(hi >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tile[rl + 16 * i][cl / 2 + k] = out ? 0u : v[k];
   }
   if (!dst_t) return;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t c = c0 + rl + 16 * i, r = r0 + cl;
-    if (c >= cols || r >= pitch_t) continue;
-    const uint32_t lo = tile[cl][rl + 16 * i] | static_cast<uint32_t>(tile[cl + 1][rl + 16 * i]) << 16;
-    const uint32_t hi = tile[cl + 2][rl + 16 * i] | static_cast<uint32_t>(tile[cl + 3][rl + 16 * i]) << 16;
-    *reinterpret_cast<uint2*>(dst_t + c * pitch_t + r) = make_uint2(lo, hi);
+    const int u = i * 256 + threadIdx.x, c = u >> 3, r = (u & 7) * 8;       // 8 rows of a column
+    if (c0 + c >= cols || r0 + r >= pitch_t) continue;
+    const int shift = (c & 1) * 16;
+    u32x4v v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = ((tile[r + 2 * k][c / 2] >> shift) & 0xffffu) | ((tile[r + 2 * k + 1][c / 2] >> shift) << 16);
+    *reinterpret_cast<u32x4v*>(dst_t + (c0 + c) * pitch_t + r0 + r) = v;
   }
 }
 
 hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch, uint16_t* dst_t, int64_t pitch_t,
                 const float* factor, hipStream_t s) {
-  const dim3 g(static_cast<uint32_t>((cols + 63) / 64), static_cast<uint32_t>((rows + 63) / 64));
+  const dim3 g(static_cast<uint32_t>((cols + kPackCols - 1) / kPackCols), static_cast<uint32_t>((rows + kPackRows - 1) / kPackRows));
   if (dt == F32) ce_pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
   else ce_pack_kernel<__bf16><<<g, 256, 0, s>>>(static_cast<const __bf16*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
   return hipGetLastError();
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int s
 struct Plan {
   int64_t hp, tp;              // hidden size and rows, padded to whole pairs of stages
   int64_t vf, vb;              // columns of a forward and of a backward piece
-  int splits;                  // of the product for dx
+  int splits, tile_dx;         // of the product for dx
   int terms_x, terms_w;
   size_t part, stat, zt, factor, scale, x, w, x_t, w_t, dz, dz_t, dxp, total;
 };
@@ -333,8 +337,40 @@ int64_t piece_of(int64_t vocab, int64_t most) {
   return std::min(up((vocab + n - 1) / n, 256), up(vocab, 256));
 }
 
-typedef TileCfgT<OpBf16, 64, 64, 2, 2, 6> CfgSmall;
-typedef TileCfgT<OpBf16, 256, 256, 2, 2, 4> CfgLarge;
+
+typedef TileCfgT<OpBf16, 64, 64, 2, 2, 6> Cfg64;
+typedef TileCfgT<OpBf16, 128, 128, 2, 2, 4> Cfg128;
+typedef TileCfgT<OpBf16, 256, 256, 2, 4, 4> Cfg256;
+
+// Measured (see tile_us): 4096 x 4096 x 8192 takes 230 us in tiles of 256, 2048
+// x 2048 x 8192 80 in tiles of 128 and 149 in 64 tiles of 256, 1024 x 1024 x 8192
+// 41 in tiles of 64.
+constexpr TileCost kCost64{64, 3, 5.0, 0.13, 0.13}, kCost128{128, 2, 6.0, 0.22, 0.30}, kCost256{256, 1, 11.0, 0.54, 0.86};
+
+// The quickest tile for a product, and how many workgroups should share each
+// tile's contraction (their parts are written, and read by the pass that adds
+// them, at 4 TB/s).
+struct Choice {
+  int tile, splits;
+};
+Choice choose(int64_t m, int64_t n, int64_t stages, bool may_split) {
+  Choice best{64, 1};
+  double least = 1e30;
+  for (const TileCost& c : {kCost64, kCost128, kCost256})
+    for (int s = 1; s == 1 || (may_split && s <= 64 && stages >= 16 * s); s *= 2) {
+      const double us = tile_us(c, m, n, (stages + s - 1) / s, s) + (s - 1) * static_cast<double>(m) * n * 8 / 4e6;
+      if (us < least) {
+        least = us;
+        best = {c.size, s};
+      }
+    }
+  return best;
+}
+
+template <typename T>
+hipError_t store(int tile, const ProductArgs& p, const StoreArgs<T>& e, hipStream_t s) {
+  return tile == 256 ? run_product_store<Cfg256, T>(p, e, s) : tile == 128 ? run_product_store<Cfg128, T>(p, e, s) : run_product_store<Cfg64, T>(p, e, s);
+}
 
 Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt, bool dx, bool dw) {
   Plan p{};
@@ -347,8 +383,9 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   const int64_t fit = std::min((int64_t{1} << 26) / std::max<int64_t>(rows, 1), (int64_t{1} << 27) / p.hp);
   p.vb = piece_of(vocab, std::min(std::max(fit / 256 * 256, int64_t{1024}), int64_t{1} << 20));
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
-  const int64_t tiles = ((rows + 63) / 64) * ((hidden + 63) / 64);
-  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), p.vb / 256)));
+  const Choice of_dx = choose(rows, hidden, p.vb / 32 * p.terms_x, true);
+  p.splits = of_dx.splits;
+  p.tile_dx = of_dx.tile;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -370,14 +407,6 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * hidden * 4);
   p.total = rows ? at : 0;
   return p;
-}
-
-// Whether the product fills the chip with tiles of 256.
-bool large(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 128; }
-
-template <typename T>
-hipError_t store(const ProductArgs& p, const StoreArgs<T>& e, hipStream_t s) {
-  return large(p.m, p.n) ? run_product_store<CfgLarge, T>(p, e, s) : run_product_store<CfgSmall, T>(p, e, s);
 }
 
 template <class C>
@@ -462,8 +491,10 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     logits.n = v;
     const CeStatsArgs e{a.targets, v0, part, zt};
     int64_t cols;
-    if (large(a.rows, v)) MO_TRY(run_stats<CfgLarge>(logits, e, cols, s));
-    else MO_TRY(run_stats<CfgSmall>(logits, e, cols, s));
+    const int tile = choose(a.rows, v, logits.stages, false).tile;
+    if (tile == 256) MO_TRY(run_stats<Cfg256>(logits, e, cols, s));
+    else if (tile == 128) MO_TRY(run_stats<Cfg128>(logits, e, cols, s));
+    else MO_TRY(run_stats<Cfg64>(logits, e, cols, s));
     ce_join_kernel<<<(a.rows + 3) / 4, 256, 0, s>>>(part, cols, a.rows, a.vocab, v0 == 0,
                                                     v0 + v >= a.vocab, a.targets, zt, stat, a.loss);
     MO_TRY(hipGetLastError());
@@ -477,7 +508,8 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
     logits.n = v;
     const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp)};
-    MO_TRY(large(a.rows, v) ? run_grad<CfgLarge>(logits, e, s) : run_grad<CfgSmall>(logits, e, s));
+    const int tile = choose(a.rows, v, logits.stages, false).tile;
+    MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
     if (want_dx) {
       ProductArgs p{};
       p.a = reinterpret_cast<const uint8_t*>(dz);
@@ -489,7 +521,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.stages_b = static_cast<int>(vp / 32);
       p.stages = p.stages_b * pl.terms_x;
       p.splits = pl.splits;
-      MO_TRY((store<float>(p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0, nullptr}, s)));
+      MO_TRY((store<float>(pl.tile_dx, p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0, nullptr}, s)));
     }
     if (want_dw) {
       ProductArgs p{};
@@ -502,9 +534,10 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.stages_b = static_cast<int>(pl.tp / 32);
       p.stages = p.stages_b * pl.terms_w;
       p.splits = 1;
+      const int tile_dw = choose(v, a.hidden, p.stages, false).tile;
       uint8_t* out = static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * esz_dw;
-      if (a.dw_dt == F32) MO_TRY((store<float>(p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
-      else MO_TRY((store<__bf16>(p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+      if (a.dw_dt == F32) MO_TRY((store<float>(tile_dw, p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+      else MO_TRY((store<__bf16>(tile_dw, p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
     }
   }
   if (want_dx) {

@@ -33,11 +33,11 @@ __device__ __forceinline__ void lds_dma16_at(const void* sbase, uint32_t voff, u
                : "memory", "m0", "scc");
 }
 
-// The same where `lanes` is -1, in a wave whose lanes are all active; where it is
-// 0 no lane takes part: it counts as a load that is done and touches no memory.
+// The same from the lanes of `lanes` (a scalar), in a wave whose lanes are all
+// active: from none it counts as a load that is done and touches no memory.
 template <int kPlus>
-__device__ __forceinline__ void lds_dma16_masked(const void* sbase, uint32_t voff, uint32_t lds_base, int lanes) {
-  asm volatile("s_add_u32 m0, %2, %3\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
+__device__ __forceinline__ void lds_dma16_masked(const void* sbase, uint32_t voff, uint32_t lds_base, uint64_t lanes) {
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
                :
                : "v"(voff), "s"(sbase), "s"(lds_base), "n"(kPlus), "s"(lanes)
                : "memory", "m0", "scc");

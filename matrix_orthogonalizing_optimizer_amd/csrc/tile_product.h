@@ -27,11 +27,17 @@ struct ProductArgs {
 // A wave's 32 x 32 outputs from 64 bytes of each row: lane l gives row l & 31 and
 // two chunks of 16 bytes, at 32 (l / 32) bytes of the stage.  (Any order of the
 // contraction is right as long as both operands agree.)
+// Two instructions a stage: first one for every output block, then the other,
+// as two in a row on the same sums would wait for each other.
+__device__ __forceinline__ f32x16v mma_bf16(u32x4v a, u32x4v b, f32x16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
 struct OpBf16 {
   static constexpr bool kScaled = false, kDecoded = false;
+  static constexpr int kSteps = 2;
+  template <int kStep>
   static __device__ __forceinline__ f32x16v mma(const u32x4v (&a)[2], const u32x4v (&b)[2], f32x16v c, uint32_t, uint32_t) {
-    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[0]), __builtin_bit_cast(bf16x8_t, b[0]), c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[1]), __builtin_bit_cast(bf16x8_t, b[1]), c, 0, 0, 0);
+    return mma_bf16(a[kStep], b[kStep], c);
   }
 };
 // 8-bit codes as they are: the instruction adds groups of products after
@@ -40,10 +46,12 @@ struct OpBf16 {
 // few values are a thousand times the others: enough for bf16 outputs.
 struct OpFp8 {
   static constexpr bool kScaled = true, kDecoded = false;
+  static constexpr int kSteps = 1;
   static __device__ __forceinline__ i32x8v codes(const u32x4v (&x)[2]) {
     return i32x8v{static_cast<int>(x[0][0]), static_cast<int>(x[0][1]), static_cast<int>(x[0][2]), static_cast<int>(x[0][3]),
                   static_cast<int>(x[1][0]), static_cast<int>(x[1][1]), static_cast<int>(x[1][2]), static_cast<int>(x[1][3])};
   }
+  template <int>
   static __device__ __forceinline__ f32x16v mma(const u32x4v (&a)[2], const u32x4v (&b)[2], f32x16v c, uint32_t sa, uint32_t sb) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes(a), codes(b), c, 0, 0, 0, static_cast<int>(sa), 0, static_cast<int>(sb));
   }
@@ -65,10 +73,6 @@ __device__ __forceinline__ void decode16(u32x4v x, float s, u32x4v& lo, u32x4v& 
     hi[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 + w], s, true));
   }
 }
-__device__ __forceinline__ f32x16v mma_bf16(u32x4v a, u32x4v b, f32x16v c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
 // TM x TN outputs, WM x WN waves, a ring of NST stages in LDS.
 template <class OpT, int TMv, int TNv, int WMv, int WNv, int NSTv>
 struct TileCfgT {
@@ -84,6 +88,21 @@ struct TileCfgT {
   static constexpr int kLds = kRing > kTurn ? kRing : kTurn;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
 };
+
+// What a tile costs, from measurements of this file's kernels with few and with
+// many tiles and short and long contractions: `fixed` us for a round of as many
+// tiles as the chip's 256 CUs hold (`resident` each), and per stage `alone` us,
+// or `shared` for every tile that a CU has where that is more.
+struct TileCost {
+  int size, resident;
+  double fixed, alone, shared;
+};
+inline double tile_us(const TileCost& c, int64_t m, int64_t n, int64_t stages, int splits) {
+  const int64_t tiles = ((m + c.size - 1) / c.size) * ((n + c.size - 1) / c.size) * splits;
+  const int64_t rounds = (tiles + 256 * c.resident - 1) / (256 * c.resident), per_cu = (tiles + 255) / 256;
+  const double stage = c.shared * static_cast<double>(per_cu);
+  return c.fixed * static_cast<double>(rounds) + static_cast<double>(stages) * (stage > c.alone ? stage : c.alone);
+}
 
 // Where a workgroup's tile is: its first row and column, the last ones inside
 // it that exist, the wave's and the lane's place.
@@ -176,7 +195,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * 64 + wave * DB * 1024;
   int tp = 0, kb = __builtin_amdgcn_readfirstlane(k0 % p.stages_b);           // the stage being requested, and b's
   const uint8_t *pa = a0, *pb = uniform_ptr(b00 + static_cast<int64_t>(kb) * 64);
-  int lanes = -1;                                          // which of them request, each half of the wave
+  uint64_t lanes = ~uint64_t{0};                            // which of them request
   auto advance = [&]() __attribute__((always_inline)) {
     ++tp;
     ++kb;
@@ -184,7 +203,8 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
     const bool wrap = kb == p.stages_b;
     kb = wrap ? 0 : kb;
     pb = uniform_ptr(wrap ? b00 : pb + 64);
-    lanes = __builtin_amdgcn_readfirstlane(tp < stages ? -1 : 0);
+    const uint32_t half_wave = __builtin_amdgcn_readfirstlane(tp < stages ? -1 : 0);
+    lanes = static_cast<uint64_t>(half_wave) << 32 | half_wave;
   };
   auto request = [&](auto I, uint32_t to) __attribute__((always_inline)) {
     constexpr int i = I;
@@ -290,19 +310,18 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
           for (int j = 0; j < FN; ++j) decode16(bf[cur][j][s], fb[j], b[j][0], b[j][1]);
 #pragma unroll
           for (int i = 0; i < FM; ++i) decode16(af[cur][i][s], fa[i], a[i][0], a[i][1]);
-          unroll<NP>([&](auto P) __attribute__((always_inline)) {
-            constexpr int i = P / FN, j = P % FN;
-            acc[i][j] = mma_bf16(b[j][0], a[i][0], acc[i][j]);
-            acc[i][j] = mma_bf16(b[j][1], a[i][1], acc[i][j]);
-            besides(std::integral_constant<int, s * NP + decltype(P)::value>{}, std::integral_constant<int, 2 * NP>{});
+          unroll<2 * NP>([&](auto P) __attribute__((always_inline)) {
+            constexpr int i = P % NP / FN, j = P % FN, h = P / NP;
+            acc[i][j] = mma_bf16(b[j][h], a[i][h], acc[i][j]);
+            besides(std::integral_constant<int, 2 * s * NP + decltype(P)::value>{}, std::integral_constant<int, 4 * NP>{});
           });
         });
       } else {
         // a product at a time, and behind each a little of everything else
-        unroll<NP>([&](auto P) __attribute__((always_inline)) {
-          constexpr int i = P / FN, j = P % FN;
-          acc[i][j] = Op::mma(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
-          besides(P, std::integral_constant<int, NP>{});
+        unroll<Op::kSteps * NP>([&](auto P) __attribute__((always_inline)) {
+          constexpr int i = P % NP / FN, j = P % FN;
+          acc[i][j] = Op::template mma<P / NP>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
+          besides(P, std::integral_constant<int, Op::kSteps * NP>{});
           __builtin_amdgcn_sched_barrier(0);
         });
       }
