@@ -205,6 +205,93 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const BalanceArgs a,
   w.f[a.experts] = wrong ? NAN : a.weight * (a.grad_loss ? *a.grad_loss : 1.0f) / n;
 }
 
+// The gradient of token t.
+template <typename T, int L, int C>
+__device__ __forceinline__ void grad_row(const BalanceArgs& a, int64_t t, int l, const float (&f)[C], float factor) {
+  T* out = static_cast<T*>(a.grad) + t * a.ld_grad;
+  float p[C];
+  load_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p);
+  const bool live = has_choice<L>(a.index + t * a.top, a.top, l);
+  softmax_row<L, C>(a.experts, l, p);
+  float mean = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) mean += p[c] * f[c];
+  mean = lanes_sum<L>(mean);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = l + L * c;
+    if (e >= a.experts) continue;
+    float v = live ? factor * (p[c] * (f[c] - mean)) : 0.0f;
+    if (a.accumulate) v += to_f(out[e]);
+    out[e] = static_cast<T>(v);
+  }
+}
+
+// Few tokens: everything in one launch of one workgroup, whose sums and counts
+// stay in LDS.
+template <typename T, int L, int C>
+__global__ void __launch_bounds__(1024) balance_small_kernel(const BalanceArgs a) {
+  constexpr int kRows = 1024 / L, kMost = L * C;
+  __shared__ int count[kMost];
+  __shared__ float part[kRows * kMost], f[kMost], lossf[kMost];
+  __shared__ int seen[2], choices;
+  const int l = threadIdx.x % L, r = threadIdx.x / L;
+  for (int e = threadIdx.x; e < kMost; e += 1024) count[e] = 0;
+  if (threadIdx.x < 2) seen[threadIdx.x] = 0;
+  if (threadIdx.x == 2) choices = 0;
+  __syncthreads();
+  float sum[C] = {};
+  for (int64_t t = r; t < a.tokens; t += kRows) {
+    int any = 0;
+    float p[C];
+    load_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p);
+    for (int k = l; k < a.top; k += L) {
+      const int64_t e = a.index[t * a.top + k];
+      any |= e >= 0;
+      if (e >= a.experts) seen[1] = 1;
+      else if (e >= 0) atomicAdd(&count[e], 1);
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) any |= __shfl_xor(any, o, 64);
+    if (!any) continue;
+    if (l == 0) atomicAdd(&seen[0], 1);
+    softmax_row<L, C>(a.experts, l, p);
+#pragma unroll
+    for (int c = 0; c < C; ++c) sum[c] += p[c];
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) part[(r * C + c) * L + l] = sum[c];
+  __syncthreads();
+  for (int e = threadIdx.x; e < kMost; e += 1024) {
+    if (e < a.experts) {
+      a.counts[e] = count[e];
+      if (count[e]) atomicAdd(&choices, count[e]);
+    }
+    float v = 0.0f;
+    for (int i = 0; i < kRows; ++i) v += part[i * kMost + e];
+    lossf[e] = v;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < kMost; e += 1024) {
+    f[e] = e < a.experts && choices ? static_cast<float>(count[e]) * static_cast<float>(a.experts) / static_cast<float>(choices) : 0.0f;
+    lossf[e] *= f[e];
+  }
+  __syncthreads();
+  const float n = seen[0] ? static_cast<float>(seen[0]) : 1.0f;
+  if (threadIdx.x < 64) {
+    float loss = 0.0f;
+    for (int e = threadIdx.x; e < kMost; e += 64) loss += e < a.experts ? lossf[e] : 0.0f;
+    loss = lanes_sum<64>(loss);
+    if (threadIdx.x == 0) *a.loss = seen[1] ? NAN : a.weight * (loss / n);
+  }
+  if (!a.grad) return;
+  const float factor = seen[1] ? NAN : a.weight * (a.grad_loss ? *a.grad_loss : 1.0f) / n;
+  float fr[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) fr[c] = f[l + L * c];
+  for (int64_t t = r; t < a.tokens; t += kRows) grad_row<T, L, C>(a, t, l, fr, factor);
+}
+
 template <typename T, int L, int C>
 __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a, const Partials w) {
   constexpr int kRows = 256 / L;
@@ -213,36 +300,26 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a, 
 #pragma unroll
   for (int c = 0; c < C; ++c) f[c] = l + L * c < a.experts ? w.f[l + L * c] : 0.0f;
   const float factor = w.f[a.experts];
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + r; t < a.tokens; t += static_cast<int64_t>(gridDim.x) * kRows) {
-    T* out = static_cast<T*>(a.grad) + t * a.ld_grad;
-    const bool live = has_choice<L>(a.index + t * a.top, a.top, l);
-    float p[C];
-    float mean = 0.0f;
-    if (live) {
-      load_row<T, L, C>(static_cast<const T*>(a.logits) + t * a.ld, a.experts, l, p);
-      softmax_row<L, C>(a.experts, l, p);
-#pragma unroll
-      for (int c = 0; c < C; ++c) mean += p[c] * f[c];
-      mean = lanes_sum<L>(mean);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = l + L * c;
-      if (e >= a.experts) continue;
-      float v = live ? factor * (p[c] * (f[c] - mean)) : 0.0f;
-      if (a.accumulate) v += to_f(out[e]);
-      out[e] = static_cast<T>(v);
-    }
-  }
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + r; t < a.tokens; t += static_cast<int64_t>(gridDim.x) * kRows)
+    grad_row<T, L, C>(a, t, l, f, factor);
 }
 
 // Workgroups of the first launch: what they leave is read by one workgroup.
 int groups_of(int64_t tokens) { return static_cast<int>(std::min<int64_t>(512, (tokens + 63) / 64)); }
 
+// One workgroup takes rows in up to kSmall rounds.
+constexpr int64_t kSmall = 4;
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <typename T, int L, int C>
 hipError_t run(const BalanceArgs& a, const Partials& w, hipStream_t s) {
+  if constexpr (C <= 8) {
+    if (a.tokens * L <= kSmall * 1024) {
+      balance_small_kernel<T, L, C><<<1, 1024, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
   if (w.groups) balance_sums_kernel<T, L, C><<<w.groups, 256, 0, s>>>(a, w);
   balance_join_kernel<<<1, 1024, 0, s>>>(a, w);
   if (a.grad && a.tokens) {

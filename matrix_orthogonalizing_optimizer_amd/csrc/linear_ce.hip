@@ -20,7 +20,7 @@ namespace mo {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // dz enters its products as a sum of bf16 terms: one where the gradient is
 // bf16 itself (its rounding, 2^-9 of a value, is of the size of the result's
@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, c
   __shared__ float most[16];
   float m = 0.0f;
   if (g)
-    for (int t = threadIdx.x; t < rows; t += 1024)
-      if (targets[t] >= 0) m = fmaxf(m, fabsf(g[t]));       // NaN is left out
+#pragma unroll 8
+    for (int t = threadIdx.x; t < rows; t += 1024) m = targets[t] >= 0 ? fmaxf(m, fabsf(g[t])) : m;       // NaN is left out
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
   __syncthreads();
@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, c
   for (int i = 1; i < 16; ++i) m = fmaxf(m, most[i]);
   const float s = m > 0.0f && m < INFINITY ? m : 1.0f;
   if (threadIdx.x == 0) *scale = s;
+#pragma unroll 8
   for (int t = threadIdx.x; t < rows; t += 1024) {
     const int64_t y = targets[t];
     const float r = g ? g[t] : 1.0f;
@@ -63,6 +64,15 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, c
 // those whose factor is 0, so that whatever they hold takes no part).  64 rows
 // x 128 columns per workgroup, through LDS; HBM bound.
 constexpr int kPackRows = 64, kPackCols = 128;
+// Eight rows of a column.
+__device__ __forceinline__ u32x4v column8(const uint32_t (&tile)[kPackRows][kPackCols / 2 + 1], int r, int c) {
+  const int shift = (c & 1) * 16;
+  u32x4v v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = ((tile[r + 2 * k][c / 2] >> shift) & 0xffffu) | ((tile[r + 2 * k + 1][c / 2] >> shift) << 16);
+  return v;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
                                                       uint16_t* dst_t, int64_t pitch_t, const float* factor) {
@@ -92,12 +102,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, 
   for (int i = 0; i < 4; ++i) {
     const int u = i * 256 + threadIdx.x, c = u >> 3, r = (u & 7) * 8;       // 8 rows of a column
     if (c0 + c >= cols || r0 + r >= pitch_t) continue;
-    const int shift = (c & 1) * 16;
-    u32x4v v;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = ((tile[r + 2 * k][c / 2] >> shift) & 0xffffu) | ((tile[r + 2 * k + 1][c / 2] >> shift) << 16);
-    *reinterpret_cast<u32x4v*>(dst_t + (c0 + c) * pitch_t + r0 + r) = v;
+    *reinterpret_cast<u32x4v*>(dst_t + (c0 + c) * pitch_t + r0 + r) = column8(tile, r, c);
   }
 }
 
@@ -110,55 +115,67 @@ hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_
 }
 
 // ------------------------------------------------------------ statistics
+// Exponentials are powers of two of z log2(e): a row's reference m is the largest
+// of those products as rounded, sums are of 2^(z log2(e) - m), where a fused
+// multiply-add rounds the difference only.
 struct CeStatsArgs {
   const int64_t* targets;
   int64_t col0;                 // the piece's first column
-  float2* part;                 // [rows][tiles_n WN]: largest logit, sum of exp(z - it)
+  float2* part;                 // [rows][tiles_n]: reference, sum
   float* target_logit;          // written by the tile that holds the row's target
+  float* z;                     // or null: the logits, rows `pitch_z` apart
+  int64_t pitch_z;
 };
 
-template <class C>
-__device__ __forceinline__ float col_mask(const TilePlace& q, int j, int g, int k, float v) {
-  const int c = q.wn * (C::TN / C::WN) + 32 * j + 8 * g + 4 * q.half + k;
-  return c <= q.nlast ? v : -INFINITY;
+// Adds (m2, s2) to (m, s).  References of -inf stand for columns of -inf only.
+__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
+  const float n = fmaxf(m, m2), ref = n == -INFINITY ? 0.0f : n;
+  s = s * __builtin_amdgcn_exp2f(m - ref) + s2 * __builtin_amdgcn_exp2f(m2 - ref);
+  m = n;
 }
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(const ProductArgs p, const CeStatsArgs e) {
+  constexpr int W = C::TN / C::WN;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
   const TilePlace q = tile_place<C>(p);
   f32x16v acc[C::FM][C::FN];
   tile_sums<C>(p, q, smem, acc);
-  const bool edge = (q.wn + 1) * (C::TN / C::WN) > q.nlast + 1;
-  const int64_t cols = static_cast<int64_t>(p.tiles_n) * C::WN, col = static_cast<int64_t>(q.tn) * C::WN + q.wn;
+  if (e.z) {
+    tile_store<C, float>({e.z + e.col0, e.pitch_z, 0, 0, nullptr}, q, smem, acc);
+    __syncthreads();
+  }
+  float2* waves = reinterpret_cast<float2*>(smem);                      // [TM][WN]
+  const int inside = q.nlast + 1 - q.wn * W;                            // of the wave's columns
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
-    if (edge) {
+    if (inside < W) {
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = col_mask<C>(q, j, r / 4, r % 4, acc[i][j][r]);
+        for (int r = 0; r < 16; ++r)
+          if (32 * j + 8 * (r / 4) + 4 * q.half + r % 4 >= inside) acc[i][j][r] = -INFINITY;
     }
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
-    m = fmaxf(m, __uint_as_float(lane_xor32(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(lane_xor32(__float_as_uint(m)))) * kLog2e;
     const float ref = m == -INFINITY ? 0.0f : m;            // columns of -inf alone: a sum of zero
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f((acc[i][j][r] - ref) * kLog2e);
+      for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -ref));
     s += __uint_as_float(lane_xor32(__float_as_uint(s)));
     const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
     const bool in = row <= q.mlast;
     const int64_t t = q.m0 + row;
-    if (in && q.half == 0) e.part[t * cols + col] = make_float2(m, s);
+    if (q.half == 0) waves[row * C::WN + q.wn] = make_float2(m, s);
     // the target's logit, where these columns hold it
-    const int64_t y = in ? e.targets[t] - e.col0 - q.n0 - q.wn * (C::TN / C::WN) : -1;
-    const bool mine = y >= 0 && y < C::TN / C::WN && ((y >> 2) & 1) == q.half && y + q.wn * (C::TN / C::WN) <= q.nlast;
+    const int64_t y = in ? e.targets[t] - e.col0 - q.n0 - q.wn * W : -1;
+    const bool mine = y >= 0 && y < min(W, inside) && ((y >> 2) & 1) == q.half;
     if (__any(mine)) {
       float z = 0.0f;
 #pragma unroll
@@ -169,41 +186,54 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
       if (mine) e.target_logit[t] = z;
     }
   }
+  __syncthreads();
+  for (int row = threadIdx.x; row <= q.mlast; row += C::kThreads) {
+    float2 v = waves[row * C::WN];
+    for (int w = 1; w < C::WN; ++w) join_stats(v.x, v.y, waves[row * C::WN + w].x, waves[row * C::WN + w].y);
+    e.part[(q.m0 + row) * p.tiles_n + q.tn] = v;
+  }
 }
 
-// Joins a piece's statistics with those of the pieces before it, a wave per
-// row; after the last piece the row's {m, 1 / sum} and its loss.
-__global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int64_t cols, int rows, int vocab, int first, int last,
+// Joins a piece's statistics with those of the pieces before it, kJoinLanes
+// threads per row; after the last piece the row's {m, 1 / sum} and its loss.
+template <int kLanes>
+__global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int cols, int rows, int vocab, int first, int last,
                                                       const int64_t* targets, const float* target_logit, float2* stat, float* loss) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= rows) return;
+  __shared__ float2 waves[4];
+  const int lane = threadIdx.x % kLanes;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  const bool in = t < rows;
   float m = -INFINITY, s = 0.0f;
-  auto add = [&](float m2, float s2) __attribute__((always_inline)) {
-    const float n = fmaxf(m, m2), ref = n == -INFINITY ? 0.0f : n;
-    s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - ref) * kLog2e);
-    m = n;
-  };
-  for (int64_t c = lane; c < cols; c += 64) {
-    const float2 v = part[t * cols + c];
-    add(v.x, v.y);
-  }
-  for (int o = 1; o < 64; o <<= 1) {
+  if (in)
+#pragma unroll 4
+    for (int c = lane; c < cols; c += kLanes) {
+      const float2 v = part[t * cols + c];
+      join_stats(m, s, v.x, v.y);
+    }
+  // a tree whose two sides always add in the same order
+#pragma unroll
+  for (int o = 1; o < (kLanes < 64 ? kLanes : 64); o <<= 1) {
     const float m2 = __shfl_xor(m, o, 64), s2 = __shfl_xor(s, o, 64);
-    const float a = m, b = s;
-    // both lanes of a pair add in the same order
     const bool low = (lane & o) == 0;
-    m = low ? a : m2;
-    s = low ? b : s2;
-    add(low ? m2 : a, low ? s2 : b);
+    float a = low ? m : m2, b = low ? s : s2;
+    join_stats(a, b, low ? m2 : m, low ? s2 : s);
+    m = a;
+    s = b;
   }
+  if constexpr (kLanes == 256) {
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = make_float2(m, s);
+    __syncthreads();
+    m = waves[0].x;
+    s = waves[0].y;
+    for (int w = 1; w < 4; ++w) join_stats(m, s, waves[w].x, waves[w].y);
+  }
+  if (!in || lane) return;
   if (!first) {
-    const float2 v = stat[t];
-    const float a = m, b = s;
+    float2 v = stat[t];
+    join_stats(v.x, v.y, m, s);
     m = v.x;
     s = v.y;
-    add(a, b);
   }
-  if (lane) return;
   if (!last) {
     stat[t] = make_float2(m, s);
     return;
@@ -212,7 +242,7 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int64_
   const bool none = m == -INFINITY;
   stat[t] = make_float2(m, none ? NAN : 1.0f / s);
   const int64_t y = targets[t];
-  loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + (m - target_logit[t]);
+  loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + __builtin_fmaf(-target_logit[t], kLog2e, m) * kLn2;
 }
 
 // ------------------------------------------------------------ dz
@@ -254,7 +284,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
-        float v = __builtin_amdgcn_exp2f((acc[i][j][r] - st.x) * kLog2e) * inv;
+        float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -st.x)) * inv;
         v = f * (c == hot ? v - 1.0f : v);
         if (f == 0.0f || (edge && q.wn * W + c > q.nlast)) v = 0.0f;
         acc[i][j][r] = v;
@@ -309,6 +339,57 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
   }
 }
 
+// The same from kept logits: 64 rows x 128 columns per workgroup; HBM bound.
+__global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, const float* z, int rows, int vocab) {
+  __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kPackRows, c0 = static_cast<int64_t>(blockIdx.x) * kPackCols;
+  const int cl = (threadIdx.x & 15) * 8, rl = threadIdx.x >> 4;
+  const int64_t c = c0 + cl;
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = r0 + rl + 16 * i;
+    const bool in = t < rows && c < vocab;
+    f32x4v lo = {}, hi = {};
+    if (in) {
+      lo = *reinterpret_cast<const f32x4v*>(z + t * e.vp + c);
+      hi = *reinterpret_cast<const f32x4v*>(z + t * e.vp + c + 4);
+    }
+    const float f = in ? e.factor[t] : 0.0f;
+    const float2 st = in ? e.stat[t] : make_float2(0.0f, 0.0f);
+    const int64_t y = in ? e.targets[t] - c : -1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float x = __builtin_amdgcn_exp2f(__builtin_fmaf(k < 4 ? lo[k] : hi[k - 4], kLog2e, -st.x)) * st.y;
+      x = f * (k == y ? x - 1.0f : x);
+      v[i][k] = f == 0.0f || c + k >= vocab ? 0.0f : x;
+    }
+  }
+  for (int term = 0; term < max(e.terms_x, e.terms_w); ++term) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = r0 + rl + 16 * i;
+      const u32x4v h = {pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]), pack_bf16x2(v[i][4], v[i][5]), pack_bf16x2(v[i][6], v[i][7])};
+      if (e.dz && term < e.terms_x && t < rows && c < e.vp) *reinterpret_cast<u32x4v*>(e.dz + (t * e.terms_x + term) * e.vp + c) = h;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        tile[rl + 16 * i][cl / 2 + k] = h[k];
+        v[i][2 * k] -= __uint_as_float(h[k] << 16);
+        v[i][2 * k + 1] -= __uint_as_float(h[k] & 0xffff0000u);
+      }
+    }
+    if (!e.dz_t || term >= e.terms_w) continue;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = i * 256 + threadIdx.x, cc = u >> 3, r = (u & 7) * 8;
+      if (c0 + cc < vocab && r0 + r < e.tp)
+        *reinterpret_cast<u32x4v*>(e.dz_t + ((c0 + cc) * e.terms_w + term) * e.tp + r0 + r) = column8(tile, r, cc);
+    }
+    __syncthreads();
+  }
+}
+
 // dx = scale times the sum of the splits' parts, 0 in rows that take no part.
 template <typename T>
 __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t n, int rows, int hidden, const float* scale,
@@ -328,7 +409,9 @@ struct Plan {
   int64_t vf, vb;              // columns of a forward and of a backward piece
   int splits, tile_dx;         // of the product for dx
   int terms_x, terms_w;
-  size_t part, stat, zt, factor, scale, x, w, x_t, w_t, dz, dz_t, dxp, total;
+  bool keep;                   // all logits are one piece, which stays
+  int64_t vz;                  // columns of a piece of dz, padded
+  size_t part, stat, zt, factor, scale, x, w, x_t, w_t, z, dz, dz_t, dxp, total;
 };
 
 // Pieces of at most `most` columns, of about equal length, in whole tiles.
@@ -376,14 +459,20 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   Plan p{};
   p.hp = up(hidden, 64);
   p.tp = up(rows, 64);
-  p.terms_x = terms_of(x_dt);
-  p.terms_w = terms_of(dw_dt);
-  // dz and its transpose stay near 2^26 elements each and a piece's weights
-  // within 2^27
-  const int64_t fit = std::min((int64_t{1} << 26) / std::max<int64_t>(rows, 1), (int64_t{1} << 27) / p.hp);
-  p.vb = piece_of(vocab, std::min(std::max(fit / 256 * 256, int64_t{1024}), int64_t{1} << 20));
+  p.terms_x = dx ? terms_of(x_dt) : 0;
+  p.terms_w = dw ? terms_of(dw_dt) : 0;
+  // A piece's dz and its transpose stay near 256 MiB in all, its weights and their
+  // transpose near 128 each: large enough for whole rounds of tiles.  Where 256
+  // MiB hold the logits of the whole vocabulary, they are a single piece, which
+  // stays in fp32 between the statistics and dz instead of being multiplied again.
+  const int64_t r = std::max<int64_t>(rows, 1), vocab_p = up(vocab, 64);
+  p.keep = (dx || dw) && vocab_p <= (int64_t{1} << 21) && r <= (int64_t{1} << 26) / vocab_p;
+  const int64_t terms = std::max(p.terms_x + p.terms_w, 2);
+  const int64_t by_w = (int64_t{1} << 26) / p.hp, by_z = p.keep ? by_w : (int64_t{1} << 27) / (terms * r);
+  p.vb = piece_of(vocab, std::min(std::max(std::min(by_w, by_z) / 256 * 256, int64_t{1024}), int64_t{1} << 20));
+  p.vz = p.keep ? vocab_p : p.vb;
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
-  const Choice of_dx = choose(rows, hidden, p.vb / 32 * p.terms_x, true);
+  const Choice of_dx = choose(rows, hidden, p.vb / 32 * (p.keep ? 1 : p.terms_x), true);
   p.splits = of_dx.splits;
   p.tile_dx = of_dx.tile;
   size_t at = 0;
@@ -393,7 +482,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
     return o;
   };
   const size_t t = static_cast<size_t>(rows);
-  p.part = take(t * static_cast<size_t>(up(std::max(p.vf, p.vb), 256) / 32) * 8);
+  p.part = take(t * static_cast<size_t>(up(std::max(p.vf, p.vb), 256) / 64) * 8);
   p.stat = take(t * 8);
   p.zt = take(t * 4);
   p.factor = take(t * 4);
@@ -402,8 +491,9 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.w = take(static_cast<size_t>(p.vb) * p.hp * 2);
   if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.tp * 2);
   if (dx) p.w_t = take(static_cast<size_t>(hidden) * p.vb * 2);
-  if (dx) p.dz = take(t * p.vb * 2 * p.terms_x);
-  if (dw) p.dz_t = take(static_cast<size_t>(p.vb) * p.tp * 2 * p.terms_w);
+  if (p.keep) p.z = take(t * p.vz * 4);
+  if (dx) p.dz = take(t * p.vz * 2 * p.terms_x);
+  if (dw) p.dz_t = take(static_cast<size_t>(p.vz) * p.tp * 2 * p.terms_w);
   if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * hidden * 4);
   p.total = rows ? at : 0;
   return p;
@@ -417,9 +507,9 @@ dim3 tiles_of(ProductArgs& p) {
 }
 
 template <class C>
-hipError_t run_stats(ProductArgs p, const CeStatsArgs& e, int64_t& cols, hipStream_t s) {
+hipError_t run_stats(ProductArgs p, const CeStatsArgs& e, int& cols, hipStream_t s) {
   const dim3 g = tiles_of<C>(p);
-  cols = static_cast<int64_t>(p.tiles_n) * C::WN;
+  cols = p.tiles_n;
   ce_stats_kernel<C><<<g, C::kThreads, 0, s>>>(p, e);
   return hipGetLastError();
 }
@@ -462,6 +552,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   uint16_t* dz = want_dx ? reinterpret_cast<uint16_t*>(base + pl.dz) : nullptr;
   uint16_t* dz_t = want_dw ? reinterpret_cast<uint16_t*>(base + pl.dz_t) : nullptr;
   float* dxp = want_dx ? reinterpret_cast<float*>(base + pl.dxp) : nullptr;
+  float* z = pl.keep ? reinterpret_cast<float*>(base + pl.z) : nullptr;
 
   // operands that the products can read in place
   auto plain = [&](const void* q, int dt, int64_t ld) {
@@ -484,48 +575,67 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
 
   auto weights = [&](int64_t v0) { return static_cast<const uint8_t*>(a.w) + v0 * a.ldw * esz_w; };
   const int64_t vf = plain_w ? pl.vf : pl.vb;
+  const bool once = pl.keep && vf >= a.vocab && pl.vb >= a.vocab;      // one piece of weights, too: its transpose comes with it
   for (int64_t v0 = 0; v0 < a.vocab; v0 += vf) {
     const int v = static_cast<int>(std::min<int64_t>(vf, a.vocab - v0));
-    if (!plain_w) MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, wb, pl.hp, nullptr, 0, nullptr, s));
+    if (!plain_w || (once && want_dx))
+      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb, pl.hp, once ? w_t : nullptr, up(v, 64), nullptr, s));
     logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
     logits.n = v;
-    const CeStatsArgs e{a.targets, v0, part, zt};
-    int64_t cols;
+    const CeStatsArgs e{a.targets, v0, part, zt, z, pl.vz};
+    int cols;
     const int tile = choose(a.rows, v, logits.stages, false).tile;
     if (tile == 256) MO_TRY(run_stats<Cfg256>(logits, e, cols, s));
     else if (tile == 128) MO_TRY(run_stats<Cfg128>(logits, e, cols, s));
     else MO_TRY(run_stats<Cfg64>(logits, e, cols, s));
-    ce_join_kernel<<<(a.rows + 3) / 4, 256, 0, s>>>(part, cols, a.rows, a.vocab, v0 == 0,
+    const auto join = cols > 256 ? ce_join_kernel<256> : ce_join_kernel<16>;
+    const int per = cols > 256 ? 1 : 16;
+    join<<<(a.rows + per - 1) / per, 256, 0, s>>>(part, cols, a.rows, a.vocab, v0 == 0,
                                                     v0 + v >= a.vocab, a.targets, zt, stat, a.loss);
     MO_TRY(hipGetLastError());
   }
   if (!grad) return hipSuccess;
 
+  if (pl.keep) {
+    const dim3 g(static_cast<uint32_t>((a.vocab + kPackCols - 1) / kPackCols), static_cast<uint32_t>((a.rows + kPackRows - 1) / kPackRows));
+    ce_kept_grad_kernel<<<g, 256, 0, s>>>({a.targets, 0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(pl.vz), static_cast<int>(pl.tp)},
+                                          z, a.rows, a.vocab);
+    MO_TRY(hipGetLastError());
+  }
   for (int64_t v0 = 0; v0 < a.vocab; v0 += pl.vb) {
     const int v = static_cast<int>(std::min<int64_t>(pl.vb, a.vocab - v0));
     const int64_t vp = up(v, 64);
-    if (!plain_w || want_dx) MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb, pl.hp, w_t, vp, nullptr, s));
-    logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
-    logits.n = v;
-    const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp)};
-    const int tile = choose(a.rows, v, logits.stages, false).tile;
-    MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
+    const bool need_w = !pl.keep && !plain_w, need_w_t = want_dx && !once;
+    if (need_w || need_w_t)
+      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.hp, need_w_t ? w_t : nullptr, vp, nullptr, s));
+    if (!pl.keep) {
+      logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
+      logits.n = v;
+      const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp)};
+      const int tile = choose(a.rows, v, logits.stages, false).tile;
+      MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
+    }
     if (want_dx) {
+      // a piece's terms lie side by side along the contraction, those of kept
+      // logits a whole row apart
+      const int64_t pitch = pl.keep ? pl.vz : vp;
       ProductArgs p{};
-      p.a = reinterpret_cast<const uint8_t*>(dz);
       p.b = reinterpret_cast<const uint8_t*>(w_t);
-      p.pitch_a = static_cast<uint32_t>(vp * 2 * pl.terms_x);
+      p.pitch_a = static_cast<uint32_t>(pitch * 2 * pl.terms_x);
       p.pitch_b = static_cast<uint32_t>(vp * 2);
       p.m = a.rows;
       p.n = a.hidden;
       p.stages_b = static_cast<int>(vp / 32);
-      p.stages = p.stages_b * pl.terms_x;
+      p.stages = p.stages_b * (pl.keep ? 1 : pl.terms_x);
       p.splits = pl.splits;
-      MO_TRY((store<float>(pl.tile_dx, p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0, nullptr}, s)));
+      for (int term = 0; term < (pl.keep ? pl.terms_x : 1); ++term) {
+        p.a = reinterpret_cast<const uint8_t*>(dz + (pl.keep ? term * pitch + v0 : 0));
+        MO_TRY((store<float>(pl.tile_dx, p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0 || term > 0, nullptr}, s)));
+      }
     }
     if (want_dw) {
       ProductArgs p{};
-      p.a = reinterpret_cast<const uint8_t*>(dz_t);
+      p.a = reinterpret_cast<const uint8_t*>(dz_t + (pl.keep ? v0 * pl.terms_w * pl.tp : 0));
       p.b = reinterpret_cast<const uint8_t*>(x_t);
       p.pitch_a = static_cast<uint32_t>(pl.tp * 2 * pl.terms_w);
       p.pitch_b = static_cast<uint32_t>(pl.tp * 2);
