@@ -467,12 +467,12 @@ int mo_distill_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, 
  * Quantisation: a = the block's largest |x|; e = the smallest integer with a
  * <= 448 2^e, at least -127 (byte 0 for a = 0); code = x 2^-e rounded to
  * nearest, halfway cases to even (what would round to 2^128, beyond fp32, to
- * 248 2^120).  With square scales a is the largest of 128
- * rows x 128 columns (rows 128 i .. 128 i + 127), so that the image of the
- * transpose holds the same values: the form for weights, whose gradients then
- * belong to the values that the forward pass multiplied.  A block that holds a
- * NaN or an infinity gets scale byte 255 and zero codes: its values read back
- * as NaN, and so does every product they enter.
+ * 240 2^120).  With square scales a is the largest of 128 rows x 128 columns
+ * (rows 128 i .. 128 i + 127), so that the image of the transpose holds the
+ * same values: the form for weights, whose gradients then belong to the values
+ * that the forward pass multiplied.  A block that holds a NaN or an infinity
+ * gets scale byte 255 and zero codes: its values read back as NaN, and so does
+ * every product they enter.
  * ---------------------------------------------------------------------- */
 typedef struct mo_fp8_image {
     const void* codes;
@@ -516,7 +516,10 @@ int mo_fp8_dequantize(const mo_fp8_image* images, void* const* dst, int64_t coun
 /* out[m, n] = sum_k a[m, k] b[n, k] over the values of two images with the
  * same cols (a [M, K], b [N, K]), + out[m, n] when accumulate != 0.
  * Products enter fp32 sums on the matrix cores; the result (after the
- * accumulation) is rounded once to out_dtype (MO_F32 or MO_BF16).  out: rows
+ * accumulation) is rounded once to out_dtype (MO_F32 or MO_BF16).  For MO_F32
+ * the products are exact (values below 2^-126 count as zero); for MO_BF16 they
+ * come from the 8-bit matrix instruction, which drops what lies about 2^-15
+ * below the largest of the up to 16 products that it adds at a time.  out: rows
  * ldo elements apart (ldo >= N), aligned to its element; columns N .. ldo - 1
  * are left as they were.  out may not overlap an image.  Results do not
  * depend on the run (no atomics).  K <= 2^23 (K = 0: zeros) and ceil(M / 64)
@@ -532,7 +535,7 @@ int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int o
  *   dz_tv   = g_t (exp(z_tv) / sum_v exp(z_tv) - [v = y_t]),
  *   dx = dz w,   dw = dz^T x  (+ dw when accumulate != 0).
  * The products take bf16 operands: x and w given in fp32 are rounded to bf16
- * on the way.  Sums and the softmax's statistics are fp32.  dz enters the
+ * on the way (values below 2^-126 count as zero).  Sums and the softmax's statistics are fp32.  dz enters the
  * products for a bf16 gradient rounded to bf16 (relative to the largest |g|),
  * for an fp32 gradient as a sum of three bf16 terms.  Each gradient is rounded
  * once to its type (after the accumulation).  Results do not depend on the run

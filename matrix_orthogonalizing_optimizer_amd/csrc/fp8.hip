@@ -25,9 +25,9 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   return e > 8u ? e - 8u : 0u;
 }
 
-// The largest magnitude that does not round to 2^128 (under the largest scale,
-// 2^120, codes are steps of 8 here).
-__device__ __forceinline__ float clip(float x) { return __builtin_amdgcn_fmed3f(x, -0x1.fp127f, 0x1.fp127f); }
+// Under the largest scale, 2^120, the next number after 240 2^120 is 2^128, past
+// fp32: what would round there stays below it.
+__device__ __forceinline__ float clip(float x) { return __builtin_amdgcn_fmed3f(x, -0x1.ep127f, 0x1.ep127f); }
 
 // Four codes from four elements under the scale, element 0 lowest.
 __device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, float s) {
