@@ -34,8 +34,8 @@ from typing import Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
-from ._lib import (KERNEL_CLASS_NAMES, MO_BF16, MO_F32, MO_MAX_TOP, MoFp8Image,  # noqa: F401
-                   MoFp8Item, MoMatrix, MoMx4Image, MoMx4Item, MoTensor, MuonError, check, last_error, lib)
+from ._lib import (KERNEL_CLASS_NAMES, MO_BF16, MO_F32, MO_MAX_TOP, MoMatrix, MoMx4Image,  # noqa: F401
+                   MoMx4Item, MoTensor, MuonError, check, last_error, lib)
 
 __all__ = ["muon_step", "adamw_step", "newton_schulz", "muon_workspace_size",
            "newton_schulz_workspace_size", "svd_entropy", "svd_entropy_workspace_size",
@@ -657,9 +657,10 @@ class Fp8Matrix:
     """The 8-bit image of a [rows, cols] matrix with a scale per block of 128:
     ``codes`` uint8 [rows, 128 nb] (e4m3) and ``scales`` uint8 [rows, 16 ceil(nb
     / 16)] with nb = ceil(cols / 128) blocks per row, as ``include/muon.h`` lays
-    them out.  Rows or columns may be none."""
+    them out.  Rows or columns may be none.  Both arrays, and those of a list's
+    images, may share one allocation, which lives as long as any of them."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("rows", "cols", "_keep", "_at", "_codes", "_scales", "_ptrs")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         if codes.dim() != 2:
@@ -673,7 +674,26 @@ class Fp8Matrix:
                                  f"[{rows}, {w}], got {t.dtype} {tuple(t.shape)}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must share a device")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, int(cols)
+        self.rows, self.cols = rows, int(cols)
+        self._keep, self._at, self._codes, self._scales = (codes, scales), None, codes, scales
+        self._ptrs = (codes.data_ptr(), scales.data_ptr())
+
+    # The arrays of an image that was made here are cut out of their allocation
+    # when they are asked for: the operators only need their addresses.
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            at, w = self._at, -(-self.cols // 128) * 128
+            self._codes = self._keep[0][at:at + self.rows * w].view(self.rows, w)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            nb = -(-self.cols // 128)
+            at, w = self._at + self.rows * 128 * nb, -(-nb // 16) * 16
+            self._scales = self._keep[0][at:at + self.rows * w].view(self.rows, w)
+        return self._scales
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -681,25 +701,41 @@ class Fp8Matrix:
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self._keep[0].device
 
     @classmethod
     def empty(cls, rows: int, cols: int, device) -> "Fp8Matrix":
         """An image whose contents are still to be written."""
         if rows < 0 or cols < 0:
             raise ValueError(f"rows and columns must not be negative, got [{rows}, {cols}]")
-        nb = -(-cols // 128)
-        q = object.__new__(cls)                 # right by construction: no checks
-        q.codes = torch.empty((rows, 128 * nb), dtype=torch.uint8, device=device)
-        q.scales = torch.empty((rows, -(-nb // 16) * 16), dtype=torch.uint8, device=device)
-        q.rows, q.cols = rows, cols
-        return q
+        return cls._empty([(rows, cols)], device)[0]
 
-    def _struct(self) -> MoFp8Image:
-        return MoFp8Image(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+    @classmethod
+    def _empty(cls, shapes, device) -> List["Fp8Matrix"]:
+        total, ats, sizes = 0, [], []
+        for rows, cols in shapes:
+            nb = -(-cols // 128)
+            codes = rows * 128 * nb
+            ats.append(total)
+            sizes.append(codes)
+            total += (codes + rows * (-(-nb // 16) * 16) + 255) & ~255
+        buf = torch.empty(total, dtype=torch.uint8, device=device)
+        base, keep, made = buf.data_ptr(), (buf,), []
+        for (rows, cols), at, codes in zip(shapes, ats, sizes):
+            q = object.__new__(cls)             # right by construction: no checks
+            q.rows, q.cols, q._keep, q._at, q._codes, q._scales = rows, cols, keep, at, None, None
+            q._ptrs = (base + at, base + at + codes)
+            made.append(q)
+        return made
+
+    def _struct(self):
+        return (ctypes.c_int64 * 4)(*self._ptrs, self.rows, self.cols)     # mo_fp8_image
 
     def __repr__(self) -> str:
         return f"Fp8Matrix([{self.rows}, {self.cols}], device={self.device})"
+
+
+_NO_IMAGE = (0, 0)
 
 
 def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str = "rows",
@@ -725,7 +761,7 @@ def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str 
     dt = _dtype_code(_common_dtype(xs, "x"), "x")
     dev = xs[0].device
     views = [_rows_of(t, "x") for t in xs]
-    given = []                                   # (image, transposed image) of each matrix
+    given, used = [], xs                         # images in the matrices' order, each one's then its transpose's
     if outs is not None:
         for (_, r, c, _), o in zip(views, outs):
             pair = tuple(o) if images == "both" else (o, None) if images == "rows" else (None, o)
@@ -738,21 +774,29 @@ def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str 
                     raise ValueError(f"out: expected an image of {shape}, got {q.shape}")
             if (images != "cols" and pair[0] is None) or (images != "rows" and pair[1] is None):
                 raise ValueError("out lacks an image")
-            given.append(pair)
-    used = xs + [t for p in given for q in p if q is not None for t in (q.codes, q.scales)]
+            given += [q for q in pair if q is not None]
+        used = xs + [t for q in given for t in q._keep]
     with _launch_on(dev, stream, used) as handle:
         if outs is None:
-            given = [(Fp8Matrix.empty(r, c, dev) if images != "cols" else None,
-                      Fp8Matrix.empty(c, r, dev) if images != "rows" else None) for _, r, c, _ in views]
-        arr = (MoFp8Item * len(xs))()
-        for it, (ptr, r, c, ld), (q, qt) in zip(arr, views, given):
-            it.src, it.rows, it.cols, it.ld = ptr, r, c, ld
-            if q is not None:
-                it.codes, it.scales = q.codes.data_ptr(), q.scales.data_ptr()
-            if qt is not None:
-                it.codes_t, it.scales_t = qt.codes.data_ptr(), qt.scales.data_ptr()
-        check(lib().mo_fp8_quantize(arr, len(xs), dt, int(square), handle))
-    res = [p if images == "both" else p[0] if images == "rows" else p[1] for p in given]
+            shapes = []
+            for _, r, c, _ in views:
+                if images != "cols":
+                    shapes.append((r, c))
+                if images != "rows":
+                    shapes.append((c, r))
+            given = Fp8Matrix._empty(shapes, dev)
+        flat = []                                # mo_fp8_item: src, codes, scales, codes_t, scales_t, rows, cols, ld
+        step = 2 if images == "both" else 1
+        for i, (ptr, r, c, ld) in enumerate(views):
+            q = given[i * step]._ptrs
+            if images == "both":
+                flat += (ptr, *q, *given[i * step + 1]._ptrs, r, c, ld)
+            elif images == "rows":
+                flat += (ptr, *q, *_NO_IMAGE, r, c, ld)
+            else:
+                flat += (ptr, *_NO_IMAGE, *q, r, c, ld)
+        check(lib().mo_fp8_quantize((ctypes.c_int64 * len(flat))(*flat), len(xs), dt, int(square), handle))
+    res = list(zip(given[::2], given[1::2])) if images == "both" else given
     return res[0] if single else res
 
 
@@ -765,11 +809,11 @@ def fp8_dequantize(q: Union[Fp8Matrix, Sequence[Fp8Matrix]], *, dtype: torch.dty
     if not qs:
         return []
     dev = qs[0].device
-    with _launch_on(dev, stream, [t for i in qs for t in (i.codes, i.scales)]) as handle:
-        res = [torch.empty(i.shape, dtype=dtype, device=dev) for i in qs]
-        arr = (MoFp8Image * len(qs))(*[i._struct() for i in qs])
-        ptrs = (ctypes.c_void_p * len(qs))(*[t.data_ptr() for t in res])
-        check(lib().mo_fp8_dequantize(arr, ptrs, len(qs), dt, handle))
+    with _launch_on(dev, stream, [t for i in qs for t in i._keep]) as handle:
+        res = [torch.empty((i.rows, i.cols), dtype=dtype, device=dev) for i in qs]
+        flat = [v for i in qs for v in (*i._ptrs, i.rows, i.cols)]         # mo_fp8_image
+        ptrs = (ctypes.c_int64 * len(qs))(*[t.data_ptr() for t in res])
+        check(lib().mo_fp8_dequantize((ctypes.c_int64 * len(flat))(*flat), ptrs, len(qs), dt, handle))
     return res[0] if single else res
 
 
@@ -777,22 +821,25 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfl
                out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
     """``a b^T`` over the values of two images with equal columns
     (``mo_fp8_matmul``): a [M, K], b [N, K] give [M, N], fp32 sums rounded
-    once.  ``out``: written instead of a new tensor (its dtype counts, rows
-    may be strided); with ``accumulate`` the product is added to it."""
+    once; fp32 results from exact products, bf16 ones from the 8-bit matrix
+    instruction.  ``out``: written instead of a new tensor (its dtype counts,
+    rows may be strided); with ``accumulate`` the product is added to it."""
     if not isinstance(a, Fp8Matrix) or not isinstance(b, Fp8Matrix):
         raise TypeError("a and b must be Fp8Matrix")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     dt = _dtype_code(out_dtype if out is None else out.dtype, "out")
-    used = [a.codes, a.scales, b.codes, b.scales, out]
-    with _launch_on(a.device, stream, used) as handle:
+    dev = a.device
+    used = [*a._keep, *b._keep, out]
+    with _launch_on(dev, stream, used) as handle:
         if out is None:
-            out = torch.empty(a.rows, b.rows, dtype=out_dtype, device=a.device)
-        ptr, r, c, ld = _rows_of(out, "out")
-        if (r, c) != (a.rows, b.rows):
-            raise ValueError(f"out must be [{a.rows}, {b.rows}], got [{r}, {c}]")
-        sa, sb = a._struct(), b._struct()
-        check(lib().mo_fp8_matmul(ctypes.byref(sa), ctypes.byref(sb), ptr, dt, ld, int(accumulate), handle))
+            out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=dev)
+            ptr, ld = out.data_ptr(), max(b.rows, 1)
+        else:
+            ptr, r, c, ld = _rows_of(out, "out")
+            if (r, c) != (a.rows, b.rows):
+                raise ValueError(f"out must be [{a.rows}, {b.rows}], got [{r}, {c}]")
+        check(lib().mo_fp8_matmul(a._struct(), b._struct(), ptr, dt, ld, int(accumulate), handle))
     return out
 
 

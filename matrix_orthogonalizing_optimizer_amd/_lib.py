@@ -118,10 +118,11 @@ _SIGS = {
                                    _c.c_float, _P, _P, _P, _c.c_int64, _P, _c.c_size_t, _P]),
     "mo_fp8_image_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.POINTER(_c.c_size_t),
                                      _c.POINTER(_c.c_size_t)]),
-    "mo_fp8_quantize": (_c.c_int, [_c.POINTER(MoFp8Item), _c.c_int64, _c.c_int, _c.c_int, _P]),
-    "mo_fp8_dequantize": (_c.c_int, [_c.POINTER(MoFp8Image), _c.POINTER(_P), _c.c_int64, _c.c_int, _P]),
-    "mo_fp8_matmul": (_c.c_int, [_c.POINTER(MoFp8Image), _c.POINTER(MoFp8Image), _P, _c.c_int,
-                                 _c.c_int64, _c.c_int, _P]),
+    # items, images and destinations as any array of 64-bit values: filling a flat one costs a
+    # third of setting fields
+    "mo_fp8_quantize": (_c.c_int, [_P, _c.c_int64, _c.c_int, _c.c_int, _P]),
+    "mo_fp8_dequantize": (_c.c_int, [_P, _P, _c.c_int64, _c.c_int, _P]),
+    "mo_fp8_matmul": (_c.c_int, [_P, _P, _P, _c.c_int, _c.c_int64, _c.c_int, _P]),
     "mo_linear_ce_workspace_size": (_c.c_int, [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int,
                                                _c.c_int, _c.c_int, _c.POINTER(_c.c_size_t)]),
     "mo_linear_ce": (_c.c_int, [_P, _c.c_int, _c.c_int64, _P, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64,
