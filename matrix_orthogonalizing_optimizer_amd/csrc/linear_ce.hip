@@ -20,6 +20,8 @@ namespace mo {
 
 namespace {
 
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // dz enters its products as a sum of bf16 terms: one where the gradient is
@@ -259,16 +261,22 @@ struct CeGradArgs {
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(const ProductArgs p, const CeGradArgs e) {
-  constexpr int W = C::TN / C::WN, kPitch = C::kTurnPitch, kLanes = W / 4;
-  // columns of 32 rows' bf16, with padding against bank conflicts
-  constexpr int kPitchT = 80;
-  static_assert(W * kPitchT <= 32 * kPitch, "the wave's place holds the transpose too");
+  constexpr int W = C::TN / C::WN;
+  // places of a wave's 32 rows in LDS: rows of W bf16, and columns of 32, with
+  // padding against bank conflicts
+  constexpr int kPitch = W * 2 + 16, kPitchT = 80, kPlace = 32 * kPitch > W * kPitchT ? 32 * kPitch : W * kPitchT;
+  static_assert(C::NW * kPlace <= C::kLds, "they fit the ring's place");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
   const TilePlace q = tile_place<C>(p);
   f32x16v acc[C::FM][C::FN];
   tile_sums<C>(p, q, smem, acc);
-  uint8_t* turn = smem + (q.wm * C::WN + q.wn) * 32 * kPitch;
-  const bool edge = (q.wn + 1) * W > q.nlast + 1;
+  uint8_t* turn = smem + (q.wm * C::WN + q.wn) * kPlace;
+  const int inside = q.nlast + 1 - q.wn * W;                            // of the wave's columns
+  const int terms = max(e.terms_x, e.terms_w);
+  const bool odd = q.lane & 1;
+  // rows r and r + 1 of a column: an even lane takes its own and its neighbour's
+  // first column of a pair, an odd lane their second
+  const uint32_t pick = odd ? 0x07060302u : 0x01000504u;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
     const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
@@ -278,45 +286,51 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
     const float2 st = e.stat[t];
     const int64_t y = e.targets[t] - e.col0 - q.n0 - q.wn * W;
     const int hot = y >= 0 && y < W ? static_cast<int>(y) : -1;
-    const float inv = f == 0.0f ? 0.0f : st.y;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
-        float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -st.x)) * inv;
+        float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -st.x)) * st.y;
         v = f * (c == hot ? v - 1.0f : v);
-        if (f == 0.0f || (edge && q.wn * W + c > q.nlast)) v = 0.0f;
-        acc[i][j][r] = v;
+        acc[i][j][r] = f == 0.0f || c >= inside ? 0.0f : v;
       }
-    for (int term = 0; term < max(e.terms_x, e.terms_w); ++term) {
+    for (int term = 0; term < terms; ++term) {
       // bf16 terms, largest first: what is left goes to the next
-      if (e.dz && term < e.terms_x) {
+      uint32_t u[C::FN][8];                                             // columns 2 k, 2 k + 1 of the lane's
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          u[j][k] = pack_bf16x2(acc[i][j][2 * k], acc[i][j][2 * k + 1]);
+          acc[i][j][2 * k] -= __uint_as_float(u[j][k] << 16);
+          acc[i][j][2 * k + 1] -= __uint_as_float(u[j][k] & 0xffff0000u);
+        }
+      if (term < e.terms_x) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<f32x4v*>(turn + q.r32 * kPitch + (32 * j + 8 * g + 4 * q.half) * 4) =
-                f32x4v{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            *reinterpret_cast<u32x2v*>(turn + q.r32 * kPitch + (32 * j + 8 * g + 4 * q.half) * 2) = u32x2v{u[j][2 * g], u[j][2 * g + 1]};
         wave_order();
+        constexpr int kLanes = W / 8;                                   // to a row
 #pragma unroll
         for (int k = 0; k < 32 * kLanes / 64; ++k) {
-          const int lr = k * (64 / kLanes) + q.lane / kLanes, lc = q.lane % kLanes * 4;
-          const f32x4v v = *reinterpret_cast<const f32x4v*>(turn + lr * kPitch + lc * 4);
+          const int lr = k * (64 / kLanes) + q.lane / kLanes, lc = q.lane % kLanes * 8;
+          const u32x4v v = *reinterpret_cast<const u32x4v*>(turn + lr * kPitch + lc * 2);
           const int64_t rr = q.wm * (C::TM / C::WM) + 32 * i + lr, cc = q.n0 + q.wn * W + lc;
-          if (rr <= q.mlast && cc < e.vp)
-            *reinterpret_cast<uint2*>(e.dz + ((q.m0 + rr) * e.terms_x + term) * e.vp + cc) =
-                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          if (rr <= q.mlast && cc < e.vp) *reinterpret_cast<u32x4v*>(e.dz + ((q.m0 + rr) * e.terms_x + term) * e.vp + cc) = v;
         }
         wave_order();
       }
-      if (e.dz_t && term < e.terms_w) {
+      if (term < e.terms_w) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
-            *reinterpret_cast<uint16_t*>(turn + c * kPitchT + q.r32 * 2) = static_cast<uint16_t>(pack_bf16x2(acc[i][j][r], acc[i][j][r]));
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(u[j][k]), 0xB1, 0xf, 0xf, true));   // lanes 1 0 3 2
+            const int c = 32 * j + 8 * (k / 2) + 4 * q.half + 2 * (k % 2) + (odd ? 1 : 0);
+            *reinterpret_cast<uint32_t*>(turn + c * kPitchT + (q.r32 >> 1) * 4) = __builtin_amdgcn_perm(u[j][k], other, pick);
           }
         wave_order();
 #pragma unroll
@@ -324,16 +338,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
           const int c = k * 16 + q.lane / 4, ch = q.lane % 4;
           const u32x4v v = *reinterpret_cast<const u32x4v*>(turn + c * kPitchT + ch * 16);
           const int64_t cc = q.wn * W + c, rr = q.m0 + q.wm * (C::TM / C::WM) + 32 * i + ch * 8;
-          if (cc <= q.nlast && rr < e.tp)
-            *reinterpret_cast<u32x4v*>(e.dz_t + ((q.n0 + cc) * e.terms_w + term) * e.tp + rr) = v;
+          if (cc <= q.nlast && rr < e.tp) *reinterpret_cast<u32x4v*>(e.dz_t + ((q.n0 + cc) * e.terms_w + term) * e.tp + rr) = v;
         }
         wave_order();
-      }
-      if (term + 1 < max(e.terms_x, e.terms_w)) {
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] -= bf2f(static_cast<uint16_t>(pack_bf16x2(acc[i][j][r], acc[i][j][r])));
       }
     }
   }
@@ -390,16 +397,30 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
   }
 }
 
-// dx = scale times the sum of the splits' parts, 0 in rows that take no part.
+// dx = scale times the sum of the splits' parts, 0 in rows that take no part: a
+// workgroup per row.
 template <typename T>
-__global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t n, int rows, int hidden, const float* scale,
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t n, int hidden, const float* scale,
                                                         const float* factor, T* dx, int64_t ld) {
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (u >= n) return;
-  const int64_t t = u / hidden, c = u - t * hidden;
-  float v = 0.0f;
-  for (int s = 0; s < splits; ++s) v += part[s * n + u];
-  dx[t * ld + c] = static_cast<T>(factor[t] == 0.0f ? 0.0f : v * *scale);
+  const int64_t t = blockIdx.x;
+  const float f = factor[t] == 0.0f ? 0.0f : *scale;
+  for (int c = threadIdx.x * 4; c < hidden; c += 1024) {
+    const int left = hidden - c;
+    f32x4v v = {};
+    for (int s = 0; s < splits; ++s) {
+      const float* p = part + s * n + t * hidden + c;
+      if (left >= 4) {
+        v += *reinterpret_cast<const f32x4u*>(p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (k < left) v[k] += p[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = f == 0.0f ? 0.0f : v[k] * f;
+    store4_out(dx + t * ld + c, v, left, 0);
+  }
 }
 
 // ------------------------------------------------------------ the plan
@@ -410,6 +431,7 @@ struct Plan {
   int splits, tile_dx;         // of the product for dx
   int terms_x, terms_w;
   bool keep;                   // all logits are one piece, which stays
+  bool keep_w;                 // so does the bf16 copy of the weights, where they are copied
   int64_t vz;                  // columns of a piece of dz, padded
   size_t part, stat, zt, factor, scale, x, w, x_t, w_t, z, dz, dz_t, dxp, total;
 };
@@ -471,8 +493,10 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   const int64_t by_w = (int64_t{1} << 26) / p.hp, by_z = p.keep ? by_w : (int64_t{1} << 27) / (terms * r);
   p.vb = piece_of(vocab, std::min(std::max(std::min(by_w, by_z) / 256 * 256, int64_t{1024}), int64_t{1} << 20));
   p.vz = p.keep ? vocab_p : p.vb;
+  // with gradients a copy of up to 1 GiB is made once, not once for each product
+  p.keep_w = (dx || dw) && vocab <= (int64_t{1} << 29) / p.hp;
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
-  const Choice of_dx = choose(rows, hidden, p.vb / 32 * (p.keep ? 1 : p.terms_x), true);
+  const Choice of_dx = choose(rows, hidden, p.vb / 32 * (p.vz > p.vb ? 1 : p.terms_x), true);
   p.splits = of_dx.splits;
   p.tile_dx = of_dx.tile;
   size_t at = 0;
@@ -488,7 +512,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.factor = take(t * 4);
   p.scale = take(4);
   p.x = take(t * p.hp * 2);
-  p.w = take(static_cast<size_t>(p.vb) * p.hp * 2);
+  p.w = take(static_cast<size_t>(p.keep_w ? vocab : p.vb) * p.hp * 2);
   if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.tp * 2);
   if (dx) p.w_t = take(static_cast<size_t>(hidden) * p.vb * 2);
   if (p.keep) p.z = take(t * p.vz * 4);
@@ -503,7 +527,7 @@ template <class C>
 dim3 tiles_of(ProductArgs& p) {
   p.tiles_m = (p.m + C::TM - 1) / C::TM;
   p.tiles_n = (p.n + C::TN - 1) / C::TN;
-  return dim3(static_cast<uint32_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n), 1u);
+  return dim3(static_cast<uint32_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n));
 }
 
 template <class C>
@@ -573,14 +597,19 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   logits.stages = logits.stages_b = static_cast<int>(pl.hp / 32);
   logits.splits = 1;
 
+  // weights as given, and as the products read them
   auto weights = [&](int64_t v0) { return static_cast<const uint8_t*>(a.w) + v0 * a.ldw * esz_w; };
-  const int64_t vf = plain_w ? pl.vf : pl.vb;
+  auto operand = [&](int64_t v0) {
+    return plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb + (pl.keep_w ? v0 * pl.hp : 0));
+  };
+  const int64_t vf = plain_w || pl.keep_w ? pl.vf : pl.vb;
   const bool once = pl.keep && vf >= a.vocab && pl.vb >= a.vocab;      // one piece of weights, too: its transpose comes with it
   for (int64_t v0 = 0; v0 < a.vocab; v0 += vf) {
     const int v = static_cast<int>(std::min<int64_t>(vf, a.vocab - v0));
     if (!plain_w || (once && want_dx))
-      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb, pl.hp, once ? w_t : nullptr, up(v, 64), nullptr, s));
-    logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
+      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb + (pl.keep_w ? v0 * pl.hp : 0), pl.hp, once ? w_t : nullptr,
+                  up(v, 64), nullptr, s));
+    logits.b = operand(v0);
     logits.n = v;
     const CeStatsArgs e{a.targets, v0, part, zt, z, pl.vz};
     int cols;
@@ -605,20 +634,23 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   for (int64_t v0 = 0; v0 < a.vocab; v0 += pl.vb) {
     const int v = static_cast<int>(std::min<int64_t>(pl.vb, a.vocab - v0));
     const int64_t vp = up(v, 64);
-    const bool need_w = !pl.keep && !plain_w, need_w_t = want_dx && !once;
+    const bool copied = !plain_w && pl.keep_w;                          // already there
+    const bool need_w = !pl.keep && !plain_w && !copied, need_w_t = want_dx && !once;
     if (need_w || need_w_t)
-      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.hp, need_w_t ? w_t : nullptr, vp, nullptr, s));
+      MO_TRY(copied ? pack(BF16, operand(v0), pl.hp, v, a.hidden, nullptr, 0, w_t, vp, nullptr, s)
+                    : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.hp, need_w_t ? w_t : nullptr, vp, nullptr, s));
     if (!pl.keep) {
-      logits.b = plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb);
+      logits.b = operand(v0);
       logits.n = v;
       const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp)};
       const int tile = choose(a.rows, v, logits.stages, false).tile;
       MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
     }
     if (want_dx) {
-      // a piece's terms lie side by side along the contraction, those of kept
-      // logits a whole row apart
+      // a piece's terms lie side by side along the contraction; where the logits
+      // are kept and the weights come in pieces, a whole row apart
       const int64_t pitch = pl.keep ? pl.vz : vp;
+      const int calls = pitch == vp ? 1 : pl.terms_x;
       ProductArgs p{};
       p.b = reinterpret_cast<const uint8_t*>(w_t);
       p.pitch_a = static_cast<uint32_t>(pitch * 2 * pl.terms_x);
@@ -626,9 +658,9 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.m = a.rows;
       p.n = a.hidden;
       p.stages_b = static_cast<int>(vp / 32);
-      p.stages = p.stages_b * (pl.keep ? 1 : pl.terms_x);
+      p.stages = p.stages_b * (calls == 1 ? pl.terms_x : 1);
       p.splits = pl.splits;
-      for (int term = 0; term < (pl.keep ? pl.terms_x : 1); ++term) {
+      for (int term = 0; term < calls; ++term) {
         p.a = reinterpret_cast<const uint8_t*>(dz + (pl.keep ? term * pitch + v0 : 0));
         MO_TRY((store<float>(pl.tile_dx, p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0 || term > 0, nullptr}, s)));
       }
@@ -652,9 +684,8 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   }
   if (want_dx) {
     const int64_t n = static_cast<int64_t>(a.rows) * a.hidden;
-    const uint32_t g = static_cast<uint32_t>((n + 255) / 256);
-    if (a.x_dt == F32) ce_finish_kernel<float><<<g, 256, 0, s>>>(dxp, pl.splits, n, a.rows, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
-    else ce_finish_kernel<__bf16><<<g, 256, 0, s>>>(dxp, pl.splits, n, a.rows, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
+    if (a.x_dt == F32) ce_finish_kernel<float><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
+    else ce_finish_kernel<__bf16><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
     MO_TRY(hipGetLastError());
   }
   return hipSuccess;

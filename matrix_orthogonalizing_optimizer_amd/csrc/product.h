@@ -49,6 +49,27 @@ __device__ __forceinline__ void store_out(T* o, float v, int accumulate) {
   *o = static_cast<T>(v);
 }
 
+// Four consecutive outputs as they are, n of them inside.
+template <typename T>
+__device__ __forceinline__ f32x4v load4_out(const T* o, int n) {
+  f32x4v v = {};
+  if (n >= 4) {
+    if constexpr (sizeof(T) == 4) {
+      v = *reinterpret_cast<const f32x4u*>(o);
+    } else {
+      typedef uint32_t u32x2u2 __attribute__((ext_vector_type(2), aligned(2)));
+      const u32x2u2 w = *reinterpret_cast<const u32x2u2*>(o);
+      v = f32x4v{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                 __uint_as_float(w[1] & 0xffff0000u)};
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < n) v[k] = to_f(o[k]);
+  }
+  return v;
+}
+
 // Four consecutive outputs, n of them inside.
 template <typename T>
 __device__ __forceinline__ void store4_out(T* o, f32x4v v, int n, int accumulate) {

@@ -107,7 +107,7 @@ inline double tile_us(const TileCost& c, int64_t m, int64_t n, int64_t stages, i
 // Where a workgroup's tile is: its first row and column, the last ones inside
 // it that exist, the wave's and the lane's place.
 struct TilePlace {
-  int tm, tn, wm, wn, lane, r32, half, mlast, nlast;
+  int split, tm, tn, wm, wn, lane, r32, half, mlast, nlast;
   int64_t m0, n0;
 };
 
@@ -121,11 +121,13 @@ __device__ __forceinline__ TilePlace tile_place(const ProductArgs& p) {
   q.r32 = q.lane & 31;
   q.half = q.lane >> 5;
   {
-    // each XCD (workgroup index mod 8) takes a contiguous range of tiles,
-    // walked in bands of 4 tile rows so that its L2 shares panels of both
-    const uint32_t tiles = static_cast<uint32_t>(p.tiles_m) * static_cast<uint32_t>(p.tiles_n);
+    // each XCD (workgroup index mod 8) takes a contiguous range of splits and
+    // tiles, walked in bands of 4 tile rows, so that its L2 shares panels of both
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles_m) * static_cast<uint32_t>(p.tiles_n), all = tiles * static_cast<uint32_t>(p.splits);
     const uint32_t x = blockIdx.x % 8, y = blockIdx.x / 8;
-    const uint32_t t = x * (tiles / 8) + min(x, tiles % 8) + y;
+    uint32_t t = x * (all / 8) + min(x, all % 8) + y;
+    q.split = __builtin_amdgcn_readfirstlane(static_cast<int>(t / tiles));
+    t %= tiles;
     constexpr uint32_t kBand = 4;
     const uint32_t band = t / (kBand * p.tiles_n);
     const uint32_t rows = min(kBand, p.tiles_m - band * kBand);
@@ -176,7 +178,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x16v{};
   int k0, k1;
-  split_range(p, blockIdx.y, k0, k1);
+  split_range(p, q.split, k0, k1);
   const int stages = __builtin_amdgcn_readfirstlane(k1 - k0);
   if (stages <= 0) return;                                // the same for the whole workgroup
   const int wave = q.wm * C::WN + q.wn, lane = q.lane;
@@ -347,7 +349,7 @@ template <class C, typename T>
 __device__ __forceinline__ void tile_store(const StoreArgs<T>& e, const TilePlace& q, uint8_t* smem, const f32x16v (&acc)[C::FM][C::FN]) {
   constexpr int W = C::TN / C::WN, kPitch = C::kTurnPitch, kLanes = W / 4;       // columns, and lanes to a row
   uint8_t* turn = smem + (q.wm * C::WN + q.wn) * 32 * kPitch;
-  T* out = e.out + blockIdx.y * e.split_stride + q.m0 * e.ldo + q.n0;
+  T* out = e.out + q.split * e.split_stride + q.m0 * e.ldo + q.n0;
   const float f = e.scale ? *e.scale : 1.0f;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
@@ -357,12 +359,23 @@ __device__ __forceinline__ void tile_store(const StoreArgs<T>& e, const TilePlac
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<f32x4v*>(turn + q.r32 * kPitch + (32 * j + 8 * g + 4 * q.half) * 4) =
             f32x4v{acc[i][j][4 * g] * f, acc[i][j][4 * g + 1] * f, acc[i][j][4 * g + 2] * f, acc[i][j][4 * g + 3] * f};
+    // what is added to comes first, all of it at once
+    constexpr int K = 32 * kLanes / 64;
+    f32x4v add[K] = {};
+    const int col = q.lane % kLanes * 4, c = q.wn * W + col, left = q.nlast + 1 - c;
+    T* to[K];
+    bool in[K];
 #pragma unroll
-    for (int k = 0; k < 32 * kLanes / 64; ++k) {
-      const int row = k * (64 / kLanes) + q.lane / kLanes, col = q.lane % kLanes * 4;
-      const f32x4v v = *reinterpret_cast<const f32x4v*>(turn + row * kPitch + col * 4);
-      const int r = q.wm * (C::TM / C::WM) + 32 * i + row, c = q.wn * W + col;
-      if (r <= q.mlast) store4_out(out + r * e.ldo + c, v, q.nlast + 1 - c, e.accumulate);
+    for (int k = 0; k < K; ++k) {
+      const int r = q.wm * (C::TM / C::WM) + 32 * i + k * (64 / kLanes) + q.lane / kLanes;
+      in[k] = r <= q.mlast && left > 0;
+      to[k] = out + r * e.ldo + c;
+      if (e.accumulate && in[k]) add[k] = load4_out(to[k], left);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const f32x4v v = *reinterpret_cast<const f32x4v*>(turn + (k * (64 / kLanes) + q.lane / kLanes) * kPitch + col * 4);
+      if (in[k]) store4_out(to[k], v + add[k], left, 0);
     }
   }
 }
@@ -392,7 +405,7 @@ template <class C, typename T>
 hipError_t run_product_store(ProductArgs p, const StoreArgs<T>& e, hipStream_t s) {
   p.tiles_m = (p.m + C::TM - 1) / C::TM;
   p.tiles_n = (p.n + C::TN - 1) / C::TN;
-  const dim3 g(static_cast<uint32_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n), static_cast<uint32_t>(p.splits));
+  const dim3 g(static_cast<uint32_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits));
   product_store_kernel<C, T><<<g, C::kThreads, 0, s>>>(p, e);
   return hipGetLastError();
 }
