@@ -307,7 +307,7 @@ bool fp8_matmul_fits(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) 
 
 template <class C, typename T>
 static hipError_t run(const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t s) {
-  return run_product_store<C, T>(p, {static_cast<T*>(a.out), a.ldo, 0, a.accumulate, nullptr}, s);
+  return run_product_store<C, T>(p, {static_cast<T*>(a.out), a.ldo, 0, a.accumulate, nullptr, worth_streaming(static_cast<T*>(a.out), a.ldo, a.m, a.n)}, s);
 }
 
 // Measured (see tile_us), in tiles of 64, 128 and 256: 1024 x 1024 x 8192 26, 2048

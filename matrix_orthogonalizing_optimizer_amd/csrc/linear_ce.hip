@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
   f32x16v acc[C::FM][C::FN];
   tile_sums<C>(p, q, smem, acc);
   if (e.z) {
-    tile_store<C, float>({e.z + e.col0, e.pitch_z, 0, 0, nullptr}, q, smem, acc);
+    tile_store<C, float>({e.z + e.col0, e.pitch_z, 0, 0, nullptr, 0}, q, smem, acc);
     __syncthreads();
   }
   float2* waves = reinterpret_cast<float2*>(smem);                      // [TM][WN]
@@ -397,29 +397,19 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
   }
 }
 
-// dx = scale times the sum of the splits' parts, 0 in rows that take no part: a
-// workgroup per row.
+// dx = scale times the sum of the splits' parts (rows of `pitch`, a multiple of
+// 4), 0 in rows that take no part: a workgroup per row.
 template <typename T>
-__global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t n, int hidden, const float* scale,
-                                                        const float* factor, T* dx, int64_t ld) {
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t stride, int64_t pitch, int hidden,
+                                                        const float* scale, const float* factor, T* dx, int64_t ld) {
   const int64_t t = blockIdx.x;
   const float f = factor[t] == 0.0f ? 0.0f : *scale;
   for (int c = threadIdx.x * 4; c < hidden; c += 1024) {
-    const int left = hidden - c;
     f32x4v v = {};
-    for (int s = 0; s < splits; ++s) {
-      const float* p = part + s * n + t * hidden + c;
-      if (left >= 4) {
-        v += *reinterpret_cast<const f32x4u*>(p);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          if (k < left) v[k] += p[k];
-      }
-    }
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4v*>(part + s * stride + t * pitch + c);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = f == 0.0f ? 0.0f : v[k] * f;
-    store4_out(dx + t * ld + c, v, left, 0);
+    store4_out(dx + t * ld + c, v, hidden - c, 0);
   }
 }
 
@@ -518,7 +508,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   if (p.keep) p.z = take(t * p.vz * 4);
   if (dx) p.dz = take(t * p.vz * 2 * p.terms_x);
   if (dw) p.dz_t = take(static_cast<size_t>(p.vz) * p.tp * 2 * p.terms_w);
-  if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * hidden * 4);
+  if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * p.hp * 4);
   p.total = rows ? at : 0;
   return p;
 }
@@ -662,7 +652,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.splits = pl.splits;
       for (int term = 0; term < calls; ++term) {
         p.a = reinterpret_cast<const uint8_t*>(dz + (pl.keep ? term * pitch + v0 : 0));
-        MO_TRY((store<float>(pl.tile_dx, p, {dxp, a.hidden, static_cast<int64_t>(a.rows) * a.hidden, v0 > 0 || term > 0, nullptr}, s)));
+        MO_TRY((store<float>(pl.tile_dx, p, {dxp, pl.hp, static_cast<int64_t>(a.rows) * pl.hp, v0 > 0 || term > 0, nullptr, 0}, s)));
       }
     }
     if (want_dw) {
@@ -676,16 +666,18 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.stages_b = static_cast<int>(pl.tp / 32);
       p.stages = p.stages_b * pl.terms_w;
       p.splits = 1;
+      const int stream_dw = a.dw_dt == F32 ? worth_streaming(static_cast<float*>(a.dw), a.ld_dw, a.vocab, a.hidden)
+                                           : worth_streaming(static_cast<__bf16*>(a.dw), a.ld_dw, a.vocab, a.hidden);
       const int tile_dw = choose(v, a.hidden, p.stages, false).tile;
       uint8_t* out = static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * esz_dw;
-      if (a.dw_dt == F32) MO_TRY((store<float>(tile_dw, p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
-      else MO_TRY((store<__bf16>(tile_dw, p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale}, s)));
+      if (a.dw_dt == F32) MO_TRY((store<float>(tile_dw, p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale, stream_dw}, s)));
+      else MO_TRY((store<__bf16>(tile_dw, p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale, stream_dw}, s)));
     }
   }
   if (want_dx) {
-    const int64_t n = static_cast<int64_t>(a.rows) * a.hidden;
-    if (a.x_dt == F32) ce_finish_kernel<float><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
-    else ce_finish_kernel<__bf16><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
+    const int64_t n = static_cast<int64_t>(a.rows) * pl.hp;
+    if (a.x_dt == F32) ce_finish_kernel<float><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, pl.hp, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
+    else ce_finish_kernel<__bf16><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, pl.hp, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
     MO_TRY(hipGetLastError());
   }
   return hipSuccess;

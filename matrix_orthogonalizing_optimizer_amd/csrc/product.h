@@ -49,6 +49,18 @@ __device__ __forceinline__ void store_out(T* o, float v, int accumulate) {
   *o = static_cast<T>(v);
 }
 
+// Four consecutive outputs past the caches: for outputs that are larger than
+// those, where keeping them would only evict what other tiles still read.
+template <typename T>
+__device__ __forceinline__ void stream4_out(T* o, f32x4v v) {
+  if constexpr (sizeof(T) == 4) {
+    __builtin_nontemporal_store(v, reinterpret_cast<f32x4u*>(o));
+  } else {
+    typedef uint32_t u32x2u2 __attribute__((ext_vector_type(2), aligned(2)));
+    __builtin_nontemporal_store(u32x2u2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, reinterpret_cast<u32x2u2*>(o));
+  }
+}
+
 // Four consecutive outputs as they are, n of them inside.
 template <typename T>
 __device__ __forceinline__ f32x4v load4_out(const T* o, int n) {

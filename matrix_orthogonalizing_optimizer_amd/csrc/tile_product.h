@@ -121,13 +121,16 @@ __device__ __forceinline__ TilePlace tile_place(const ProductArgs& p) {
   q.r32 = q.lane & 31;
   q.half = q.lane >> 5;
   {
-    // each XCD (workgroup index mod 8) takes a contiguous range of splits and
-    // tiles, walked in bands of 4 tile rows, so that its L2 shares panels of both
-    const uint32_t tiles = static_cast<uint32_t>(p.tiles_m) * static_cast<uint32_t>(p.tiles_n), all = tiles * static_cast<uint32_t>(p.splits);
-    const uint32_t x = blockIdx.x % 8, y = blockIdx.x / 8;
-    uint32_t t = x * (all / 8) + min(x, all % 8) + y;
-    q.split = __builtin_amdgcn_readfirstlane(static_cast<int>(t / tiles));
-    t %= tiles;
+    // one split after the other; of its tiles each XCD (workgroup index mod 8)
+    // takes a contiguous range, walked in bands of 4 tile rows so that its L2
+    // shares panels of both operands (a contiguous range of splits and tiles per
+    // XCD: 1021 x 2045 x 32512 in 8 splits 262 instead of 222 us; blocks of 16 x
+    // 16 tiles for the whole chip: nothing for 8192 x 8192 x 8192, 2% longer for
+    // 8192 x 32000 x 2048)
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles_m) * static_cast<uint32_t>(p.tiles_n);
+    q.split = __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x / tiles));
+    const uint32_t id = blockIdx.x % tiles, x = id % 8, y = id / 8;
+    const uint32_t t = x * (tiles / 8) + min(x, tiles % 8) + y;
     constexpr uint32_t kBand = 4;
     const uint32_t band = t / (kBand * p.tiles_n);
     const uint32_t rows = min(kBand, p.tiles_m - band * kBand);
@@ -280,6 +283,8 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   take_scales();
 
   constexpr int NP = FM * FN;
+  // columns forth and back, so that a product keeps one operand of the last
+  constexpr auto snake = [](int p) constexpr { return p / FN % 2 ? FN - 1 - p % FN : p % FN; };
   uint32_t at = 0;                                         // place of the stage in registers
   for (int t = 0; t < stages; t += 2) {
     unroll<2>([&](auto S) __attribute__((always_inline)) {
@@ -287,12 +292,17 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
       // this wave's reads of the stage are done, its part of the next has come
       wait_loads<(NST - 2) * DPW>();
       meet();
-      const uint32_t next = at + kStage == NST * kStage ? 0u : at + kStage;
-      if constexpr (Op::kScaled && cur == 0)
-        if ((t & 31) == 0 && (t >> 5) + 1 < groups) request_scales((t >> 5) + 1);
-      advance();
-      auto besides = [&](auto P, auto N) __attribute__((always_inline)) {     // what goes with product P of N
+      uint32_t next = 0;
+      // what goes with product P of N; the stage's bookkeeping too comes behind
+      // its first product, as nothing else would keep the matrix cores busy
+      auto besides = [&](auto P, auto N) __attribute__((always_inline)) {
         constexpr int n = N, r0 = P * NR / n, r1 = (P + 1) * NR / n, l0 = P * DPW / n, l1 = (P + 1) * DPW / n;
+        if constexpr (P == 0) {
+          next = at + kStage == NST * kStage ? 0u : at + kStage;
+          if constexpr (Op::kScaled && cur == 0)
+            if ((t & 31) == 0 && (t >> 5) + 1 < groups) request_scales((t >> 5) + 1);
+          advance();
+        }
         unroll<r1 - r0>([&](auto R) __attribute__((always_inline)) {
           read(std::integral_constant<int, r0 + decltype(R)::value>{}, std::integral_constant<int, nxt>{}, next);
         });
@@ -313,7 +323,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
 #pragma unroll
           for (int i = 0; i < FM; ++i) decode16(af[cur][i][s], fa[i], a[i][0], a[i][1]);
           unroll<2 * NP>([&](auto P) __attribute__((always_inline)) {
-            constexpr int i = P % NP / FN, j = P % FN, h = P / NP;
+            constexpr int i = P % NP / FN, j = snake(P), h = P / NP;
             acc[i][j] = mma_bf16(b[j][h], a[i][h], acc[i][j]);
             besides(std::integral_constant<int, 2 * s * NP + decltype(P)::value>{}, std::integral_constant<int, 4 * NP>{});
           });
@@ -321,7 +331,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
       } else {
         // a product at a time, and behind each a little of everything else
         unroll<Op::kSteps * NP>([&](auto P) __attribute__((always_inline)) {
-          constexpr int i = P % NP / FN, j = P % FN;
+          constexpr int i = P % NP / FN, j = snake(P);
           acc[i][j] = Op::template mma<P / NP>(bf[cur][j], af[cur][i], acc[i][j], sb[j], sa[i]);
           besides(P, std::integral_constant<int, Op::kSteps * NP>{});
           __builtin_amdgcn_sched_barrier(0);
@@ -344,7 +354,16 @@ struct StoreArgs {
   int64_t ldo, split_stride;     // elements from a split's outputs to the next split's
   int accumulate;
   const float* scale;            // or null
+  int stream;                    // past the caches
 };
+// Outputs larger than the L2s whose rows are whole lines: 8192 x 32000 x 2048 in
+// bf16 (524 MB) 1034 to 958 us, 8192 x 8192 x 8192 843 to 822.  Rows that share
+// lines lose: dw of 129283 x 2045 in fp32 takes 12% longer past the caches.
+template <typename T>
+int worth_streaming(const T* out, int64_t ldo, int64_t m, int64_t n) {
+  constexpr int kSize = sizeof(T);
+  return m * n * kSize > (int64_t{32} << 20) && reinterpret_cast<uintptr_t>(out) % 128 == 0 && ldo * kSize % 128 == 0;
+}
 template <class C, typename T>
 __device__ __forceinline__ void tile_store(const StoreArgs<T>& e, const TilePlace& q, uint8_t* smem, const f32x16v (&acc)[C::FM][C::FN]) {
   constexpr int W = C::TN / C::WN, kPitch = C::kTurnPitch, kLanes = W / 4;       // columns, and lanes to a row
@@ -359,23 +378,33 @@ __device__ __forceinline__ void tile_store(const StoreArgs<T>& e, const TilePlac
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<f32x4v*>(turn + q.r32 * kPitch + (32 * j + 8 * g + 4 * q.half) * 4) =
             f32x4v{acc[i][j][4 * g] * f, acc[i][j][4 * g + 1] * f, acc[i][j][4 * g + 2] * f, acc[i][j][4 * g + 3] * f};
-    // what is added to comes first, all of it at once
-    constexpr int K = 32 * kLanes / 64;
-    f32x4v add[K] = {};
-    const int col = q.lane % kLanes * 4, c = q.wn * W + col, left = q.nlast + 1 - c;
-    T* to[K];
-    bool in[K];
+    // four rows of stores at a time, before which what is added to comes at once
+    constexpr int K = 32 * kLanes / 64, kStep = 64 / kLanes, kAtOnce = K < 4 ? K : 4;
+    const int row = q.lane / kLanes, col = q.lane % kLanes * 4, c = q.wn * W + col, left = q.nlast + 1 - c;
+    const int r = q.wm * (C::TM / C::WM) + 32 * i + row, rows = left > 0 ? q.mlast + 1 - r : 0;
+    T* to = out + r * e.ldo + c;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int r = q.wm * (C::TM / C::WM) + 32 * i + k * (64 / kLanes) + q.lane / kLanes;
-      in[k] = r <= q.mlast && left > 0;
-      to[k] = out + r * e.ldo + c;
-      if (e.accumulate && in[k]) add[k] = load4_out(to[k], left);
-    }
+    for (int k0 = 0; k0 < K; k0 += kAtOnce) {
+      f32x4v v[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const f32x4v v = *reinterpret_cast<const f32x4v*>(turn + (k * (64 / kLanes) + q.lane / kLanes) * kPitch + col * 4);
-      if (in[k]) store4_out(to[k], v + add[k], left, 0);
+      for (int k = 0; k < kAtOnce; ++k) v[k] = *reinterpret_cast<const f32x4v*>(turn + ((k0 + k) * kStep + row) * kPitch + col * 4);
+      if (e.accumulate) {
+        f32x4v add[kAtOnce] = {};
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if ((k0 + k) * kStep < rows) add[k] = load4_out(to + (k0 + k) * kStep * e.ldo, left);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) v[k] += add[k];
+      }
+      if (e.stream && left >= 4) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if ((k0 + k) * kStep < rows) stream4_out(to + (k0 + k) * kStep * e.ldo, v[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if ((k0 + k) * kStep < rows) store4_out(to + (k0 + k) * kStep * e.ldo, v[k], left, 0);
+      }
     }
   }
 }
