@@ -36,6 +36,12 @@ __device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+// Rows of the workspace's matrices lie an odd number of 256 bytes apart, so that
+// the rows of a tile spread over the memory's channels: 4096 x 4096 x 4096 takes
+// 139 us with rows 16384 bytes apart and 124 with 16640, 1024 x 2048 x 31744 in 8
+// splits 115 with 63488 and 172 with 65024 and shares of 8192 bytes.
+int64_t apart(int64_t elements) { return ((elements + 127) / 128 | 1) * 128; }
+
 // ------------------------------------------------------------ rows and packing
 // Per row: its factor in dz, relative to the largest |g| (so that equal g do
 // not add a rounding of their own to dz's): 0 for a row that takes no part, NaN
@@ -61,9 +67,10 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, c
   }
 }
 
-// bf16 copies of a [rows, cols] matrix: dst [rows][pitch] (columns past `cols`
-// zero) and its transpose dst_t [cols][pitch_t] (rows past `rows` zero, and
-// those whose factor is 0, so that whatever they hold takes no part).  64 rows
+// bf16 copies of a [rows, cols] matrix: dst [rows][pitch] (columns past `cols`,
+// up to a multiple of 64, zero) and its transpose dst_t [cols][pitch_t] (rows
+// past `rows` likewise, and those whose factor is 0, so that whatever they hold
+// takes no part).  64 rows
 // x 128 columns per workgroup, through LDS; HBM bound.
 constexpr int kPackRows = 64, kPackCols = 128;
 // Eight rows of a column.
@@ -78,6 +85,7 @@ __device__ __forceinline__ u32x4v column8(const uint32_t (&tile)[kPackRows][kPac
 template <typename T>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
                                                       uint16_t* dst_t, int64_t pitch_t, const float* factor) {
+  const int64_t cols_p = (cols + 63) / 64 * 64, rows_p = (static_cast<int64_t>(rows) + 63) / 64 * 64;
   __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];       // pairs of columns; odd rows of dwords: columns spread over the banks
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kPackRows, c0 = static_cast<int64_t>(blockIdx.x) * kPackCols;
   const int cl = (threadIdx.x & 15) * 8, rl = threadIdx.x >> 4;
@@ -93,7 +101,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, 
     const int64_t r = r0 + rl + 16 * i;
     const u32x4v v = {pack_bf16x2(o[i].get(0), o[i].get(1)), pack_bf16x2(o[i].get(2), o[i].get(3)),
                       pack_bf16x2(o[i].get(4), o[i].get(5)), pack_bf16x2(o[i].get(6), o[i].get(7))};
-    if (dst && r < rows && c0 + cl < pitch) *reinterpret_cast<u32x4v*>(dst + r * pitch + c0 + cl) = v;
+    if (dst && r < rows && c0 + cl < cols_p) *reinterpret_cast<u32x4v*>(dst + r * pitch + c0 + cl) = v;
     const bool out = factor && r < rows && factor[r] == 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) tile[rl + 16 * i][cl / 2 + k] = out ? 0u : v[k];
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int u = i * 256 + threadIdx.x, c = u >> 3, r = (u & 7) * 8;       // 8 rows of a column
-    if (c0 + c >= cols || r0 + r >= pitch_t) continue;
+    if (c0 + c >= cols || r0 + r >= rows_p) continue;
     *reinterpret_cast<u32x4v*>(dst_t + (c0 + c) * pitch_t + r0 + r) = column8(tile, r, c);
   }
 }
@@ -253,10 +261,11 @@ struct CeGradArgs {
   int64_t col0;
   const float2* stat;
   const float* factor;
-  uint16_t* dz;                 // [rows][terms_x][vp], or null
-  uint16_t* dz_t;               // [columns][terms_w][tp], or null
-  int terms_x, terms_w;
+  uint16_t* dz;                 // [rows]: terms_x times vp, rows pitch_x apart
+  uint16_t* dz_t;               // [columns]: terms_w times tp, pitch_w apart
+  int terms_x, terms_w;         // 0: not wanted
   int vp, tp;                   // the piece's columns and the rows, padded (zeros)
+  int64_t pitch_x, pitch_w;
 };
 
 template <class C>
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
           const int lr = k * (64 / kLanes) + q.lane / kLanes, lc = q.lane % kLanes * 8;
           const u32x4v v = *reinterpret_cast<const u32x4v*>(turn + lr * kPitch + lc * 2);
           const int64_t rr = q.wm * (C::TM / C::WM) + 32 * i + lr, cc = q.n0 + q.wn * W + lc;
-          if (rr <= q.mlast && cc < e.vp) *reinterpret_cast<u32x4v*>(e.dz + ((q.m0 + rr) * e.terms_x + term) * e.vp + cc) = v;
+          if (rr <= q.mlast && cc < e.vp) *reinterpret_cast<u32x4v*>(e.dz + (q.m0 + rr) * e.pitch_x + static_cast<int64_t>(term) * e.vp + cc) = v;
         }
         wave_order();
       }
@@ -338,7 +347,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
           const int c = k * 16 + q.lane / 4, ch = q.lane % 4;
           const u32x4v v = *reinterpret_cast<const u32x4v*>(turn + c * kPitchT + ch * 16);
           const int64_t cc = q.wn * W + c, rr = q.m0 + q.wm * (C::TM / C::WM) + 32 * i + ch * 8;
-          if (cc <= q.nlast && rr < e.tp) *reinterpret_cast<u32x4v*>(e.dz_t + ((q.n0 + cc) * e.terms_w + term) * e.tp + rr) = v;
+          if (cc <= q.nlast && rr < e.tp) *reinterpret_cast<u32x4v*>(e.dz_t + (q.n0 + cc) * e.pitch_w + static_cast<int64_t>(term) * e.tp + rr) = v;
         }
         wave_order();
       }
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
     for (int i = 0; i < 4; ++i) {
       const int64_t t = r0 + rl + 16 * i;
       const u32x4v h = {pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]), pack_bf16x2(v[i][4], v[i][5]), pack_bf16x2(v[i][6], v[i][7])};
-      if (e.dz && term < e.terms_x && t < rows && c < e.vp) *reinterpret_cast<u32x4v*>(e.dz + (t * e.terms_x + term) * e.vp + c) = h;
+      if (term < e.terms_x && t < rows && c < e.vp) *reinterpret_cast<u32x4v*>(e.dz + t * e.pitch_x + static_cast<int64_t>(term) * e.vp + c) = h;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         tile[rl + 16 * i][cl / 2 + k] = h[k];
@@ -385,13 +394,13 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
         v[i][2 * k + 1] -= __uint_as_float(h[k] & 0xffff0000u);
       }
     }
-    if (!e.dz_t || term >= e.terms_w) continue;
+    if (term >= e.terms_w) continue;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int u = i * 256 + threadIdx.x, cc = u >> 3, r = (u & 7) * 8;
       if (c0 + cc < vocab && r0 + r < e.tp)
-        *reinterpret_cast<u32x4v*>(e.dz_t + ((c0 + cc) * e.terms_w + term) * e.tp + r0 + r) = column8(tile, r, cc);
+        *reinterpret_cast<u32x4v*>(e.dz_t + (c0 + cc) * e.pitch_w + static_cast<int64_t>(term) * e.tp + r0 + r) = column8(tile, r, cc);
     }
     __syncthreads();
   }
@@ -417,6 +426,7 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int s
 // Pieces of the vocabulary, and the places of everything in the workspace.
 struct Plan {
   int64_t hp, tp;              // hidden size and rows, padded to whole pairs of stages
+  int64_t ph, pt;              // and how far apart rows of that length lie
   int64_t vf, vb;              // columns of a forward and of a backward piece
   int splits, tile_dx;         // of the product for dx
   int terms_x, terms_w;
@@ -471,6 +481,8 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   Plan p{};
   p.hp = up(hidden, 64);
   p.tp = up(rows, 64);
+  p.ph = apart(p.hp);
+  p.pt = apart(p.tp);
   p.terms_x = dx ? terms_of(x_dt) : 0;
   p.terms_w = dw ? terms_of(dw_dt) : 0;
   // A piece's dz and its transpose stay near 256 MiB in all, its weights and their
@@ -484,7 +496,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.vb = piece_of(vocab, std::min(std::max(std::min(by_w, by_z) / 256 * 256, int64_t{1024}), int64_t{1} << 20));
   p.vz = p.keep ? vocab_p : p.vb;
   // with gradients a copy of up to 1 GiB is made once, not once for each product
-  p.keep_w = (dx || dw) && vocab <= (int64_t{1} << 29) / p.hp;
+  p.keep_w = (dx || dw) && vocab <= (int64_t{1} << 29) / p.ph;
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
   const Choice of_dx = choose(rows, hidden, p.vb / 32 * (p.vz > p.vb ? 1 : p.terms_x), true);
   p.splits = of_dx.splits;
@@ -501,13 +513,13 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.zt = take(t * 4);
   p.factor = take(t * 4);
   p.scale = take(4);
-  p.x = take(t * p.hp * 2);
-  p.w = take(static_cast<size_t>(p.keep_w ? vocab : p.vb) * p.hp * 2);
-  if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.tp * 2);
-  if (dx) p.w_t = take(static_cast<size_t>(hidden) * p.vb * 2);
+  p.x = take(t * p.ph * 2);
+  p.w = take(static_cast<size_t>(p.keep_w ? vocab : p.vb) * p.ph * 2);
+  if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.pt * 2);
+  if (dx) p.w_t = take(static_cast<size_t>(hidden) * apart(p.vb) * 2);
   if (p.keep) p.z = take(t * p.vz * 4);
-  if (dx) p.dz = take(t * p.vz * 2 * p.terms_x);
-  if (dw) p.dz_t = take(static_cast<size_t>(p.vz) * p.tp * 2 * p.terms_w);
+  if (dx) p.dz = take(t * apart(p.vz * p.terms_x) * 2);
+  if (dw) p.dz_t = take(static_cast<size_t>(p.vz) * apart(p.tp * p.terms_w) * 2);
   if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * p.hp * 4);
   p.total = rows ? at : 0;
   return p;
@@ -577,12 +589,12 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
 
   if (grad) ce_rows_kernel<<<1, 1024, 0, s>>>(a.targets, a.grad_loss, a.rows, a.vocab, factor, scale);
   MO_TRY(hipGetLastError());
-  if (!plain_x || want_dw) MO_TRY(pack(a.x_dt, a.x, a.ldx, a.rows, a.hidden, plain_x ? nullptr : xb, pl.hp, x_t, pl.tp, factor, s));
+  if (!plain_x || want_dw) MO_TRY(pack(a.x_dt, a.x, a.ldx, a.rows, a.hidden, plain_x ? nullptr : xb, pl.ph, x_t, pl.pt, factor, s));
 
   ProductArgs logits{};
   logits.a = static_cast<const uint8_t*>(plain_x ? a.x : xb);
-  logits.pitch_a = static_cast<uint32_t>((plain_x ? a.ldx : pl.hp) * 2);
-  logits.pitch_b = static_cast<uint32_t>((plain_w ? a.ldw : pl.hp) * 2);
+  logits.pitch_a = static_cast<uint32_t>((plain_x ? a.ldx : pl.ph) * 2);
+  logits.pitch_b = static_cast<uint32_t>((plain_w ? a.ldw : pl.ph) * 2);
   logits.m = a.rows;
   logits.stages = logits.stages_b = static_cast<int>(pl.hp / 32);
   logits.splits = 1;
@@ -590,15 +602,15 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   // weights as given, and as the products read them
   auto weights = [&](int64_t v0) { return static_cast<const uint8_t*>(a.w) + v0 * a.ldw * esz_w; };
   auto operand = [&](int64_t v0) {
-    return plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb + (pl.keep_w ? v0 * pl.hp : 0));
+    return plain_w ? weights(v0) : reinterpret_cast<const uint8_t*>(wb + (pl.keep_w ? v0 * pl.ph : 0));
   };
   const int64_t vf = plain_w || pl.keep_w ? pl.vf : pl.vb;
   const bool once = pl.keep && vf >= a.vocab && pl.vb >= a.vocab;      // one piece of weights, too: its transpose comes with it
   for (int64_t v0 = 0; v0 < a.vocab; v0 += vf) {
     const int v = static_cast<int>(std::min<int64_t>(vf, a.vocab - v0));
     if (!plain_w || (once && want_dx))
-      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb + (pl.keep_w ? v0 * pl.hp : 0), pl.hp, once ? w_t : nullptr,
-                  up(v, 64), nullptr, s));
+      MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb + (pl.keep_w ? v0 * pl.ph : 0), pl.ph, once ? w_t : nullptr,
+                  apart(up(v, 64)), nullptr, s));
     logits.b = operand(v0);
     logits.n = v;
     const CeStatsArgs e{a.targets, v0, part, zt, z, pl.vz};
@@ -617,50 +629,51 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
 
   if (pl.keep) {
     const dim3 g(static_cast<uint32_t>((a.vocab + kPackCols - 1) / kPackCols), static_cast<uint32_t>((a.rows + kPackRows - 1) / kPackRows));
-    ce_kept_grad_kernel<<<g, 256, 0, s>>>({a.targets, 0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(pl.vz), static_cast<int>(pl.tp)},
-                                          z, a.rows, a.vocab);
+    ce_kept_grad_kernel<<<g, 256, 0, s>>>({a.targets, 0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(pl.vz), static_cast<int>(pl.tp),
+                                           apart(pl.vz * pl.terms_x), apart(pl.tp * pl.terms_w)}, z, a.rows, a.vocab);
     MO_TRY(hipGetLastError());
   }
   for (int64_t v0 = 0; v0 < a.vocab; v0 += pl.vb) {
     const int v = static_cast<int>(std::min<int64_t>(pl.vb, a.vocab - v0));
-    const int64_t vp = up(v, 64);
+    const int64_t vp = up(v, 64), pv = apart(vp);
     const bool copied = !plain_w && pl.keep_w;                          // already there
     const bool need_w = !pl.keep && !plain_w && !copied, need_w_t = want_dx && !once;
     if (need_w || need_w_t)
-      MO_TRY(copied ? pack(BF16, operand(v0), pl.hp, v, a.hidden, nullptr, 0, w_t, vp, nullptr, s)
-                    : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.hp, need_w_t ? w_t : nullptr, vp, nullptr, s));
+      MO_TRY(copied ? pack(BF16, operand(v0), pl.ph, v, a.hidden, nullptr, 0, w_t, pv, nullptr, s)
+                    : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.ph, need_w_t ? w_t : nullptr, pv, nullptr, s));
     if (!pl.keep) {
       logits.b = operand(v0);
       logits.n = v;
-      const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp)};
+      const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp),
+                         apart(vp * pl.terms_x), apart(pl.tp * pl.terms_w)};
       const int tile = choose(a.rows, v, logits.stages, false).tile;
       MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
     }
     if (want_dx) {
       // a piece's terms lie side by side along the contraction; where the logits
       // are kept and the weights come in pieces, a whole row apart
-      const int64_t pitch = pl.keep ? pl.vz : vp;
-      const int calls = pitch == vp ? 1 : pl.terms_x;
+      const int64_t term_at = pl.keep ? pl.vz : vp;
+      const int calls = term_at == vp ? 1 : pl.terms_x;
       ProductArgs p{};
       p.b = reinterpret_cast<const uint8_t*>(w_t);
-      p.pitch_a = static_cast<uint32_t>(pitch * 2 * pl.terms_x);
-      p.pitch_b = static_cast<uint32_t>(vp * 2);
+      p.pitch_a = static_cast<uint32_t>(apart(term_at * pl.terms_x) * 2);
+      p.pitch_b = static_cast<uint32_t>(pv * 2);
       p.m = a.rows;
       p.n = a.hidden;
       p.stages_b = static_cast<int>(vp / 32);
       p.stages = p.stages_b * (calls == 1 ? pl.terms_x : 1);
       p.splits = pl.splits;
       for (int term = 0; term < calls; ++term) {
-        p.a = reinterpret_cast<const uint8_t*>(dz + (pl.keep ? term * pitch + v0 : 0));
+        p.a = reinterpret_cast<const uint8_t*>(dz + (pl.keep ? term * term_at + v0 : 0));
         MO_TRY((store<float>(pl.tile_dx, p, {dxp, pl.hp, static_cast<int64_t>(a.rows) * pl.hp, v0 > 0 || term > 0, nullptr, 0}, s)));
       }
     }
     if (want_dw) {
       ProductArgs p{};
-      p.a = reinterpret_cast<const uint8_t*>(dz_t + (pl.keep ? v0 * pl.terms_w * pl.tp : 0));
+      p.a = reinterpret_cast<const uint8_t*>(dz_t + (pl.keep ? v0 * apart(pl.tp * pl.terms_w) : 0));
       p.b = reinterpret_cast<const uint8_t*>(x_t);
-      p.pitch_a = static_cast<uint32_t>(pl.tp * 2 * pl.terms_w);
-      p.pitch_b = static_cast<uint32_t>(pl.tp * 2);
+      p.pitch_a = static_cast<uint32_t>(apart(pl.tp * pl.terms_w) * 2);
+      p.pitch_b = static_cast<uint32_t>(pl.pt * 2);
       p.m = v;
       p.n = a.hidden;
       p.stages_b = static_cast<int>(pl.tp / 32);

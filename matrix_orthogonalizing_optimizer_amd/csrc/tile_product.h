@@ -145,11 +145,17 @@ __device__ __forceinline__ TilePlace tile_place(const ProductArgs& p) {
   return q;
 }
 
-// The stages of split `s`, in pairs.
+// The stages of split `s`: an odd number of 256 bytes of each row, so that the
+// splits, which advance together, use different channels of the memory.
 __device__ __forceinline__ void split_range(const ProductArgs& p, int s, int& k0, int& k1) {
-  const int pairs = p.stages / 2, per = (pairs + p.splits - 1) / p.splits;
-  k0 = 2 * min(s * per, pairs);
-  k1 = 2 * min((s + 1) * per, pairs);
+  if (p.splits == 1) {
+    k0 = 0;
+    k1 = p.stages;
+    return;
+  }
+  const int per = 4 * ((((p.stages + 3) / 4 + p.splits - 1) / p.splits) | 1);
+  k0 = min(s * per, p.stages);
+  k1 = min(s * per + per, p.stages);
 }
 
 // acc[i][j]: lane (r32, half), element 4 e + k of the tile's row
