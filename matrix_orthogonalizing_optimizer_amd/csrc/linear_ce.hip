@@ -85,9 +85,9 @@ __device__ __forceinline__ u32x4v column8(const uint32_t (&tile)[kPackRows][kPac
 template <typename T>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
                                                       uint16_t* dst_t, int64_t pitch_t, const float* factor) {
-  const int64_t cols_p = (cols + 63) / 64 * 64, rows_p = (static_cast<int64_t>(rows) + 63) / 64 * 64;
+  const int64_t cols_p = (static_cast<int64_t>(cols) + 63) / 64 * 64, rows_p = (static_cast<int64_t>(rows) + 63) / 64 * 64;
   __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];       // pairs of columns; odd rows of dwords: columns spread over the banks
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kPackRows, c0 = static_cast<int64_t>(blockIdx.x) * kPackCols;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPackRows, c0 = static_cast<int64_t>(blockIdx.y) * kPackCols;
   const int cl = (threadIdx.x & 15) * 8, rl = threadIdx.x >> 4;
   const int left = static_cast<int>(min(int64_t{8}, cols - c0 - cl));
   Oct<T> o[4];
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, 
 
 hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch, uint16_t* dst_t, int64_t pitch_t,
                 const float* factor, hipStream_t s) {
-  const dim3 g(static_cast<uint32_t>((cols + kPackCols - 1) / kPackCols), static_cast<uint32_t>((rows + kPackRows - 1) / kPackRows));
+  // rows along the grid's long axis: up to 2^22 columns are 2^15 workgroups
+  const dim3 g(static_cast<uint32_t>((static_cast<int64_t>(rows) + kPackRows - 1) / kPackRows), static_cast<uint32_t>((cols + kPackCols - 1) / kPackCols));
   if (dt == F32) ce_pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
   else ce_pack_kernel<__bf16><<<g, 256, 0, s>>>(static_cast<const __bf16*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
   return hipGetLastError();

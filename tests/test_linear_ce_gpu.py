@@ -119,6 +119,7 @@ def test_strided_operands_and_accumulation(dwd):
     (40, 4096, 33000, BF16, F32),         # kept logits, several pieces of weights
     (24, 4100, 33000, F32, BF16),
     (4500, 128, 15001, BF16, BF16),       # two pieces, odd columns
+    (3, 4, 4194300, F32, BF16),           # more rows of weights than 65535 times 64
 ])
 def test_pieces(t, h, v, wd, dwd):
     x, w, y, g = _inputs(t, h, v, 11, BF16, wd)
