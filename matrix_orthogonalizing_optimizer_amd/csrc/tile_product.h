@@ -73,18 +73,21 @@ __device__ __forceinline__ void decode16(u32x4v x, float s, u32x4v& lo, u32x4v& 
     hi[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 + w], s, true));
   }
 }
-// TM x TN outputs, WM x WN waves, a ring of NST stages in LDS.
-template <class OpT, int TMv, int TNv, int WMv, int WNv, int NSTv>
+// TM x TN outputs, WM x WN waves, a ring of NST stages in LDS.  Sliced: each wave
+// takes a part of the contraction for all outputs, with a ring of its own, and
+// the waves' sums meet at the end; a wave then has its WM x WN part of them.
+template <class OpT, int TMv, int TNv, int WMv, int WNv, int NSTv, bool kSlicedv = false>
 struct TileCfgT {
   typedef OpT Op;
   static constexpr int TM = TMv, TN = TNv, WM = WMv, WN = WNv, NST = NSTv, NW = WM * WN;
+  static constexpr bool kSliced = kSlicedv;
   static constexpr int FM = TM / (32 * WM), FN = TN / (32 * WN);
   static constexpr int kThreads = 64 * NW;
   static constexpr int kMinWaves = FM * FN >= 16 ? 1 : 2;        // per SIMD: 256 sums a lane leave room for one
   static constexpr int kStage = (TM + TN) * 64, kScaleGroup = Op::kScaled ? (TM + TN) * 16 : 0;
   // what the epilogues need to turn 32 rows per wave
   static constexpr int kTurnPitch = TN / WN * 4 + 16;
-  static constexpr int kRing = NST * kStage + 2 * kScaleGroup, kTurn = NW * 32 * kTurnPitch;
+  static constexpr int kRings = NST * kStage + 2 * kScaleGroup, kRing = (kSliced ? NW : 1) * kRings, kTurn = NW * 32 * kTurnPitch;
   static constexpr int kLds = kRing > kTurn ? kRing : kTurn;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
 };
@@ -174,8 +177,12 @@ __device__ __forceinline__ void split_range(const ProductArgs& p, int s, int& k0
 // Past the end no lane requests, and the number of loads in flight is still the
 // same at every wait.  Rows past the end repeat the last row; what comes of them
 // is not stored.
+//
+// C: the waves that share the ring at `smem`; `wave` of them, at wm, wn, which
+// add up stages k0 to k1.
 template <class C>
-__device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace& q, uint8_t* smem, f32x16v (&acc)[C::FM][C::FN]) {
+__device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace& q, int wave, int wm, int wn, int k0, int k1, uint8_t* smem,
+                                          f32x16v (&acc)[C::FM][C::FN]) {
   typedef typename C::Op Op;
   constexpr int TM = C::TM, TN = C::TN, NW = C::NW, FM = C::FM, FN = C::FN, NST = C::NST, kStage = C::kStage;
   constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW), DPW = DA + DB;      // requests of a wave and stage
@@ -186,11 +193,9 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x16v{};
-  int k0, k1;
-  split_range(p, q.split, k0, k1);
   const int stages = __builtin_amdgcn_readfirstlane(k1 - k0);
-  if (stages <= 0) return;                                // the same for the whole workgroup
-  const int wave = q.wm * C::WN + q.wn, lane = q.lane;
+  if (stages <= 0) return;                                // the same for all waves of the ring
+  const int lane = q.lane;
   const uint8_t* a0 = uniform_ptr(p.a + q.m0 * p.pitch_a + static_cast<int64_t>(k0) * 64);
   const uint8_t* b00 = uniform_ptr(p.b + q.n0 * p.pitch_b);
 
@@ -222,8 +227,9 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
     if constexpr (i < DA) lds_dma16_masked<i * 1024>(pa, arow[i], dst + to, lanes);
     else lds_dma16_masked<(i - DA) * 1024>(pb, brow[i - DA], dstb + to, lanes);
   };
-  // Scale bytes: 64 rows a request, 16 bytes of each; two groups in turn.
-  const int blocks = stages / 2, groups = (blocks + 15) / 16;
+  // Scale bytes: 64 rows a request, 16 bytes of each (groups of 16 blocks); two
+  // groups in turn.
+  const int block0 = k0 / 2, blocks = k1 / 2, groups = (blocks + 15) / 16;
   auto request_scales = [&](int g) __attribute__((always_inline)) {
     if constexpr (Op::kScaled) {
 #pragma unroll
@@ -238,10 +244,10 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   };
 
   // Fragments: 32 rows, lane l holds row l & 31.
-  const uint8_t* abase = smem + (q.wm * (TM / C::WM) + q.r32) * 64;
-  const uint8_t* bbase = smem + TM * 64 + (q.wn * (TN / C::WN) + q.r32) * 64;
-  const uint8_t* asbase = smem + kScales + (q.wm * (TM / C::WM) + q.r32) * 16;
-  const uint8_t* bsbase = smem + kScales + (TM + q.wn * (TN / C::WN) + q.r32) * 16;
+  const uint8_t* abase = smem + (wm * (TM / C::WM) + q.r32) * 64;
+  const uint8_t* bbase = smem + TM * 64 + (wn * (TN / C::WN) + q.r32) * 64;
+  const uint8_t* asbase = smem + kScales + (wm * (TM / C::WM) + q.r32) * 16;
+  const uint8_t* bsbase = smem + kScales + (TM + wn * (TN / C::WN) + q.r32) * 16;
   uint32_t xs[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) xs[s] = static_cast<uint32_t>(((q.half * 2 + s) ^ ((q.r32 >> 2) & 3)) * 16);
@@ -273,11 +279,12 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   };
   auto meet = [&]() __attribute__((always_inline)) {       // no memory fence: it would drain the loads
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
+    if constexpr (NW > 1) __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  request_scales(0);
+  request_scales(block0 >> 4);
+  if ((block0 & 15) && (block0 >> 4) + 1 < groups) request_scales((block0 >> 4) + 1);
   unroll<NST>([&](auto Q) __attribute__((always_inline)) {
     if constexpr (Q > 0) advance();
     unroll<DPW>([&](auto I) __attribute__((always_inline)) { request(I, static_cast<uint32_t>(Q * kStage)); });
@@ -285,7 +292,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
   wait_loads<(NST - 1) * DPW>();
   meet();
   unroll<NR>([&](auto R) __attribute__((always_inline)) { read(R, std::integral_constant<int, 0>{}, 0u); });
-  read_scales(0);
+  read_scales(block0);
   take_scales();
 
   constexpr int NP = FM * FN;
@@ -306,14 +313,14 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
         if constexpr (P == 0) {
           next = at + kStage == NST * kStage ? 0u : at + kStage;
           if constexpr (Op::kScaled && cur == 0)
-            if ((t & 31) == 0 && (t >> 5) + 1 < groups) request_scales((t >> 5) + 1);
+            if (const int b = block0 + t / 2; (b & 15) == 0 && (b >> 4) + 1 < groups) request_scales((b >> 4) + 1);
           advance();
         }
         unroll<r1 - r0>([&](auto R) __attribute__((always_inline)) {
           read(std::integral_constant<int, r0 + decltype(R)::value>{}, std::integral_constant<int, nxt>{}, next);
         });
         unroll<l1 - l0>([&](auto L) __attribute__((always_inline)) { request(std::integral_constant<int, l0 + decltype(L)::value>{}, at); });
-        if constexpr (cur == 1 && P == n - 1) read_scales(t / 2 + 1);
+        if constexpr (cur == 1 && P == n - 1) read_scales(block0 + t / 2 + 1);
       };
       if constexpr (Op::kDecoded) {
         float fa[FM], fb[FN];
@@ -348,8 +355,47 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
     });
   }
   wait_loads<0>();                                         // no request outlives the workgroup
+}
+
+template <class C>
+__device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace& q, uint8_t* smem, f32x16v (&acc)[C::FM][C::FN]) {
+  const int wave = q.wm * C::WN + q.wn;
+  int k0, k1;
+  split_range(p, q.split, k0, k1);
+  if constexpr (!C::kSliced) {
+    ring_sums<C>(p, q, wave, q.wm, q.wn, k0, k1, smem, acc);
+  } else {
+    static_assert(C::FM == 1 && C::FN == 1, "a wave keeps one block of 32 x 32");
+    typedef TileCfgT<typename C::Op, C::TM, C::TN, 1, 1, C::NST> One;
+    const int pairs = (k1 - k0) / 2, per = (pairs + C::NW - 1) / C::NW;
+    const int s0 = k0 + 2 * min(wave * per, pairs), s1 = k0 + 2 * min(wave * per + per, pairs);
+    f32x16v sums[One::FM][One::FN];
+    uint8_t* ring = smem + wave * C::kRings;
+    ring_sums<One>(p, q, 0, 0, 0, s0, s1, ring, sums);
+    // each block to the wave that keeps it; sums in the waves' order
+    static_assert(C::NW * 4096 <= C::kRings, "the blocks fit the wave's ring");
+    unroll<C::NW>([&](auto B) __attribute__((always_inline)) {
+      constexpr int b = B;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x16v& s = sums[b / C::WN][b % C::WN];
+        *reinterpret_cast<f32x4v*>(ring + b * 4096 + g * 1024 + q.lane * 16) = f32x4v{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
+      }
+    });
+    __syncthreads();
+    acc[0][0] = f32x16v{};
+#pragma unroll
+    for (int w = 0; w < C::NW; ++w)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4v v = *reinterpret_cast<const f32x4v*>(smem + w * C::kRings + wave * 4096 + g * 1024 + q.lane * 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[0][0][4 * g + k] += v[k];
+      }
+  }
   __syncthreads();
 }
+
 
 // Stores the sums, times a factor in device memory where one is given.  Each
 // wave turns 32 rows at a time through LDS of its own, so that rows leave as
