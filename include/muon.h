@@ -591,6 +591,7 @@ int mo_linear_ce(const void* x, int x_dtype, int64_t ldx, const void* w, int w_d
  * top <= 4096, weight finite.  Outputs may not overlap each other, an input or
  * the workspace.
  * ---------------------------------------------------------------------- */
+/* Workspace of mo_balance_loss (may be 0: then it may be NULL).  Host-only. */
 int mo_balance_loss_workspace_size(int64_t tokens, int64_t experts, size_t* bytes);
 int mo_balance_loss(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
                     const int64_t* index, int64_t top, float weight, const float* grad_loss,

@@ -653,6 +653,9 @@ def mx4_linear_backward(dy: torch.Tensor, x_t: Mx4Matrix, w_t: Mx4Matrix, *,
 
 
 # ---------------------------------------------------------------- 8-bit matrices
+_I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
+
+
 class Fp8Matrix:
     """The 8-bit image of a [rows, cols] matrix with a scale per block of 128:
     ``codes`` uint8 [rows, 128 nb] (e4m3) and ``scales`` uint8 [rows, 16 ceil(nb
@@ -660,7 +663,7 @@ class Fp8Matrix:
     them out.  Rows or columns may be none.  Both arrays, and those of a list's
     images, may share one allocation, which lives as long as any of them."""
 
-    __slots__ = ("rows", "cols", "_keep", "_at", "_codes", "_scales", "_ptrs")
+    __slots__ = ("rows", "cols", "_keep", "_at", "_codes", "_scales", "_ptrs", "_image")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         if codes.dim() != 2:
@@ -676,7 +679,7 @@ class Fp8Matrix:
             raise ValueError("codes and scales must share a device")
         self.rows, self.cols = rows, int(cols)
         self._keep, self._at, self._codes, self._scales = (codes, scales), None, codes, scales
-        self._ptrs = (codes.data_ptr(), scales.data_ptr())
+        self._ptrs, self._image = (codes.data_ptr(), scales.data_ptr()), None
 
     # The arrays of an image that was made here are cut out of their allocation
     # when they are asked for: the operators only need their addresses.
@@ -724,12 +727,14 @@ class Fp8Matrix:
         for (rows, cols), at, codes in zip(shapes, ats, sizes):
             q = object.__new__(cls)             # right by construction: no checks
             q.rows, q.cols, q._keep, q._at, q._codes, q._scales = rows, cols, keep, at, None, None
-            q._ptrs = (base + at, base + at + codes)
+            q._ptrs, q._image = (base + at, base + at + codes), None
             made.append(q)
         return made
 
-    def _struct(self):
-        return (ctypes.c_int64 * 4)(*self._ptrs, self.rows, self.cols)     # mo_fp8_image
+    def _struct(self):                          # mo_fp8_image
+        if self._image is None:
+            self._image = _I64x4(*self._ptrs, self.rows, self.cols)
+        return self._image
 
     def __repr__(self) -> str:
         return f"Fp8Matrix([{self.rows}, {self.cols}], device={self.device})"
@@ -843,6 +848,21 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfl
     return out
 
 
+def _fp8_images(view, dt: int, both: bool, dev: torch.device, handle: int) -> List[Fp8Matrix]:
+    """Images of one matrix, and of its transpose where ``both``, inside a launch context."""
+    ptr, r, c, ld = view
+    made = Fp8Matrix._empty(((r, c), (c, r)) if both else ((r, c),), dev)
+    item = _I64x8(ptr, *made[0]._ptrs, *(made[1]._ptrs if both else _NO_IMAGE), r, c, ld)
+    check(lib().mo_fp8_quantize(item, 1, dt, 0, handle))
+    return made
+
+
+def _fp8_product(a: Fp8Matrix, b: Fp8Matrix, dtype: torch.dtype, dt: int, dev: torch.device, handle: int) -> torch.Tensor:
+    out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
+    check(lib().mo_fp8_matmul(a._struct(), b._struct(), out.data_ptr(), dt, max(b.rows, 1), 0, handle))
+    return out
+
+
 def fp8_linear(x: torch.Tensor, w: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
                save: bool = False, stream=None):
     """``y = x W^T`` with W [N, K] held in 8 bits and x [..., K] (fp32 or
@@ -850,15 +870,15 @@ def fp8_linear(x: torch.Tensor, w: Fp8Matrix, *, out_dtype: torch.dtype = torch.
     returns the image of x^T that :func:`fp8_linear_backward` takes.  x may
     have no tokens.  Not seen by autograd."""
     x2 = _flat2(x)
-    if x2.shape[1] != w.cols:
-        raise ValueError(f"x has {x2.shape[1]} features, the weights {w.cols}")
-    if save:
-        xq, x_t = fp8_quantize(x2, images="both", stream=stream)
-    else:
-        xq = fp8_quantize(x2, stream=stream)
-    y = fp8_matmul(xq, w, out_dtype=out_dtype, stream=stream)
+    view = _rows_of(x2, "x")
+    if view[2] != w.cols:
+        raise ValueError(f"x has {view[2]} features, the weights {w.cols}")
+    x_dt, out_dt, dev = _dtype_code(x.dtype, "x"), _dtype_code(out_dtype, "out_dtype"), x.device
+    with _launch_on(dev, stream, (x2, *w._keep)) as handle:     # one context for both launches
+        images = _fp8_images(view, x_dt, save, dev, handle)
+        y = _fp8_product(images[0], w, out_dtype, out_dt, dev, handle)
     y = y if x.dim() == 2 else y.view(*x.shape[:-1], w.rows)
-    return (y, x_t) if save else y
+    return (y, images[1]) if save else y
 
 
 def fp8_linear_backward(dy: torch.Tensor, x_t: Fp8Matrix, w_t: Fp8Matrix, *,
@@ -871,7 +891,8 @@ def fp8_linear_backward(dy: torch.Tensor, x_t: Fp8Matrix, w_t: Fp8Matrix, *,
     unless ``dw`` gives it; ``accumulate`` adds to ``dw``.  Without tokens dW
     is zeros (or stays as it was)."""
     d2 = _flat2(dy)
-    if d2.shape[0] != x_t.cols or d2.shape[1] != w_t.cols:
+    view = _rows_of(d2, "dy")
+    if view[1] != x_t.cols or view[2] != w_t.cols:
         raise ValueError(f"dy is {tuple(d2.shape)}, the images want [{x_t.cols}, {w_t.cols}]")
     if x_t.rows != w_t.rows:
         raise ValueError(f"x has {x_t.rows} features, the weights {w_t.rows}")
@@ -879,9 +900,16 @@ def fp8_linear_backward(dy: torch.Tensor, x_t: Fp8Matrix, w_t: Fp8Matrix, *,
         raise ValueError("accumulate needs dw")
     if dw is not None and tuple(dw.shape) != (w_t.cols, x_t.rows):
         raise ValueError(f"dw must be [{w_t.cols}, {x_t.rows}], got {tuple(dw.shape)}")
-    dq, dq_t = fp8_quantize(d2, images="both", stream=stream)
-    dx = fp8_matmul(dq, w_t, out_dtype=dx_dtype, stream=stream)
-    dw = fp8_matmul(dq_t, x_t, out_dtype=torch.float32, out=dw, accumulate=accumulate, stream=stream)
+    dy_dt, dx_dt, dev = _dtype_code(dy.dtype, "dy"), _dtype_code(dx_dtype, "dx_dtype"), dy.device
+    dw_dt = MO_F32 if dw is None else _dtype_code(dw.dtype, "dw")
+    dw_view = None if dw is None else _rows_of(dw, "dw")
+    with _launch_on(dev, stream, (d2, *x_t._keep, *w_t._keep, dw)) as handle:
+        dq, dq_t = _fp8_images(view, dy_dt, True, dev, handle)
+        dx = _fp8_product(dq, w_t, dx_dtype, dx_dt, dev, handle)
+        if dw is None:
+            dw = _fp8_product(dq_t, x_t, torch.float32, dw_dt, dev, handle)
+        else:
+            check(lib().mo_fp8_matmul(dq_t._struct(), x_t._struct(), dw_view[0], dw_dt, dw_view[3], int(accumulate), handle))
     return dx if dy.dim() == 2 else dx.view(*dy.shape[:-1], w_t.rows), dw
 
 
@@ -1076,7 +1104,9 @@ def balance_loss(logits: torch.Tensor, index: torch.Tensor, *, weight: float = 1
             ws = _scratch(need, handle, dev)
             check(lib().mo_balance_loss(ptr, dt, tokens, experts, ld, ip, top, weight,
                                         grad_loss.data_ptr() if grad_loss is not None else None, loss.data_ptr(),
-                                        counts.data_ptr(), gp, ldg, int(accumulate), ws.data_ptr(), ws.numel(), handle))
+                                        counts.data_ptr(), gp, ldg, int(accumulate),
+                                        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                                        handle))
     return BalanceLoss(loss, counts, g)
 
 

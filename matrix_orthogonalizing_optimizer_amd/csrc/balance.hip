@@ -307,15 +307,17 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a, 
 // Workgroups of the first launch: what they leave is read by one workgroup.
 int groups_of(int64_t tokens) { return static_cast<int>(std::min<int64_t>(512, (tokens + 63) / 64)); }
 
-// One workgroup takes rows in up to kSmall rounds.
-constexpr int64_t kSmall = 4;
-
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Lanes to a row, and whether one workgroup takes all rows, in up to four rounds
+// (37 x 64 in bf16: 19 us in three launches, 14 in one, both with the call's 13).
+int lanes_of(int experts) { return experts <= 64 ? 16 : 64; }
+bool small(int64_t tokens, int experts) { return experts <= 512 && tokens * lanes_of(experts) <= 4 * 1024; }
 
 template <typename T, int L, int C>
 hipError_t run(const BalanceArgs& a, const Partials& w, hipStream_t s) {
   if constexpr (C <= 8) {
-    if (a.tokens * L <= kSmall * 1024) {
+    if (small(a.tokens, a.experts)) {
       balance_small_kernel<T, L, C><<<1, 1024, 0, s>>>(a);
       return hipGetLastError();
     }
@@ -344,6 +346,7 @@ hipError_t run_t(const BalanceArgs& a, const Partials& w, hipStream_t s) {
 }  // namespace
 
 size_t balance_workspace(int64_t tokens, int experts) {
+  if (small(tokens, experts)) return 0;
   const size_t g = static_cast<size_t>(groups_of(tokens)), e = static_cast<size_t>(experts);
   return 2 * align256(g * e * 4) + align256(g * 8) + align256((e + 1) * 4);
 }

@@ -47,7 +47,7 @@ int balance(int dtype, int64_t experts, int64_t top, BalanceArgs a, void* worksp
   a.experts = static_cast<int>(experts);
   a.top = static_cast<int>(top);
   const size_t need = balance_workspace(a.tokens, a.experts);
-  if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+  if (need && (rc = check_workspace(workspace, workspace_bytes, need))) return rc;
   std::vector<Range> ranges;
   add_range(ranges, a.logits, view_bytes(a.tokens, experts, a.ld, esz_of(dtype)), 0, false);
   add_range(ranges, a.index, static_cast<size_t>(a.tokens) * top * 8, 1, false);

@@ -188,8 +188,11 @@ def test_balance_refuses(kw, word):
 def test_balance_workspace():
     n = ctypes.c_size_t()
     f = L.lib().mo_balance_loss_workspace_size
-    assert f(8, 16, ctypes.byref(n)) == L.MO_OK and n.value > 0
-    assert L.lib().mo_balance_loss(*{**_BL, "ws_bytes": n.value - 1}.values()) == L.MO_EWORKSPACE
+    assert f(8, 16, ctypes.byref(n)) == L.MO_OK and n.value == 0            # one workgroup, no workspace
+    assert f(8000, 16, ctypes.byref(n)) == L.MO_OK and n.value > 0
+    a = {**_BL, "tokens": 8000, "logits": BASE << 4, "index": BASE << 5, "grad": BASE << 6, "ws": BASE << 7}
+    assert L.lib().mo_balance_loss(*{**a, "ws_bytes": n.value - 1}.values()) == L.MO_EWORKSPACE
+    assert L.lib().mo_balance_loss(*{**a, "ws": None}.values()) == L.MO_EWORKSPACE
     assert f(-1, 16, ctypes.byref(n)) == L.MO_EINVAL and f(8, 4097, ctypes.byref(n)) == L.MO_EINVAL
     assert f(8, 16, None) == L.MO_EINVAL
 
