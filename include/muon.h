@@ -528,7 +528,7 @@ int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int o
                   int64_t ldo, int accumulate, void* stream);
 
 /* ------------------------------------------------------------------------
- * Cross entropy of a linear layer's logits, without keeping the logits.
+ * Cross entropy of a linear layer's logits, without logits of the caller's.
  *
  * x [rows, hidden], w [vocab, hidden], z = x w^T.  Per row t with target y_t:
  *   loss[t] = log sum_v exp(z_tv) - z_{t, y_t},
@@ -550,7 +550,9 @@ int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int o
  * ---------------------------------------------------------------------- */
 
 /* Workspace of mo_linear_ce.  want_dx, want_dw: whether the call gives dx and
- * dw; dx has x's dtype.  Host-only. */
+ * dw; dx has x's dtype.  With gradients it holds, beside copies of x, of the
+ * weights (1 GiB at most) and of a piece of their transpose, 1 GiB of dz and, up
+ * to 4 GiB, the logits in fp32; larger ones are computed twice.  Host-only. */
 int mo_linear_ce_workspace_size(int64_t rows, int64_t hidden, int64_t vocab, int x_dtype,
                                 int dw_dtype, int want_dx, int want_dw, size_t* bytes);
 

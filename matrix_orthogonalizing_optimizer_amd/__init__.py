@@ -997,8 +997,8 @@ _GRADS = (True, False, "x", "weight")
 def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
                          grad_loss: Optional[torch.Tensor] = None, grad: Union[bool, str] = True,
                          dw: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None):
-    """Cross entropy of the logits ``x weight^T``, which are never kept
-    (``mo_linear_ce``): (loss fp32 [rows], dx, dW).  x [..., hidden] and weight
+    """Cross entropy of the logits ``x weight^T``, which the call does not
+    leave behind (``mo_linear_ce``): (loss fp32 [rows], dx, dW).  x [..., hidden] and weight
     [vocab, hidden] are fp32 or bf16 (rows may be strided) and are multiplied
     in bf16; ``targets`` int64, one per row of x (negative: the row is skipped).
 

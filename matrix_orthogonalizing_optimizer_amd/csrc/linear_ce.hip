@@ -1,14 +1,15 @@
-// Cross entropy of logits z = x W^T that are never kept, with the gradients for
+// Cross entropy of logits z = x W^T that no caller keeps, with the gradients for
 // x and W (gfx950).
 //
 //   loss_t = log sum_v exp z_tv - z_{t, target}
 //   dz_tv = g_t (exp(z_tv - log sum exp z_t) - [v = target]),  dx = dz W,  dW = dz^T x
 //
 // The products run on the matrix cores in bf16 with fp32 sums, in pieces of the
-// vocabulary.  A first product's tiles leave only each row's largest logit and
-// sum of exponentials per wave of columns; a second one, with the row's
-// statistics known, turns its sums into dz, which two further products contract
-// with the piece's weights and with x while it is the only piece that exists.
+// vocabulary.  A first product's tiles leave each row's largest logit and sum of
+// exponentials per tile, and the logits where the workspace holds them.  With the
+// row's statistics known a pass over the logits, or a second product, makes a
+// piece's dz, which two further products contract with the piece's weights and
+// with x.
 #include <algorithm>
 #include <cmath>
 
@@ -136,6 +137,7 @@ struct CeStatsArgs {
   float* target_logit;          // written by the tile that holds the row's target
   float* z;                     // or null: the logits, rows `pitch_z` apart
   int64_t pitch_z;
+  int stream_z;
 };
 
 // Adds (m2, s2) to (m, s).  References of -inf stand for columns of -inf only.
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
   f32x16v acc[C::FM][C::FN];
   tile_sums<C>(p, q, smem, acc);
   if (e.z) {
-    tile_store<C, float>({e.z + e.col0, e.pitch_z, 0, 0, nullptr, 0}, q, smem, acc);
+    tile_store<C, float>({e.z + e.col0, e.pitch_z, 0, 0, nullptr, e.stream_z}, q, smem, acc);
     __syncthreads();
   }
   float2* waves = reinterpret_cast<float2*>(smem);                      // [TM][WN]
@@ -356,8 +358,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
   }
 }
 
-// The same from kept logits: 64 rows x 128 columns per workgroup; HBM bound.
-__global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, const float* z, int rows, int vocab) {
+// The same from a piece of kept logits: 64 rows x 128 columns per workgroup; HBM
+// bound.
+__global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, const float* z, int64_t pitch_z, int rows, int cols) {
   __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kPackRows, c0 = static_cast<int64_t>(blockIdx.x) * kPackCols;
   const int cl = (threadIdx.x & 15) * 8, rl = threadIdx.x >> 4;
@@ -366,20 +369,20 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t t = r0 + rl + 16 * i;
-    const bool in = t < rows && c < vocab;
+    const bool in = t < rows && c < cols;
     f32x4v lo = {}, hi = {};
     if (in) {
-      lo = *reinterpret_cast<const f32x4v*>(z + t * e.vp + c);
-      hi = *reinterpret_cast<const f32x4v*>(z + t * e.vp + c + 4);
+      lo = *reinterpret_cast<const f32x4v*>(z + t * pitch_z + c);
+      hi = *reinterpret_cast<const f32x4v*>(z + t * pitch_z + c + 4);
     }
     const float f = in ? e.factor[t] : 0.0f;
     const float2 st = in ? e.stat[t] : make_float2(0.0f, 0.0f);
-    const int64_t y = in ? e.targets[t] - c : -1;
+    const int64_t y = in ? e.targets[t] - e.col0 - c : -1;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float x = __builtin_amdgcn_exp2f(__builtin_fmaf(k < 4 ? lo[k] : hi[k - 4], kLog2e, -st.x)) * st.y;
       x = f * (k == y ? x - 1.0f : x);
-      v[i][k] = f == 0.0f || c + k >= vocab ? 0.0f : x;
+      v[i][k] = f == 0.0f || c + k >= cols ? 0.0f : x;
     }
   }
   for (int term = 0; term < max(e.terms_x, e.terms_w); ++term) {
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int u = i * 256 + threadIdx.x, cc = u >> 3, r = (u & 7) * 8;
-      if (c0 + cc < vocab && r0 + r < e.tp)
+      if (c0 + cc < cols && r0 + r < e.tp)
         *reinterpret_cast<u32x4v*>(e.dz_t + (c0 + cc) * e.pitch_w + static_cast<int64_t>(term) * e.tp + r0 + r) = column8(tile, r, cc);
     }
     __syncthreads();
@@ -431,9 +434,9 @@ struct Plan {
   int64_t vf, vb;              // columns of a forward and of a backward piece
   int splits, tile_dx;         // of the product for dx
   int terms_x, terms_w;
-  bool keep;                   // all logits are one piece, which stays
+  bool keep;                   // the logits stay
   bool keep_w;                 // so does the bf16 copy of the weights, where they are copied
-  int64_t vz;                  // columns of a piece of dz, padded
+  int64_t pz;                  // their rows' distance
   size_t part, stat, zt, factor, scale, x, w, x_t, w_t, z, dz, dz_t, dxp, total;
 };
 
@@ -486,20 +489,26 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.pt = apart(p.tp);
   p.terms_x = dx ? terms_of(x_dt) : 0;
   p.terms_w = dw ? terms_of(dw_dt) : 0;
-  // A piece's dz and its transpose stay near 256 MiB in all, its weights and their
-  // transpose near 128 each: large enough for whole rounds of tiles.  Where 256
-  // MiB hold the logits of the whole vocabulary, they are a single piece, which
-  // stays in fp32 between the statistics and dz instead of being multiplied again.
+  // Of the workspace: dz and its transpose take up to 1 GiB for a piece, the
+  // weights and their transpose up to 512 MiB each (8192 x 32000 x 512 in bf16 takes
+  // 1.71 ms with a quarter of that for dz, 1.51 with half and 1.29 so; 1021 x
+  // 129283 x 2045 with dw in fp32 3.69 with a quarter of that for weights, 3.40 so).
+  // Logits that 4 GiB hold stay in fp32 between the statistics and dz, instead of
+  // being multiplied again: 8192 x 32000 x 2048 4.04 to 3.36 ms, 8192 x 128256 x
+  // 2048 15.8 to 13.1.  Where the product is quicker than that writing and
+  // reading (x 256 1.12 and 1.08 ms, x 128 0.90 and 0.93), they stay only where
+  // the last-level cache holds them.
   const int64_t r = std::max<int64_t>(rows, 1), vocab_p = up(vocab, 64);
-  p.keep = (dx || dw) && vocab_p <= (int64_t{1} << 21) && r <= (int64_t{1} << 26) / vocab_p;
+  const int64_t held = int64_t{1} << (hidden >= 256 ? 30 : 26);
+  p.keep = (dx || dw) && vocab_p <= held && r <= held / vocab_p;
   const int64_t terms = std::max(p.terms_x + p.terms_w, 2);
-  const int64_t by_w = (int64_t{1} << 26) / p.hp, by_z = p.keep ? by_w : (int64_t{1} << 27) / (terms * r);
+  const int64_t by_w = (int64_t{1} << 28) / p.hp, by_z = (int64_t{1} << 29) / (terms * r);
   p.vb = piece_of(vocab, std::min(std::max(std::min(by_w, by_z) / 256 * 256, int64_t{1024}), int64_t{1} << 20));
-  p.vz = p.keep ? vocab_p : p.vb;
+  p.pz = (vocab_p / 64 | 1) * 64;
   // with gradients a copy of up to 1 GiB is made once, not once for each product
   p.keep_w = (dx || dw) && vocab <= (int64_t{1} << 29) / p.ph;
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
-  const Choice of_dx = choose(rows, hidden, p.vb / 32 * (p.vz > p.vb ? 1 : p.terms_x), true);
+  const Choice of_dx = choose(rows, hidden, p.vb / 32 * p.terms_x, true);
   p.splits = of_dx.splits;
   p.tile_dx = of_dx.tile;
   size_t at = 0;
@@ -518,9 +527,9 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.w = take(static_cast<size_t>(p.keep_w ? vocab : p.vb) * p.ph * 2);
   if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.pt * 2);
   if (dx) p.w_t = take(static_cast<size_t>(hidden) * apart(p.vb) * 2);
-  if (p.keep) p.z = take(t * p.vz * 4);
-  if (dx) p.dz = take(t * apart(p.vz * p.terms_x) * 2);
-  if (dw) p.dz_t = take(static_cast<size_t>(p.vz) * apart(p.tp * p.terms_w) * 2);
+  if (p.keep) p.z = take(t * p.pz * 4);
+  if (dx) p.dz = take(t * apart(p.vb * p.terms_x) * 2);
+  if (dw) p.dz_t = take(static_cast<size_t>(p.vb) * apart(p.tp * p.terms_w) * 2);
   if (dx) p.dxp = take(static_cast<size_t>(p.splits) * t * p.hp * 4);
   p.total = rows ? at : 0;
   return p;
@@ -614,7 +623,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
                   apart(up(v, 64)), nullptr, s));
     logits.b = operand(v0);
     logits.n = v;
-    const CeStatsArgs e{a.targets, v0, part, zt, z, pl.vz};
+    const CeStatsArgs e{a.targets, v0, part, zt, z, pl.pz, pl.keep && worth_streaming(z, pl.pz, a.rows, a.vocab)};
     int cols;
     const int tile = choose(a.rows, v, logits.stages, false).tile;
     if (tile == 256) MO_TRY(run_stats<Cfg256>(logits, e, cols, s));
@@ -628,12 +637,6 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   }
   if (!grad) return hipSuccess;
 
-  if (pl.keep) {
-    const dim3 g(static_cast<uint32_t>((a.vocab + kPackCols - 1) / kPackCols), static_cast<uint32_t>((a.rows + kPackRows - 1) / kPackRows));
-    ce_kept_grad_kernel<<<g, 256, 0, s>>>({a.targets, 0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(pl.vz), static_cast<int>(pl.tp),
-                                           apart(pl.vz * pl.terms_x), apart(pl.tp * pl.terms_w)}, z, a.rows, a.vocab);
-    MO_TRY(hipGetLastError());
-  }
   for (int64_t v0 = 0; v0 < a.vocab; v0 += pl.vb) {
     const int v = static_cast<int>(std::min<int64_t>(pl.vb, a.vocab - v0));
     const int64_t vp = up(v, 64), pv = apart(vp);
@@ -642,36 +645,35 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     if (need_w || need_w_t)
       MO_TRY(copied ? pack(BF16, operand(v0), pl.ph, v, a.hidden, nullptr, 0, w_t, pv, nullptr, s)
                     : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.ph, need_w_t ? w_t : nullptr, pv, nullptr, s));
-    if (!pl.keep) {
+    const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp),
+                       apart(vp * pl.terms_x), apart(pl.tp * pl.terms_w)};
+    if (pl.keep) {
+      const dim3 g(static_cast<uint32_t>((v + kPackCols - 1) / kPackCols), static_cast<uint32_t>((a.rows + kPackRows - 1) / kPackRows));
+      ce_kept_grad_kernel<<<g, 256, 0, s>>>(e, z + v0, pl.pz, a.rows, v);
+      MO_TRY(hipGetLastError());
+    } else {
       logits.b = operand(v0);
       logits.n = v;
-      const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp),
-                         apart(vp * pl.terms_x), apart(pl.tp * pl.terms_w)};
       const int tile = choose(a.rows, v, logits.stages, false).tile;
       MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
     }
     if (want_dx) {
-      // a piece's terms lie side by side along the contraction; where the logits
-      // are kept and the weights come in pieces, a whole row apart
-      const int64_t term_at = pl.keep ? pl.vz : vp;
-      const int calls = term_at == vp ? 1 : pl.terms_x;
+      // a piece's terms lie side by side along the contraction
       ProductArgs p{};
+      p.a = reinterpret_cast<const uint8_t*>(dz);
       p.b = reinterpret_cast<const uint8_t*>(w_t);
-      p.pitch_a = static_cast<uint32_t>(apart(term_at * pl.terms_x) * 2);
+      p.pitch_a = static_cast<uint32_t>(apart(vp * pl.terms_x) * 2);
       p.pitch_b = static_cast<uint32_t>(pv * 2);
       p.m = a.rows;
       p.n = a.hidden;
       p.stages_b = static_cast<int>(vp / 32);
-      p.stages = p.stages_b * (calls == 1 ? pl.terms_x : 1);
+      p.stages = p.stages_b * pl.terms_x;
       p.splits = pl.splits;
-      for (int term = 0; term < calls; ++term) {
-        p.a = reinterpret_cast<const uint8_t*>(dz + (pl.keep ? term * term_at + v0 : 0));
-        MO_TRY((store<float>(pl.tile_dx, p, {dxp, pl.hp, static_cast<int64_t>(a.rows) * pl.hp, v0 > 0 || term > 0, nullptr, 0}, s)));
-      }
+      MO_TRY((store<float>(pl.tile_dx, p, {dxp, pl.hp, static_cast<int64_t>(a.rows) * pl.hp, v0 > 0, nullptr, 0}, s)));
     }
     if (want_dw) {
       ProductArgs p{};
-      p.a = reinterpret_cast<const uint8_t*>(dz_t + (pl.keep ? v0 * apart(pl.tp * pl.terms_w) : 0));
+      p.a = reinterpret_cast<const uint8_t*>(dz_t);
       p.b = reinterpret_cast<const uint8_t*>(x_t);
       p.pitch_a = static_cast<uint32_t>(apart(pl.tp * pl.terms_w) * 2);
       p.pitch_b = static_cast<uint32_t>(pl.pt * 2);

@@ -114,11 +114,17 @@ def test_strided_operands_and_accumulation(dwd):
 
 
 @pytest.mark.parametrize("t,h,v,wd,dwd", [
-    (2200, 64, 33000, BF16, BF16),        # several pieces of dz, tiles of 256
+    (2200, 64, 33000, BF16, BF16),        # logits computed twice, tiles of 256
     (2200, 72, 33000, F32, F32),          # the same, packed operands, three terms
-    (40, 4096, 33000, BF16, F32),         # kept logits, several pieces of weights
+    (9000, 64, 33000, BF16, BF16),        # the same in several pieces of dz
+    (4500, 72, 33001, F32, F32),
+    (4500, 256, 33001, BF16, F32),        # kept logits, several pieces of dz
+    (50, 130, 1400001, F32, F32),         # weights copied for each product, logits computed twice
+    (24, 20000, 27001, F32, BF16),        # the same with kept logits, several pieces of weights
+    (40, 4096, 66000, BF16, F32),
+    (40, 4096, 33000, BF16, F32),         # kept logits
     (24, 4100, 33000, F32, BF16),
-    (4500, 128, 15001, BF16, BF16),       # two pieces, odd columns
+    (4500, 128, 15001, BF16, BF16),       # computed twice, odd columns
     (3, 4, 4194300, F32, BF16),           # more rows of weights than 65535 times 64
 ])
 def test_pieces(t, h, v, wd, dwd):
