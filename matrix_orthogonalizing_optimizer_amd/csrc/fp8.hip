@@ -325,11 +325,11 @@ static hipError_t run_op(const TileCost (&cost)[3], const ProductArgs& p, const 
   for (int i = 0; i < 3; ++i) us[i] = tile_us(cost[i], a.m, a.n, p.stages, 1);
   if constexpr (Op::kDecoded) {
     const double sliced = tile_us(kCostSliced, a.m, a.n, p.stages, 1);
-    if (sliced <= us[0] && sliced <= us[1] && sliced <= us[2]) return run<TileCfgT<Op, 64, 64, 2, 2, 4, true>, T>(p, a, s);
+    if (sliced <= us[0] && sliced <= us[1] && sliced <= us[2]) return run<TileCfgT<Op, 64, 64, 2, 2, 5, true>, T>(p, a, s);
   }
-  if (us[2] <= us[1] && us[2] <= us[0]) return run<TileCfgT<Op, 256, 256, 2, 4, 4>, T>(p, a, s);
-  if (us[1] <= us[0]) return run<TileCfgT<Op, 128, 128, 2, 2, 4>, T>(p, a, s);
-  return run<TileCfgT<Op, 64, 64, 2, 2, 6>, T>(p, a, s);
+  if (us[2] <= us[1] && us[2] <= us[0]) return run<TileCfgT<Op, 256, 256, 2, 4, 5>, T>(p, a, s);
+  if (us[1] <= us[0]) return run<TileCfgT<Op, 128, 128, 2, 2, 5>, T>(p, a, s);
+  return run<TileCfgT<Op, 64, 64, 2, 2, 7>, T>(p, a, s);
 }
 
 hipError_t launch_fp8_matmul(int out_dt, const Fp8MatmulArgs& a, hipStream_t s) {

@@ -447,9 +447,9 @@ int64_t piece_of(int64_t vocab, int64_t most) {
 }
 
 
-typedef TileCfgT<OpBf16, 64, 64, 2, 2, 6> Cfg64;
-typedef TileCfgT<OpBf16, 128, 128, 2, 2, 4> Cfg128;
-typedef TileCfgT<OpBf16, 256, 256, 2, 4, 4> Cfg256;
+typedef TileCfgT<OpBf16, 64, 64, 2, 2, 7> Cfg64;
+typedef TileCfgT<OpBf16, 128, 128, 2, 2, 5> Cfg128;
+typedef TileCfgT<OpBf16, 256, 256, 2, 4, 5> Cfg256;
 
 // Measured (see tile_us): 4096 x 4096 x 8192 takes 230 us in tiles of 256, 2048
 // x 2048 x 8192 80 in tiles of 128 and 149 in 64 tiles of 256, 1024 x 1024 x 8192

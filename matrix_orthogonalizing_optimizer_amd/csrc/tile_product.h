@@ -73,21 +73,22 @@ __device__ __forceinline__ void decode16(u32x4v x, float s, u32x4v& lo, u32x4v& 
     hi[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 + w], s, true));
   }
 }
-// TM x TN outputs, WM x WN waves, a ring of NST stages in LDS.  Sliced: each wave
+// TM x TN outputs, WM x WN waves, in LDS rings of NA stages of A (odd) and one
+// less of B.  Sliced: each wave
 // takes a part of the contraction for all outputs, with a ring of its own, and
 // the waves' sums meet at the end; a wave then has its WM x WN part of them.
-template <class OpT, int TMv, int TNv, int WMv, int WNv, int NSTv, bool kSlicedv = false>
+template <class OpT, int TMv, int TNv, int WMv, int WNv, int NAv, bool kSlicedv = false>
 struct TileCfgT {
   typedef OpT Op;
-  static constexpr int TM = TMv, TN = TNv, WM = WMv, WN = WNv, NST = NSTv, NW = WM * WN;
+  static constexpr int TM = TMv, TN = TNv, WM = WMv, WN = WNv, NA = NAv, NB = NA - 1, NW = WM * WN;
   static constexpr bool kSliced = kSlicedv;
   static constexpr int FM = TM / (32 * WM), FN = TN / (32 * WN);
   static constexpr int kThreads = 64 * NW;
   static constexpr int kMinWaves = FM * FN >= 16 ? 1 : 2;        // per SIMD: 256 sums a lane leave room for one
-  static constexpr int kStage = (TM + TN) * 64, kScaleGroup = Op::kScaled ? (TM + TN) * 16 : 0;
+  static constexpr int kStageA = TM * 64, kStageB = TN * 64, kScaleGroup = Op::kScaled ? (TM + TN) * 16 : 0;
   // what the epilogues need to turn 32 rows per wave
   static constexpr int kTurnPitch = TN / WN * 4 + 16;
-  static constexpr int kRings = NST * kStage + 2 * kScaleGroup, kRing = (kSliced ? NW : 1) * kRings, kTurn = NW * 32 * kTurnPitch;
+  static constexpr int kRings = NA * kStageA + NB * kStageB + 2 * kScaleGroup, kRing = (kSliced ? NW : 1) * kRings, kTurn = NW * 32 * kTurnPitch;
   static constexpr int kLds = kRing > kTurn ? kRing : kTurn;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
 };
@@ -184,11 +185,12 @@ template <class C>
 __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace& q, int wave, int wm, int wn, int k0, int k1, uint8_t* smem,
                                           f32x16v (&acc)[C::FM][C::FN]) {
   typedef typename C::Op Op;
-  constexpr int TM = C::TM, TN = C::TN, NW = C::NW, FM = C::FM, FN = C::FN, NST = C::NST, kStage = C::kStage;
-  constexpr int DA = TM / (16 * NW), DB = TN / (16 * NW), DPW = DA + DB;      // requests of a wave and stage
+  constexpr int TM = C::TM, TN = C::TN, NW = C::NW, FM = C::FM, FN = C::FN, NA = C::NA, NB = C::NB;
+  constexpr int kStageA = C::kStageA, kStageB = C::kStageB;
+  constexpr int D = TM / (16 * NW), DP = 2 * D;                               // requests of a wave for a stage and a pair of one operand
   constexpr int DS = Op::kScaled ? ((TM + TN) / 64 + NW - 1) / NW : 0;        // and of a group of scales
-  constexpr int kScales = NST * kStage;
-  static_assert(NST % 2 == 0, "stages come in pairs");
+  constexpr int kRingB = NA * kStageA, kScales = kRingB + NB * kStageB;
+  static_assert(TM == TN && NA % 2 == 1 && NA >= 5, "pairs of stages, of both operands alike");
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -202,30 +204,37 @@ __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace&
   // Requests.  Lane l copies chunk l & 3 of row l / 4 of 16 rows, so it fetches
   // the chunk that is stored there.
   const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
-  uint32_t arow[DA], brow[DB];
+  uint32_t arow[D], brow[D];
 #pragma unroll
-  for (int i = 0; i < DA; ++i) arow[i] = min(16 * (wave * DA + i) + lane / 4, q.mlast) * p.pitch_a + chunk * 16;
-#pragma unroll
-  for (int i = 0; i < DB; ++i) brow[i] = min(16 * (wave * DB + i) + lane / 4, q.nlast) * p.pitch_b + chunk * 16;
+  for (int i = 0; i < D; ++i) {
+    arow[i] = min(16 * (wave * D + i) + lane / 4, q.mlast) * p.pitch_a + chunk * 16;
+    brow[i] = min(16 * (wave * D + i) + lane / 4, q.nlast) * p.pitch_b + chunk * 16;
+  }
   const uint32_t lds0 = lds_addr(smem);
-  const uint32_t dst = lds0 + wave * DA * 1024, dstb = lds0 + TM * 64 + wave * DB * 1024;
-  int tp = 0, kb = __builtin_amdgcn_readfirstlane(k0 % p.stages_b);           // the stage being requested, and b's
+  const uint32_t dst = lds0 + wave * D * 1024, dstb = dst + kRingB;
+  int tp = 0, kb = __builtin_amdgcn_readfirstlane(k0 % p.stages_b);           // the pair being requested: its first stage, and b's
   const uint8_t *pa = a0, *pb = uniform_ptr(b00 + static_cast<int64_t>(kb) * 64);
   uint64_t lanes = ~uint64_t{0};                            // which of them request
   auto advance = [&]() __attribute__((always_inline)) {
-    ++tp;
-    ++kb;
-    pa = uniform_ptr(pa + 64);
+    tp += 2;
+    kb += 2;
+    pa = uniform_ptr(pa + 128);
     const bool wrap = kb == p.stages_b;
     kb = wrap ? 0 : kb;
-    pb = uniform_ptr(wrap ? b00 : pb + 64);
+    pb = uniform_ptr(wrap ? b00 : pb + 128);
     const uint32_t half_wave = __builtin_amdgcn_readfirstlane(tp < stages ? -1 : 0);
     lanes = static_cast<uint64_t>(half_wave) << 32 | half_wave;
   };
-  auto request = [&](auto I, uint32_t to) __attribute__((always_inline)) {
-    constexpr int i = I;
-    if constexpr (i < DA) lds_dma16_masked<i * 1024>(pa, arow[i], dst + to, lanes);
-    else lds_dma16_masked<(i - DA) * 1024>(pb, brow[i - DA], dstb + to, lanes);
+  // request I of a pair's DP: the two stages of the same rows in turn
+  auto request_a = [&](auto I, uint32_t to0, uint32_t to1) __attribute__((always_inline)) {
+    constexpr int i = I / 2;
+    if constexpr (I % 2 == 0) lds_dma16_masked<i * 1024>(pa, arow[i], dst + to0, lanes);
+    else lds_dma16_masked<i * 1024>(uniform_ptr(pa + 64), arow[i], dst + to1, lanes);
+  };
+  auto request_b = [&](auto I, uint32_t to0, uint32_t to1) __attribute__((always_inline)) {
+    constexpr int i = I / 2;
+    if constexpr (I % 2 == 0) lds_dma16_masked<i * 1024>(pb, brow[i], dstb + to0, lanes);
+    else lds_dma16_masked<i * 1024>(uniform_ptr(pb + 64), brow[i], dstb + to1, lanes);
   };
   // Scale bytes: 64 rows a request, 16 bytes of each (groups of 16 blocks); two
   // groups in turn.
@@ -245,7 +254,7 @@ __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace&
 
   // Fragments: 32 rows, lane l holds row l & 31.
   const uint8_t* abase = smem + (wm * (TM / C::WM) + q.r32) * 64;
-  const uint8_t* bbase = smem + TM * 64 + (wn * (TN / C::WN) + q.r32) * 64;
+  const uint8_t* bbase = smem + kRingB + (wn * (TN / C::WN) + q.r32) * 64;
   const uint8_t* asbase = smem + kScales + (wm * (TM / C::WM) + q.r32) * 16;
   const uint8_t* bsbase = smem + kScales + (TM + wn * (TN / C::WN) + q.r32) * 16;
   uint32_t xs[2];
@@ -255,11 +264,11 @@ __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace&
   uint32_t sa[FM] = {}, sb[FN] = {}, san[FM] = {}, sbn[FN] = {};
   // reading r of a stage's 2 (FM + FN), in the order of need: A's first rows, B, the rest of A
   constexpr int NR = 2 * (FM + FN);
-  auto read = [&](auto R, auto set, uint32_t at) __attribute__((always_inline)) {
+  auto read = [&](auto R, auto set, uint32_t at, uint32_t at_b) __attribute__((always_inline)) {
     constexpr int f = R / 2, s = R % 2, S = set;
     constexpr int fa = f == 0 ? 0 : f > FN ? f - FN : -1, fb = f >= 1 && f <= FN ? f - 1 : -1;
     if constexpr (fa >= 0) af[S][fa][s] = *reinterpret_cast<const u32x4v*>(abase + (at + xs[s]) + fa * 32 * 64);
-    if constexpr (fb >= 0) bf[S][fb][s] = *reinterpret_cast<const u32x4v*>(bbase + (at + xs[s]) + fb * 32 * 64);
+    if constexpr (fb >= 0) bf[S][fb][s] = *reinterpret_cast<const u32x4v*>(bbase + (at_b + xs[s]) + fb * 32 * 64);
   };
   auto read_scales = [&](int block) __attribute__((always_inline)) {
     if constexpr (Op::kScaled) {
@@ -285,41 +294,48 @@ __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace&
 
   request_scales(block0 >> 4);
   if ((block0 & 15) && (block0 >> 4) + 1 < groups) request_scales((block0 >> 4) + 1);
-  unroll<NST>([&](auto Q) __attribute__((always_inline)) {
+  unroll<NB / 2>([&](auto Q) __attribute__((always_inline)) {
     if constexpr (Q > 0) advance();
-    unroll<DPW>([&](auto I) __attribute__((always_inline)) { request(I, static_cast<uint32_t>(Q * kStage)); });
+    unroll<DP>([&](auto I) __attribute__((always_inline)) { request_a(I, 2 * Q * kStageA, (2 * Q + 1) * kStageA); });
+    unroll<DP>([&](auto I) __attribute__((always_inline)) { request_b(I, 2 * Q * kStageB, (2 * Q + 1) * kStageB); });
   });
-  wait_loads<(NST - 1) * DPW>();
+  wait_loads<(NB - 2) * DP>();
   meet();
-  unroll<NR>([&](auto R) __attribute__((always_inline)) { read(R, std::integral_constant<int, 0>{}, 0u); });
+  unroll<NR>([&](auto R) __attribute__((always_inline)) { read(R, std::integral_constant<int, 0>{}, 0u, 0u); });
   read_scales(block0);
   take_scales();
 
   constexpr int NP = FM * FN;
   // columns forth and back, so that a product keeps one operand of the last
   constexpr auto snake = [](int p) constexpr { return p / FN % 2 ? FN - 1 - p % FN : p % FN; };
-  uint32_t at = 0;                                         // place of the stage in registers
+  uint32_t at = 0, at_b = 0;                               // places of the stage in registers
   for (int t = 0; t < stages; t += 2) {
     unroll<2>([&](auto S) __attribute__((always_inline)) {
       constexpr int cur = S, nxt = cur ^ 1;
       // this wave's reads of the stage are done, its part of the next has come
-      wait_loads<(NST - 2) * DPW>();
+      wait_loads<(NB - 2 - cur) * DP>();
       meet();
-      uint32_t next = 0;
+      uint32_t next = 0, next_b = 0, last = 0;
       // what goes with product P of N; the stage's bookkeeping too comes behind
       // its first product, as nothing else would keep the matrix cores busy
       auto besides = [&](auto P, auto N) __attribute__((always_inline)) {
-        constexpr int n = N, r0 = P * NR / n, r1 = (P + 1) * NR / n, l0 = P * DPW / n, l1 = (P + 1) * DPW / n;
+        constexpr int n = N, r0 = P * NR / n, r1 = (P + 1) * NR / n, l0 = P * DP / n, l1 = (P + 1) * DP / n;
         if constexpr (P == 0) {
-          next = at + kStage == NST * kStage ? 0u : at + kStage;
+          next = at + kStageA == NA * kStageA ? 0u : at + kStageA;
+          next_b = cur == 1 && at_b + kStageB == NB * kStageB ? 0u : at_b + kStageB;
+          last = at == 0 ? (NA - 1) * kStageA : at - kStageA;
           if constexpr (Op::kScaled && cur == 0)
             if (const int b = block0 + t / 2; (b & 15) == 0 && (b >> 4) + 1 < groups) request_scales((b >> 4) + 1);
-          advance();
+          if constexpr (cur == 0) advance();
         }
         unroll<r1 - r0>([&](auto R) __attribute__((always_inline)) {
-          read(std::integral_constant<int, r0 + decltype(R)::value>{}, std::integral_constant<int, nxt>{}, next);
+          read(std::integral_constant<int, r0 + decltype(R)::value>{}, std::integral_constant<int, nxt>{}, next, next_b);
         });
-        unroll<l1 - l0>([&](auto L) __attribute__((always_inline)) { request(std::integral_constant<int, l0 + decltype(L)::value>{}, at); });
+        unroll<l1 - l0>([&](auto L) __attribute__((always_inline)) {
+          constexpr auto l = std::integral_constant<int, l0 + decltype(L)::value>{};
+          if constexpr (cur == 0) request_a(l, last, at);
+          else request_b(l, at_b - kStageB, at_b);
+        });
         if constexpr (cur == 1 && P == n - 1) read_scales(block0 + t / 2 + 1);
       };
       if constexpr (Op::kDecoded) {
@@ -352,6 +368,7 @@ __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace&
       }
       if constexpr (cur == 1) take_scales();
       at = next;
+      at_b = next_b;
     });
   }
   wait_loads<0>();                                         // no request outlives the workgroup
@@ -366,7 +383,7 @@ __device__ __forceinline__ void tile_sums(const ProductArgs& p, const TilePlace&
     ring_sums<C>(p, q, wave, q.wm, q.wn, k0, k1, smem, acc);
   } else {
     static_assert(C::FM == 1 && C::FN == 1, "a wave keeps one block of 32 x 32");
-    typedef TileCfgT<typename C::Op, C::TM, C::TN, 1, 1, C::NST> One;
+    typedef TileCfgT<typename C::Op, C::TM, C::TN, 1, 1, C::NA> One;
     const int pairs = (k1 - k0) / 2, per = (pairs + C::NW - 1) / C::NW;
     const int s0 = k0 + 2 * min(wave * per, pairs), s1 = k0 + 2 * min(wave * per + per, pairs);
     f32x16v sums[One::FM][One::FN];
