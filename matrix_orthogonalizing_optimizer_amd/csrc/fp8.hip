@@ -310,26 +310,22 @@ static hipError_t run(const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t 
   return run_product_store<C, T>(p, {static_cast<T*>(a.out), a.ldo, 0, a.accumulate, nullptr, worth_streaming(static_cast<T*>(a.out), a.ldo, a.m, a.n)}, s);
 }
 
-// Measured (see tile_us), in tiles of 64, 128 and 256: 1024 x 1024 x 8192 26, 2048
-// x 2048 x 8192 44, 4096 x 4096 x 8192 114 us from codes, 38, 76 and 201 decoded.
-constexpr TileCost kCostCodes[3] = {{64, 3, 4.0, 0.15, 0.15}, {128, 2, 7.0, 0.25, 0.29}, {256, 1, 13.0, 0.60, 0.78}};
-constexpr TileCost kCostExact[3] = {{64, 3, 5.0, 0.25, 0.20}, {128, 2, 7.0, 0.52, 0.43}, {256, 1, 16.0, 1.10, 1.45}};
-// Decoded, with the contraction in four parts (each wave then decodes its own
-// codes for all 64 x 64 outputs, half as many): 1024 x 1024 x 8192 25 us, while a
-// CU has no second tile.  (From codes 23.5 instead of 25.6: not worth a kernel.)
-constexpr TileCost kCostSliced = {64, 1, 5.5, 0.15, 0.15};
+// Measured (see tile_us), in tiles of 64, 128 and 256: 1024 x 1024 x 8192 25, 2048
+// x 2048 x 8192 40, 4096 x 4096 x 8192 104 us from codes, 22, 72 and 200 decoded.
+constexpr TileCost kCostCodes[3] = {{64, 2, 4.5, 0.16, 0.13}, {128, 2, 8.0, 0.25, 0.22}, {256, 1, 12.0, 0.60, 0.705}};
+constexpr TileCost kCostExact[3] = {{64, 1, 5.5, 0.12, 0.124}, {128, 2, 8.0, 0.50, 0.40}, {256, 1, 14.0, 1.10, 1.40}};
 
 template <class Op, typename T>
 static hipError_t run_op(const TileCost (&cost)[3], const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t s) {
   double us[3];
   for (int i = 0; i < 3; ++i) us[i] = tile_us(cost[i], a.m, a.n, p.stages, 1);
-  if constexpr (Op::kDecoded) {
-    const double sliced = tile_us(kCostSliced, a.m, a.n, p.stages, 1);
-    if (sliced <= us[0] && sliced <= us[1] && sliced <= us[2]) return run<TileCfgT<Op, 64, 64, 2, 2, 5, true>, T>(p, a, s);
-  }
   if (us[2] <= us[1] && us[2] <= us[0]) return run<TileCfgT<Op, 256, 256, 2, 4, 5>, T>(p, a, s);
   if (us[1] <= us[0]) return run<TileCfgT<Op, 128, 128, 2, 2, 5>, T>(p, a, s);
-  return run<TileCfgT<Op, 64, 64, 2, 2, 7>, T>(p, a, s);
+  // Decoded, the waves share the contraction: each then decodes its own codes for
+  // all 64 x 64 outputs, half as many, and 1024 x 1024 x 8192 takes 22 us instead
+  // of 43.  (From codes 23.5 instead of 25.6, and one tile a CU instead of two.)
+  if constexpr (Op::kDecoded) return run<TileCfgT<Op, 64, 64, 2, 2, 5, true>, T>(p, a, s);
+  else return run<TileCfgT<Op, 64, 64, 2, 2, 7>, T>(p, a, s);
 }
 
 hipError_t launch_fp8_matmul(int out_dt, const Fp8MatmulArgs& a, hipStream_t s) {

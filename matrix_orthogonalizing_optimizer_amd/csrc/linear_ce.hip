@@ -451,10 +451,9 @@ typedef TileCfgT<OpBf16, 64, 64, 2, 2, 7> Cfg64;
 typedef TileCfgT<OpBf16, 128, 128, 2, 2, 5> Cfg128;
 typedef TileCfgT<OpBf16, 256, 256, 2, 4, 5> Cfg256;
 
-// Measured (see tile_us): 4096 x 4096 x 8192 takes 230 us in tiles of 256, 2048
-// x 2048 x 8192 80 in tiles of 128 and 149 in 64 tiles of 256, 1024 x 1024 x 8192
-// 41 in tiles of 64.
-constexpr TileCost kCost64{64, 3, 5.0, 0.13, 0.13}, kCost128{128, 2, 6.0, 0.22, 0.30}, kCost256{256, 1, 11.0, 0.54, 0.86};
+// Measured (see tile_us): 4096 x 4096 x 8192 takes 211 us in tiles of 256, 2048
+// x 2048 x 8192 70 in tiles of 128, 1024 x 1024 x 8192 39 in tiles of 64.
+constexpr TileCost kCost64{64, 3, 4.5, 0.137, 0.108}, kCost128{128, 2, 7.0, 0.24, 0.222}, kCost256{256, 1, 10.0, 0.45, 0.765};
 
 // The quickest tile for a product, and how many workgroups should share each
 // tile's contraction (their parts are written, and read by the pass that adds
