@@ -310,22 +310,32 @@ static hipError_t run(const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t 
   return run_product_store<C, T>(p, {static_cast<T*>(a.out), a.ldo, 0, a.accumulate, nullptr, worth_streaming(static_cast<T*>(a.out), a.ldo, a.m, a.n)}, s);
 }
 
-// Measured (see tile_us), in tiles of 64, 128 and 256: 1024 x 1024 x 8192 25, 2048
-// x 2048 x 8192 40, 4096 x 4096 x 8192 104 us from codes, 22, 72 and 200 decoded.
+// Measured (see tile_us), in tiles of 64, 128 and 256: 1024 x 1024 x 8192 24, 2048
+// x 2048 x 8192 40, 4096 x 4096 x 8192 104 us from codes; in sliced tiles of 64 and
+// in tiles of 128 and 256 22, 72 and 200 decoded.
 constexpr TileCost kCostCodes[3] = {{64, 2, 4.5, 0.16, 0.13}, {128, 2, 8.0, 0.25, 0.22}, {256, 1, 12.0, 0.60, 0.705}};
 constexpr TileCost kCostExact[3] = {{64, 1, 5.5, 0.12, 0.124}, {128, 2, 8.0, 0.50, 0.40}, {256, 1, 14.0, 1.10, 1.40}};
+// Few tiles of a long contraction are bound by the waits of a wave that adds all
+// of it up: sliced, 64 x 1024 x 8192 takes 12.3 instead of 22.3 us and 1024 x 1024 x
+// 8192 17.2 instead of 24.2; 64 x 1024 x 1024 8.2 instead of 6.0, 64 x 28672 x 8192
+// 42 instead of 39.  Decoded, each wave then decodes its own codes, half as many in
+// all, and 64 x 64 tiles are always sliced (1024 x 1024 x 8192 22 instead of 43).
+constexpr TileCost kCostSliced = {64, 1, 6.4, 0.04, 0.10};
 
 template <class Op, typename T>
 static hipError_t run_op(const TileCost (&cost)[3], const ProductArgs& p, const Fp8MatmulArgs& a, hipStream_t s) {
   double us[3];
   for (int i = 0; i < 3; ++i) us[i] = tile_us(cost[i], a.m, a.n, p.stages, 1);
+  bool sliced = Op::kDecoded;
+  if (const double v = tile_us(kCostSliced, a.m, a.n, p.stages, 1); !Op::kDecoded && v < us[0]) {
+    sliced = true;
+    us[0] = v;
+  }
   if (us[2] <= us[1] && us[2] <= us[0]) return run<TileCfgT<Op, 256, 256, 2, 4, 5>, T>(p, a, s);
   if (us[1] <= us[0]) return run<TileCfgT<Op, 128, 128, 2, 2, 5>, T>(p, a, s);
-  // Decoded, the waves share the contraction: each then decodes its own codes for
-  // all 64 x 64 outputs, half as many, and 1024 x 1024 x 8192 takes 22 us instead
-  // of 43.  (From codes 23.5 instead of 25.6, and one tile a CU instead of two.)
-  if constexpr (Op::kDecoded) return run<TileCfgT<Op, 64, 64, 2, 2, 5, true>, T>(p, a, s);
-  else return run<TileCfgT<Op, 64, 64, 2, 2, 7>, T>(p, a, s);
+  if constexpr (!Op::kDecoded)
+    if (!sliced) return run<TileCfgT<Op, 64, 64, 2, 2, 7>, T>(p, a, s);
+  return run<TileCfgT<Op, 64, 64, 2, 2, 5, true>, T>(p, a, s);
 }
 
 hipError_t launch_fp8_matmul(int out_dt, const Fp8MatmulArgs& a, hipStream_t s) {

@@ -426,13 +426,64 @@ __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int s
   }
 }
 
+// ------------------------------------------------------------ tiles
+typedef TileCfgT<OpBf16, 64, 64, 2, 2, 7> Cfg64;
+typedef TileCfgT<OpBf16, 64, 64, 2, 2, 5, true> Cfg64Sliced;
+typedef TileCfgT<OpBf16, 128, 128, 2, 2, 5> Cfg128;
+typedef TileCfgT<OpBf16, 256, 256, 2, 4, 5> Cfg256;
+
+// Measured (see tile_us): 4096 x 4096 x 8192 takes 211 us in tiles of 256, 2048
+// x 2048 x 8192 70 in tiles of 128, 1024 x 1024 x 8192 39 in tiles of 64 and 30 in
+// sliced ones; 64 x 1024 x 8192 37 and 19, 64 x 1024 x 512 5.4 and 5.8, 64 x 32000 x
+// 2048 22 and 28.
+enum Tile { kTile64, kTile64Sliced, kTile128, kTile256, kTiles };
+constexpr TileCost kCosts[kTiles] = {{64, 3, 4.5, 0.137, 0.108}, {64, 1, 5.6, 0.055, 0.10}, {128, 2, 7.0, 0.24, 0.222}, {256, 1, 10.0, 0.45, 0.765}};
+
+// The quickest tile for a product, and how many workgroups should share each
+// tile's contraction (their parts are written, and read by the pass that adds
+// them, at 4 TB/s).
+struct Choice {
+  Tile tile;
+  int splits;
+};
+Choice choose(int64_t m, int64_t n, int64_t stages, bool may_split) {
+  Choice best{kTile64, 1};
+  double least = 1e30;
+  for (int t = 0; t < kTiles; ++t)
+    for (int s = 1; s == 1 || (may_split && s <= 64 && stages >= 16 * s); s *= 2) {
+      const double us = tile_us(kCosts[t], m, n, (stages + s - 1) / s, s) + (s - 1) * static_cast<double>(m) * n * 8 / 4e6;
+      if (us < least) {
+        least = us;
+        best = {static_cast<Tile>(t), s};
+      }
+    }
+  return best;
+}
+
+// f with the configuration of a tile.
+template <class F>
+hipError_t with(Tile t, F f) {
+  switch (t) {
+    case kTile256: return f(Cfg256{});
+    case kTile128: return f(Cfg128{});
+    case kTile64Sliced: return f(Cfg64Sliced{});
+    default: return f(Cfg64{});
+  }
+}
+
+template <typename T>
+hipError_t store(Tile tile, const ProductArgs& p, const StoreArgs<T>& e, hipStream_t s) {
+  return with(tile, [&](auto c) { return run_product_store<decltype(c), T>(p, e, s); });
+}
+
 // ------------------------------------------------------------ the plan
 // Pieces of the vocabulary, and the places of everything in the workspace.
 struct Plan {
   int64_t hp, tp;              // hidden size and rows, padded to whole pairs of stages
   int64_t ph, pt;              // and how far apart rows of that length lie
   int64_t vf, vb;              // columns of a forward and of a backward piece
-  int splits, tile_dx;         // of the product for dx
+  int splits;                  // of the product for dx
+  Tile tile_dx;
   int terms_x, terms_w;
   bool keep;                   // the logits stay
   bool keep_w;                 // so does the bf16 copy of the weights, where they are copied
@@ -447,39 +498,6 @@ int64_t piece_of(int64_t vocab, int64_t most) {
 }
 
 
-typedef TileCfgT<OpBf16, 64, 64, 2, 2, 7> Cfg64;
-typedef TileCfgT<OpBf16, 128, 128, 2, 2, 5> Cfg128;
-typedef TileCfgT<OpBf16, 256, 256, 2, 4, 5> Cfg256;
-
-// Measured (see tile_us): 4096 x 4096 x 8192 takes 211 us in tiles of 256, 2048
-// x 2048 x 8192 70 in tiles of 128, 1024 x 1024 x 8192 39 in tiles of 64.
-constexpr TileCost kCost64{64, 3, 4.5, 0.137, 0.108}, kCost128{128, 2, 7.0, 0.24, 0.222}, kCost256{256, 1, 10.0, 0.45, 0.765};
-
-// The quickest tile for a product, and how many workgroups should share each
-// tile's contraction (their parts are written, and read by the pass that adds
-// them, at 4 TB/s).
-struct Choice {
-  int tile, splits;
-};
-Choice choose(int64_t m, int64_t n, int64_t stages, bool may_split) {
-  Choice best{64, 1};
-  double least = 1e30;
-  for (const TileCost& c : {kCost64, kCost128, kCost256})
-    for (int s = 1; s == 1 || (may_split && s <= 64 && stages >= 16 * s); s *= 2) {
-      const double us = tile_us(c, m, n, (stages + s - 1) / s, s) + (s - 1) * static_cast<double>(m) * n * 8 / 4e6;
-      if (us < least) {
-        least = us;
-        best = {c.size, s};
-      }
-    }
-  return best;
-}
-
-template <typename T>
-hipError_t store(int tile, const ProductArgs& p, const StoreArgs<T>& e, hipStream_t s) {
-  return tile == 256 ? run_product_store<Cfg256, T>(p, e, s) : tile == 128 ? run_product_store<Cfg128, T>(p, e, s) : run_product_store<Cfg64, T>(p, e, s);
-}
-
 Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt, bool dx, bool dw) {
   Plan p{};
   p.hp = up(hidden, 64);
@@ -489,7 +507,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.terms_x = dx ? terms_of(x_dt) : 0;
   p.terms_w = dw ? terms_of(dw_dt) : 0;
   // Of the workspace: dz and its transpose take up to 1 GiB for a piece, the
-  // weights and their transpose up to 512 MiB each (8192 x 32000 x 512 in bf16 takes
+  // weights and their transpose up to 1 GiB each (8192 x 32000 x 512 in bf16 takes
   // 1.71 ms with a quarter of that for dz, 1.51 with half and 1.29 so; 1021 x
   // 129283 x 2045 with dw in fp32 3.69 with a quarter of that for weights, 3.40 so).
   // Logits that 4 GiB hold stay in fp32 between the statistics and dz, instead of
@@ -501,7 +519,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   const int64_t held = int64_t{1} << (hidden >= 256 ? 30 : 26);
   p.keep = (dx || dw) && vocab_p <= held && r <= held / vocab_p;
   const int64_t terms = std::max(p.terms_x + p.terms_w, 2);
-  const int64_t by_w = (int64_t{1} << 28) / p.hp, by_z = (int64_t{1} << 29) / (terms * r);
+  const int64_t by_w = (int64_t{1} << 29) / p.hp, by_z = (int64_t{1} << 29) / (terms * r);
   p.vb = piece_of(vocab, std::min(std::max(std::min(by_w, by_z) / 256 * 256, int64_t{1024}), int64_t{1} << 20));
   p.pz = (vocab_p / 64 | 1) * 64;
   // with gradients a copy of up to 1 GiB is made once, not once for each product
@@ -624,10 +642,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     logits.n = v;
     const CeStatsArgs e{a.targets, v0, part, zt, z, pl.pz, pl.keep && worth_streaming(z, pl.pz, a.rows, a.vocab)};
     int cols;
-    const int tile = choose(a.rows, v, logits.stages, false).tile;
-    if (tile == 256) MO_TRY(run_stats<Cfg256>(logits, e, cols, s));
-    else if (tile == 128) MO_TRY(run_stats<Cfg128>(logits, e, cols, s));
-    else MO_TRY(run_stats<Cfg64>(logits, e, cols, s));
+    MO_TRY(with(choose(a.rows, v, logits.stages, false).tile, [&](auto c) { return run_stats<decltype(c)>(logits, e, cols, s); }));
     const auto join = cols > 256 ? ce_join_kernel<256> : ce_join_kernel<16>;
     const int per = cols > 256 ? 1 : 16;
     join<<<(a.rows + per - 1) / per, 256, 0, s>>>(part, cols, a.rows, a.vocab, v0 == 0,
@@ -653,8 +668,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     } else {
       logits.b = operand(v0);
       logits.n = v;
-      const int tile = choose(a.rows, v, logits.stages, false).tile;
-      MO_TRY(tile == 256 ? run_grad<Cfg256>(logits, e, s) : tile == 128 ? run_grad<Cfg128>(logits, e, s) : run_grad<Cfg64>(logits, e, s));
+      MO_TRY(with(choose(a.rows, v, logits.stages, false).tile, [&](auto c) { return run_grad<decltype(c)>(logits, e, s); }));
     }
     if (want_dx) {
       // a piece's terms lie side by side along the contraction
@@ -683,7 +697,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       p.splits = 1;
       const int stream_dw = a.dw_dt == F32 ? worth_streaming(static_cast<float*>(a.dw), a.ld_dw, a.vocab, a.hidden)
                                            : worth_streaming(static_cast<__bf16*>(a.dw), a.ld_dw, a.vocab, a.hidden);
-      const int tile_dw = choose(v, a.hidden, p.stages, false).tile;
+      const Tile tile_dw = choose(v, a.hidden, p.stages, false).tile;
       uint8_t* out = static_cast<uint8_t*>(a.dw) + v0 * a.ld_dw * esz_dw;
       if (a.dw_dt == F32) MO_TRY((store<float>(tile_dw, p, {reinterpret_cast<float*>(out), a.ld_dw, 0, a.accumulate, scale, stream_dw}, s)));
       else MO_TRY((store<__bf16>(tile_dw, p, {reinterpret_cast<__bf16*>(out), a.ld_dw, 0, a.accumulate, scale, stream_dw}, s)));

@@ -162,9 +162,9 @@ def test_cross_entropy_workspace_does_not_grow_with_the_vocabulary():
     """Where 4 GiB do not hold the logits, the workspace holds pieces: those of
     16384 x 256000 in fp32 would be 16.8 GB."""
     some, more = _ce_need(16384, 4096, 66000), _ce_need(16384, 4096, 256000)
-    assert more < 1.6 * some and more < 3e9
+    assert more < 2 * some and more < 4e9
     for vocab in (32000, 64000, 65536, 66000, 1024000):
-        assert _ce_need(16384, 4096, vocab) < (1 << 32) + 4e9
+        assert _ce_need(16384, 4096, vocab) < (1 << 32) + 5e9
     assert _ce_need(16384, 4096, 256000, dx=0, dw=0) < 1e9
 
 
