@@ -411,19 +411,22 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
 }
 
 // dx = scale times the sum of the splits' parts (rows of `pitch`, a multiple of
-// 4), 0 in rows that take no part: a workgroup per row.
+// 4), 0 in rows that take no part: a workgroup per row and 1024 columns, as a
+// single long row with 64 parts would keep one CU busy (84 x 4352 with 32 parts
+// 66 us with a workgroup per row, 10 so).
 template <typename T>
 __global__ void __launch_bounds__(256) ce_finish_kernel(const float* part, int splits, int64_t stride, int64_t pitch, int hidden,
                                                         const float* scale, const float* factor, T* dx, int64_t ld) {
   const int64_t t = blockIdx.x;
+  const int c = blockIdx.y * 1024 + threadIdx.x * 4;
+  if (c >= hidden) return;
   const float f = factor[t] == 0.0f ? 0.0f : *scale;
-  for (int c = threadIdx.x * 4; c < hidden; c += 1024) {
-    f32x4v v = {};
-    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4v*>(part + s * stride + t * pitch + c);
+  f32x4v v = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4v*>(part + s * stride + t * pitch + c);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = f == 0.0f ? 0.0f : v[k] * f;
-    store4_out(dx + t * ld + c, v, hidden - c, 0);
-  }
+  for (int k = 0; k < 4; ++k) v[k] = f == 0.0f ? 0.0f : v[k] * f;
+  store4_out(dx + t * ld + c, v, hidden - c, 0);
 }
 
 // ------------------------------------------------------------ tiles
@@ -705,8 +708,9 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   }
   if (want_dx) {
     const int64_t n = static_cast<int64_t>(a.rows) * pl.hp;
-    if (a.x_dt == F32) ce_finish_kernel<float><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, pl.hp, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
-    else ce_finish_kernel<__bf16><<<a.rows, 256, 0, s>>>(dxp, pl.splits, n, pl.hp, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
+    const dim3 g(static_cast<uint32_t>(a.rows), static_cast<uint32_t>((a.hidden + 1023) / 1024));
+    if (a.x_dt == F32) ce_finish_kernel<float><<<g, 256, 0, s>>>(dxp, pl.splits, n, pl.hp, a.hidden, scale, factor, static_cast<float*>(a.dx), a.ld_dx);
+    else ce_finish_kernel<__bf16><<<g, 256, 0, s>>>(dxp, pl.splits, n, pl.hp, a.hidden, scale, factor, static_cast<__bf16*>(a.dx), a.ld_dx);
     MO_TRY(hipGetLastError());
   }
   return hipSuccess;
