@@ -1007,7 +1007,9 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     False for the loss alone; what is not asked for is None.  dx has x's dtype
     and shape, dW the weights' dtype unless ``dw`` [vocab, hidden] gives it;
     ``accumulate`` adds to ``dw``.  Not seen by autograd: pass the gradients on
-    yourself."""
+    yourself.  For the time of the call, gradients take a workspace: copies of
+    the operands, up to 1 GiB of the logits' gradient, and the logits in fp32
+    where 4 GiB hold them (computed twice where not)."""
     if grad not in _GRADS:
         raise ValueError(f"grad must be one of {_GRADS}")
     x2 = _flat2(x)
@@ -1033,12 +1035,11 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
         if want_dw and dw is None:
             dw = torch.empty(vocab, hidden, dtype=weight.dtype, device=dev)
         wgp, _, _, ld_dw = _rows_of(dw, "dw") if want_dw else (None, 0, 0, 0)
-        with _SCRATCH_LOCK:
-            ws = _scratch(need, handle, dev)
-            check(lib().mo_linear_ce(xp, x_dt, ldx, wp, w_dt, ldw, rows, hidden, vocab, tp, gp, loss.data_ptr(),
-                                     dx.data_ptr() if want_dx else None, hidden, wgp, dw_dt, ld_dw, int(accumulate),
-                                     ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-                                     handle))
+        # gigabytes for long calls: of this call alone, not kept for the next one
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        check(lib().mo_linear_ce(xp, x_dt, ldx, wp, w_dt, ldw, rows, hidden, vocab, tp, gp, loss.data_ptr(),
+                                 dx.data_ptr() if want_dx else None, hidden, wgp, dw_dt, ld_dw, int(accumulate),
+                                 ws.data_ptr() if need else None, need, handle))
     return loss, dx if dx is None or x.dim() == 2 else dx.view(x.shape), dw
 
 
