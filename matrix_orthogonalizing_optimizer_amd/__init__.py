@@ -422,9 +422,11 @@ def _rows_of(t: torch.Tensor, what: str) -> Tuple[int, int, int, int]:
     """(pointer, rows, cols, row stride) of a 2-D tensor with unit column stride."""
     if t.dim() != 2:
         raise ValueError(f"{what} must be 2-D, got shape {tuple(t.shape)}")
-    r, c = (int(v) for v in t.shape)
-    ld = int(t.stride(0)) if r > 1 else max(c, 1)
-    if (c > 1 and t.stride(1) != 1) or ld < c:
+    r, c = t.shape
+    ld, step = t.stride()
+    if r < 2:
+        ld = c or 1
+    if (c > 1 and step != 1) or ld < c:
         raise ValueError(f"{what}: rows must be contiguous and must not overlap (strides {t.stride()})")
     return t.data_ptr(), r, c, ld
 
@@ -653,7 +655,7 @@ def mx4_linear_backward(dy: torch.Tensor, x_t: Mx4Matrix, w_t: Mx4Matrix, *,
 
 
 # ---------------------------------------------------------------- 8-bit matrices
-_I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
+_I64x1, _I64x4, _I64x8 = ctypes.c_int64 * 1, ctypes.c_int64 * 4, ctypes.c_int64 * 8
 
 
 class Fp8Matrix:
@@ -757,9 +759,16 @@ def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str 
     if images not in _IMAGES:
         raise ValueError(f"images must be one of {_IMAGES}")
     single = isinstance(x, torch.Tensor)
+    if single and out is None:                   # the common call, with little beside its launch
+        dt, view, dev = _dtype_code(x.dtype, "x"), _rows_of(x, "x"), x.device
+        with _launch_on(dev, stream, (x,)) as handle:
+            made = _fp8_images(view, dt, images, dev, handle, int(square))
+        return tuple(made) if images == "both" else made[0]
     xs = [x] if single else list(x)
     if not xs:
         return []
+    if len(xs) == 1 and out is None:
+        return [fp8_quantize(xs[0], images=images, square=square, stream=stream)]
     outs = None if out is None else ([out] if single else list(out))
     if outs is not None and len(outs) != len(xs):
         raise ValueError(f"out has {len(outs)} entries for {len(xs)} matrices")
@@ -808,18 +817,25 @@ def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str 
 def fp8_dequantize(q: Union[Fp8Matrix, Sequence[Fp8Matrix]], *, dtype: torch.dtype = torch.bfloat16,
                    stream=None):
     """The values that an image, or each of a list, stands for (``mo_fp8_dequantize``)."""
-    single = isinstance(q, Fp8Matrix)
-    qs = [q] if single else list(q)
     dt = _dtype_code(dtype, "dtype")
+    if isinstance(q, Fp8Matrix):
+        dev = q.device
+        with _launch_on(dev, stream, q._keep) as handle:
+            res = torch.empty((q.rows, q.cols), dtype=dtype, device=dev)
+            check(lib().mo_fp8_dequantize(q._struct(), _I64x1(res.data_ptr()), 1, dt, handle))
+        return res
+    qs = list(q)
     if not qs:
         return []
+    if len(qs) == 1:
+        return [fp8_dequantize(qs[0], dtype=dtype, stream=stream)]
     dev = qs[0].device
     with _launch_on(dev, stream, [t for i in qs for t in i._keep]) as handle:
         res = [torch.empty((i.rows, i.cols), dtype=dtype, device=dev) for i in qs]
         flat = [v for i in qs for v in (*i._ptrs, i.rows, i.cols)]         # mo_fp8_image
         ptrs = (ctypes.c_int64 * len(qs))(*[t.data_ptr() for t in res])
         check(lib().mo_fp8_dequantize((ctypes.c_int64 * len(flat))(*flat), ptrs, len(qs), dt, handle))
-    return res[0] if single else res
+    return res
 
 
 def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
@@ -848,12 +864,19 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfl
     return out
 
 
-def _fp8_images(view, dt: int, both: bool, dev: torch.device, handle: int) -> List[Fp8Matrix]:
-    """Images of one matrix, and of its transpose where ``both``, inside a launch context."""
+def _fp8_images(view, dt: int, images: str, dev: torch.device, handle: int, square: int = 0) -> List[Fp8Matrix]:
+    """Images of one matrix, inside a launch context."""
     ptr, r, c, ld = view
-    made = Fp8Matrix._empty(((r, c), (c, r)) if both else ((r, c),), dev)
-    item = _I64x8(ptr, *made[0]._ptrs, *(made[1]._ptrs if both else _NO_IMAGE), r, c, ld)
-    check(lib().mo_fp8_quantize(item, 1, dt, 0, handle))
+    if images == "both":
+        made = Fp8Matrix._empty(((r, c), (c, r)), dev)
+        item = _I64x8(ptr, *made[0]._ptrs, *made[1]._ptrs, r, c, ld)
+    elif images == "rows":
+        made = Fp8Matrix._empty(((r, c),), dev)
+        item = _I64x8(ptr, *made[0]._ptrs, 0, 0, r, c, ld)
+    else:
+        made = Fp8Matrix._empty(((c, r),), dev)
+        item = _I64x8(ptr, 0, 0, *made[0]._ptrs, r, c, ld)
+    check(lib().mo_fp8_quantize(item, 1, dt, square, handle))
     return made
 
 
@@ -875,7 +898,7 @@ def fp8_linear(x: torch.Tensor, w: Fp8Matrix, *, out_dtype: torch.dtype = torch.
         raise ValueError(f"x has {view[2]} features, the weights {w.cols}")
     x_dt, out_dt, dev = _dtype_code(x.dtype, "x"), _dtype_code(out_dtype, "out_dtype"), x.device
     with _launch_on(dev, stream, (x2, *w._keep)) as handle:     # one context for both launches
-        images = _fp8_images(view, x_dt, save, dev, handle)
+        images = _fp8_images(view, x_dt, "both" if save else "rows", dev, handle)
         y = _fp8_product(images[0], w, out_dtype, out_dt, dev, handle)
     y = y if x.dim() == 2 else y.view(*x.shape[:-1], w.rows)
     return (y, images[1]) if save else y
@@ -904,7 +927,7 @@ def fp8_linear_backward(dy: torch.Tensor, x_t: Fp8Matrix, w_t: Fp8Matrix, *,
     dw_dt = MO_F32 if dw is None else _dtype_code(dw.dtype, "dw")
     dw_view = None if dw is None else _rows_of(dw, "dw")
     with _launch_on(dev, stream, (d2, *x_t._keep, *w_t._keep, dw)) as handle:
-        dq, dq_t = _fp8_images(view, dy_dt, True, dev, handle)
+        dq, dq_t = _fp8_images(view, dy_dt, "both", dev, handle)
         dx = _fp8_product(dq, w_t, dx_dtype, dx_dt, dev, handle)
         if dw is None:
             dw = _fp8_product(dq_t, x_t, torch.float32, dw_dt, dev, handle)
