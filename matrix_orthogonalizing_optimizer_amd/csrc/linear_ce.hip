@@ -419,6 +419,139 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
   }
 }
 
+// ------------------------------------------------------------ dx of few rows
+// Parts of dz W where there are few rows: the weights' bytes are all there is to
+// it, so they are read as they lie, along their rows, instead of as a transposed
+// copy.  A lane loads 4 columns of 8 rows of W, and the matrix instruction takes
+// those 8 as its contraction: the lanes' first columns are one operand, their
+// second ones another.  A workgroup takes 128 columns and a share of the
+// vocabulary, whose rows its waves take in turn, 64 at a time; the waves' sums
+// meet in LDS in a fixed order.
+//
+// HBM bound: 4 x 128000 x 4096 178 us, 5.9 TB/s, 64 rows 286, where dz is half as
+// much to load as W (the transposed copy alone takes 410, its product 230; all of
+// the call 1104 to 696 and 1174 to 825 us).  128 rows in four blocks of 32 and two
+// columns a lane took 598, no less than the copy and its product.
+struct CeDxRowsArgs {
+  const uint16_t* dz;           // [rows]: TERMS times vp, rows pitch_x apart
+  const uint8_t* w;             // bf16, rows pitch_w bytes apart
+  float* part;                  // [splits][rows][hp]
+  int64_t pitch_x, pitch_w;
+  int rows, cols, vp, hp;       // cols: the piece's rows of W
+  int per;                      // rows of W to a split, a multiple of 256
+  int accumulate;
+};
+
+template <int TB, int TERMS>
+__global__ void __launch_bounds__(256, 2) ce_dx_rows_kernel(const CeDxRowsArgs e) {
+  constexpr int NC = 4, kSums = TB * NC;
+  constexpr int kSets = TERMS == 1 ? 4 : 2;                 // 16 rows of W each, on their way
+  typedef uint32_t wvec __attribute__((ext_vector_type(2)));
+  __shared__ f32x4v meet[2][kSums * 4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r32 = lane & 31, half = lane >> 5;
+  const int c0 = blockIdx.x * (32 * NC), c = min(c0 + r32 * NC, e.hp - NC);
+  const int s0 = blockIdx.y * e.per, s1 = min(s0 + e.per, e.vp);
+  f32x16v acc[TB][NC];
+#pragma unroll
+  for (int t = 0; t < TB; ++t)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) acc[t][j] = f32x16v{};
+  const uint8_t* wcol = e.w + static_cast<int64_t>(c) * 2;
+  const uint16_t* zrow[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) zrow[t] = e.dz + static_cast<int64_t>(min(32 * t + r32, e.rows - 1)) * e.pitch_x + 8 * half;
+  wvec w[kSets][8];
+  u32x4v z[kSets][TB][TERMS];
+  // rows past the piece's last repeat it: dz is 0 there
+  auto load = [&](int set, int v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[set][i] = *reinterpret_cast<const wvec*>(wcol + static_cast<int64_t>(min(v + 8 * half + i, e.cols - 1)) * e.pitch_w);
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k) z[set][t][k] = *reinterpret_cast<const u32x4v*>(zrow[t] + static_cast<int64_t>(k) * e.vp + v);
+  };
+  auto add = [&](int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      u32x4v b;                                             // column j of the lane's, 8 rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __builtin_amdgcn_perm(w[set][2 * i + 1][j / 2], w[set][2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[t][j] = mma_bf16(b, z[set][t][k], acc[t][j]);
+    }
+  };
+  // the wave's blocks of 64 rows, kSets times 16 of them in flight
+  int v = s0 + wave * 64;
+  if (v < s1) {
+#pragma unroll
+    for (int k = 0; k < kSets; ++k) load(k, v + 16 * k);
+    for (;;) {
+      const int next = v + 256;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        add(k % kSets);
+        const int ahead = k + kSets < 4 ? v + 16 * (k + kSets) : next + 16 * (k + kSets - 4);
+        if (k + kSets < 4 || next < s1) load(k % kSets, ahead);
+      }
+      if (next >= s1) break;
+      v = next;
+    }
+  }
+  // waves 2 and 3 to 0 and 1, then 1 to 0
+#pragma unroll
+  for (int step = 2; step >= 1; step >>= 1) {
+    if (wave >= step && wave < 2 * step) {
+#pragma unroll
+      for (int q = 0; q < kSums; ++q)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16v& a = acc[q / NC][q % NC];
+          meet[wave - step][q * 4 + g][lane] = f32x4v{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
+        }
+    }
+    __syncthreads();
+    if (wave < step) {
+#pragma unroll
+      for (int q = 0; q < kSums; ++q)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4v a = meet[wave][q * 4 + g][lane];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[q / NC][q % NC][4 * g + k] += a[k];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave) return;
+  // lane r32 has row 32 t + r32; element r of operand j is column NC (8 (r / 4) + 4 half + r % 4) + j
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    const int row = 32 * t + r32;
+    if (row >= e.rows) continue;
+    float* to = e.part + (static_cast<int64_t>(blockIdx.y) * e.rows + row) * e.hp;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int h = c0 + NC * (8 * (r / 4) + 4 * half + r % 4);
+      if (h >= e.hp) continue;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) to[h + j] = e.accumulate ? to[h + j] + acc[t][j][r] : acc[t][j][r];
+    }
+  }
+}
+
+template <int TB>
+hipError_t run_dx_rows(const CeDxRowsArgs& e, int terms, int splits, hipStream_t s) {
+  const dim3 g(static_cast<uint32_t>((e.hp + 127) / 128), static_cast<uint32_t>(splits));
+  if (terms == 1) ce_dx_rows_kernel<TB, 1><<<g, 256, 0, s>>>(e);
+  else ce_dx_rows_kernel<TB, 3><<<g, 256, 0, s>>>(e);
+  return hipGetLastError();
+}
+
 // dx = scale times the sum of the splits' parts (rows of `pitch`, a multiple of
 // 4), 0 in rows that take no part: a workgroup per row and 1024 columns, as a
 // single long row with 64 parts would keep one CU busy (84 x 4352 with 32 parts
@@ -489,6 +622,7 @@ hipError_t store(Tile tile, const ProductArgs& p, const StoreArgs<T>& e, hipStre
 }
 
 // ------------------------------------------------------------ the plan
+constexpr int64_t kDxRows = 64;
 // Pieces of the vocabulary, and the places of everything in the workspace.
 struct Plan {
   int64_t hp, tp;              // hidden size and rows, padded to whole pairs of stages
@@ -496,6 +630,7 @@ struct Plan {
   int64_t vf, vb;              // columns of a forward and of a backward piece
   int splits;                  // of the product for dx
   Tile tile_dx;
+  bool dx_rows;                // which reads the weights along their rows
   int terms_x, terms_w;
   bool keep;                   // the logits stay
   bool keep_w;                 // so does the bf16 copy of the weights, where they are copied
@@ -537,9 +672,16 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   // with gradients a copy of up to 1 GiB is made once, not once for each product
   p.keep_w = (dx || dw) && vocab <= (int64_t{1} << 29) / p.ph;
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));
-  const Choice of_dx = choose(rows, hidden, p.vb / 32 * p.terms_x, true);
-  p.splits = of_dx.splits;
-  p.tile_dx = of_dx.tile;
+  p.dx_rows = dx && rows <= kDxRows;
+  if (p.dx_rows) {
+    // some workgroups for every CU, but 1024 rows of weights at least to each
+    const int64_t chunks = (p.hp + 127) / 128;
+    p.splits = static_cast<int>(std::max<int64_t>(1, std::min({int64_t{64}, (1024 + chunks - 1) / chunks, p.vb / 1024})));
+  } else {
+    const Choice of_dx = choose(rows, hidden, p.vb / 32 * p.terms_x, true);
+    p.splits = of_dx.splits;
+    p.tile_dx = of_dx.tile;
+  }
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -555,7 +697,7 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   p.x = take(t * p.ph * 2);
   p.w = take(static_cast<size_t>(p.keep_w ? vocab : p.vb) * p.ph * 2);
   if (dw) p.x_t = take(static_cast<size_t>(hidden) * p.pt * 2);
-  if (dx) p.w_t = take(static_cast<size_t>(hidden) * apart(p.vb) * 2);
+  if (dx && !p.dx_rows) p.w_t = take(static_cast<size_t>(hidden) * apart(p.vb) * 2);
   if (p.keep) p.z = take(t * p.pz * 4);
   if (dx) p.dz = take(t * apart(p.vb * p.terms_x) * 2);
   if (dw) p.dz_t = take(static_cast<size_t>(p.vb) * apart(p.tp * p.terms_w) * 2);
@@ -613,7 +755,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   uint16_t* xb = reinterpret_cast<uint16_t*>(base + pl.x);
   uint16_t* wb = reinterpret_cast<uint16_t*>(base + pl.w);
   uint16_t* x_t = want_dw ? reinterpret_cast<uint16_t*>(base + pl.x_t) : nullptr;
-  uint16_t* w_t = want_dx ? reinterpret_cast<uint16_t*>(base + pl.w_t) : nullptr;
+  uint16_t* w_t = want_dx && !pl.dx_rows ? reinterpret_cast<uint16_t*>(base + pl.w_t) : nullptr;
   uint16_t* dz = want_dx ? reinterpret_cast<uint16_t*>(base + pl.dz) : nullptr;
   uint16_t* dz_t = want_dw ? reinterpret_cast<uint16_t*>(base + pl.dz_t) : nullptr;
   float* dxp = want_dx ? reinterpret_cast<float*>(base + pl.dxp) : nullptr;
@@ -647,7 +789,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   const bool once = pl.keep && vf >= a.vocab && pl.vb >= a.vocab;      // one piece of weights, too: its transpose comes with it
   for (int64_t v0 = 0; v0 < a.vocab; v0 += vf) {
     const int v = static_cast<int>(std::min<int64_t>(vf, a.vocab - v0));
-    if (!plain_w || (once && want_dx))
+    if (!plain_w || (once && w_t))
       MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb + (pl.keep_w ? v0 * pl.ph : 0), pl.ph, once ? w_t : nullptr,
                   apart(up(v, 64)), nullptr, s));
     logits.b = operand(v0);
@@ -668,7 +810,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     const int v = static_cast<int>(std::min<int64_t>(pl.vb, a.vocab - v0));
     const int64_t vp = up(v, 64), pv = apart(vp);
     const bool copied = !plain_w && pl.keep_w;                          // already there
-    const bool need_w = !pl.keep && !plain_w && !copied, need_w_t = want_dx && !once;
+    const bool need_w = (!pl.keep || pl.dx_rows) && !plain_w && !copied, need_w_t = w_t && !once;
     if (need_w || need_w_t)
       MO_TRY(copied ? pack(BF16, operand(v0), pl.ph, v, a.hidden, nullptr, 0, w_t, pv, nullptr, s)
                     : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.ph, need_w_t ? w_t : nullptr, pv, nullptr, s));
@@ -683,7 +825,11 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
       logits.n = v;
       MO_TRY(with(choose(a.rows, v, logits.stages, false).tile, [&](auto c) { return run_grad<decltype(c)>(logits, e, s); }));
     }
-    if (want_dx) {
+    if (want_dx && pl.dx_rows) {
+      const CeDxRowsArgs r{dz, operand(v0), dxp, apart(vp * pl.terms_x), static_cast<int64_t>(logits.pitch_b), a.rows, v, static_cast<int>(vp),
+                           static_cast<int>(pl.hp), static_cast<int>(up((vp + pl.splits - 1) / pl.splits, 256)), v0 > 0};
+      MO_TRY(a.rows <= 32 ? run_dx_rows<1>(r, pl.terms_x, pl.splits, s) : run_dx_rows<2>(r, pl.terms_x, pl.splits, s));
+    } else if (want_dx) {
       // a piece's terms lie side by side along the contraction
       ProductArgs p{};
       p.a = reinterpret_cast<const uint8_t*>(dz);

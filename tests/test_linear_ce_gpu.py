@@ -138,6 +138,23 @@ def test_pieces(t, h, v, wd, dwd):
     _check(x, w, y, g, l2, None, dw)
 
 
+@pytest.mark.parametrize("t,h,v", [(1, 64, 70000), (31, 200, 5003), (32, 129, 4097), (33, 1025, 9000), (64, 2048, 20011),
+                                   (47, 68, 1027), (5, 1, 2049), (64, 130, 1024)])
+@pytest.mark.parametrize("xd,wd", [(BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_dx_of_few_rows(t, h, v, xd, wd):
+    """Weights read along their rows: odd sizes, several shares of the vocabulary,
+    rows that end inside a block, and skipped rows that hold NaN."""
+    x, w, y, g = _inputs(t, h, v, 3 * t + h, xd, wd)
+    y[0] = v - 1
+    loss, dx, dw = mo.linear_cross_entropy(x, w, y, grad_loss=g, grad="x")
+    assert dw is None
+    _check(x, w, y, g, loss, dx, None)
+    bad = x.clone()
+    bad[y < 0] = float("nan")
+    l2, dx2, _ = mo.linear_cross_entropy(bad, w, y, grad_loss=g)
+    assert torch.equal(loss, l2) and torch.equal(dx, dx2) and not bool(dx[y < 0].any())
+
+
 def test_rows_that_take_no_part():
     """Skipped rows and rows with g = 0 may hold anything; all skipped; no rows."""
     x, w, y, g = _inputs(90, 100, 400, 7, skip=0.3)
