@@ -170,7 +170,9 @@ __device__ __forceinline__ void split_range(const ProductArgs& p, int s, int& k0
 //   * a row of a stage is 4 chunks of 16 bytes, stored at chunk ^ ((row / 4) &
 //     3): the 16 rows that a 16-byte read serves at a time then touch each of
 //     the 64 banks once;
-//   * scale bytes come for 16 blocks (32 stages) of a row at a time;
+//   * scale bytes come for 16 blocks (32 stages) of a row at a time, and are read
+//     a block ahead, behind its first product (as the last reads of a block, which
+//     every wave then waits for: 8192 x 28672 x 8192 1456 instead of 1425 us);
 //   * a line of 128 bytes holds two stages of a row.  Stages are requested in
 //     pairs, both halves of a line one after the other, so that a line is fetched
 //     once: a stage of 512 rows at a time fills the first-level cache twice over
@@ -345,7 +347,7 @@ __device__ __forceinline__ void ring_sums(const ProductArgs& p, const TilePlace&
           if constexpr (cur == 0) request_a(l, last, at);
           else request_b(l, at_b - kStageB, at_b);
         });
-        if constexpr (cur == 1 && P == n - 1) read_scales(block0 + t / 2 + 1);
+        if constexpr (cur == 0 && P == 0) read_scales(block0 + t / 2 + 1);
       };
       if constexpr (Op::kDecoded) {
         float fa[FM], fb[FN];
