@@ -767,6 +767,8 @@ def fp8_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], *, images: str 
     xs = [x] if single else list(x)
     if not xs:
         return []
+    if not all(isinstance(t, torch.Tensor) for t in xs):
+        raise TypeError("x must be a tensor or a list of tensors")
     if len(xs) == 1 and out is None:
         return [fp8_quantize(xs[0], images=images, square=square, stream=stream)]
     outs = None if out is None else ([out] if single else list(out))
@@ -827,6 +829,8 @@ def fp8_dequantize(q: Union[Fp8Matrix, Sequence[Fp8Matrix]], *, dtype: torch.dty
     qs = list(q)
     if not qs:
         return []
+    if not all(isinstance(i, Fp8Matrix) for i in qs):
+        raise TypeError("q must be an Fp8Matrix or a list of them")
     if len(qs) == 1:
         return [fp8_dequantize(qs[0], dtype=dtype, stream=stream)]
     dev = qs[0].device
@@ -892,6 +896,8 @@ def fp8_linear(x: torch.Tensor, w: Fp8Matrix, *, out_dtype: torch.dtype = torch.
     bf16) quantised on the way, a scale per 128 of a row.  ``save=True`` also
     returns the image of x^T that :func:`fp8_linear_backward` takes.  x may
     have no tokens.  Not seen by autograd."""
+    if not isinstance(w, Fp8Matrix):
+        raise TypeError("w must be an Fp8Matrix")
     x2 = _flat2(x)
     view = _rows_of(x2, "x")
     if view[2] != w.cols:
@@ -913,6 +919,8 @@ def fp8_linear_backward(dy: torch.Tensor, x_t: Fp8Matrix, w_t: Fp8Matrix, *,
     rounding of x and W passes gradients straight through.  dW is fp32 [N, K]
     unless ``dw`` gives it; ``accumulate`` adds to ``dw``.  Without tokens dW
     is zeros (or stays as it was)."""
+    if not isinstance(x_t, Fp8Matrix) or not isinstance(w_t, Fp8Matrix):
+        raise TypeError("x_t and w_t must be Fp8Matrix")
     d2 = _flat2(dy)
     view = _rows_of(d2, "dy")
     if view[1] != x_t.cols or view[2] != w_t.cols:

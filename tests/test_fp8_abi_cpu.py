@@ -200,6 +200,14 @@ def test_balance_workspace():
 
 
 # ------------------------------------------------------------- the Python front
+@pytest.mark.parametrize("bad", [[[torch.zeros(2, 2)]], ["x"], [None], [torch.zeros(2, 2), "x"], [3]])
+def test_front_refuses_lists_of_other_things(bad):
+    with pytest.raises(TypeError, match="list"):
+        mo.fp8_quantize(bad)
+    with pytest.raises(TypeError, match="list"):
+        mo.fp8_dequantize(bad)
+
+
 def test_front_refuses_cpu_tensors_and_shapes():
     x = torch.zeros(4, 64)
     with pytest.raises(ValueError, match="GPU"):
@@ -234,6 +242,10 @@ def test_front_checks_images():
         mo.fp8_matmul(q, mo.Mx4Matrix.empty(3, 40, "cpu"))
     with pytest.raises(ValueError, match="accumulate"):
         mo.fp8_matmul(q, q, accumulate=True)
+    with pytest.raises(TypeError):
+        mo.fp8_linear(torch.zeros(2, 40), codes)
+    with pytest.raises(TypeError):
+        mo.fp8_linear_backward(torch.zeros(2, 40), q, codes)
     with pytest.raises(ValueError, match="features"):
         mo.fp8_linear(torch.zeros(2, 41), q)
     with pytest.raises(ValueError, match="want"):
