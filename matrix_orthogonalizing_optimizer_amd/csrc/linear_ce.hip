@@ -46,32 +46,41 @@ int64_t apart(int64_t elements) { return ((elements + 127) / 128 | 1) * 128; }
 // ------------------------------------------------------------ rows and packing
 // Per row: its factor in dz, relative to the largest |g| (so that equal g do
 // not add a rounding of their own to dz's): 0 for a row that takes no part, NaN
-// for a target that is no column.  scale[0] is that largest |g|, or 1.
-__global__ void __launch_bounds__(1024) ce_rows_kernel(const int64_t* targets, const float* g, int rows, int vocab, float* factor, float* scale) {
-  __shared__ float most[16];
+// for a target that is no column.  scale[0] is that largest |g|, or 1.  One
+// workgroup, beside those that pack x.
+struct CeRows {
+  const int64_t* targets;       // null: nothing to do
+  const float* g;               // or null: 1
+  float *factor, *scale;
+  int rows, vocab;
+};
+__device__ __forceinline__ void ce_rows(const CeRows& a) {
+  __shared__ float most[4];
   float m = 0.0f;
-  if (g)
+  if (a.g)
 #pragma unroll 8
-    for (int t = threadIdx.x; t < rows; t += 1024) m = targets[t] >= 0 ? fmaxf(m, fabsf(g[t])) : m;       // NaN is left out
+    for (int t = threadIdx.x; t < a.rows; t += 256) {
+      const int64_t y = a.targets[t];
+      const float r = fmaxf(m, fabsf(a.g[t]));                // NaN is left out
+      m = y >= 0 ? r : m;
+    }
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
   __syncthreads();
-  m = most[0];
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, most[i]);
+  m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
   const float s = m > 0.0f && m < INFINITY ? m : 1.0f;
-  if (threadIdx.x == 0) *scale = s;
+  if (threadIdx.x == 0) *a.scale = s;
 #pragma unroll 8
-  for (int t = threadIdx.x; t < rows; t += 1024) {
-    const int64_t y = targets[t];
-    const float r = g ? g[t] : 1.0f;
-    factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= vocab ? NAN : r / s;
+  for (int t = threadIdx.x; t < a.rows; t += 256) {
+    const int64_t y = a.targets[t];
+    const float r = a.g ? a.g[t] : 1.0f;
+    a.factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= a.vocab ? NAN : r / s;
   }
 }
 
 // bf16 copies of a [rows, cols] matrix: dst [rows][pitch] (columns past `cols`,
 // up to a multiple of 64, zero) and its transpose dst_t [cols][pitch_t] (rows
-// past `rows` likewise, and those whose factor is 0, so that whatever they hold
-// takes no part).  64 rows x 128 columns per workgroup, through LDS; HBM bound:
+// past `rows` likewise, and of x those that take no part, whatever they hold).  64 rows x 128 columns per workgroup, through LDS; HBM bound:
 // 129283 x 2045 fp32 to both 425 us, 5.0 TB/s.
 constexpr int kPackRows = 64, kPackCols = 128;
 // Eight rows of a column.
@@ -85,7 +94,11 @@ __device__ __forceinline__ u32x4v column8(const uint32_t (&tile)[kPackRows][kPac
 
 template <typename T>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
-                                                      uint16_t* dst_t, int64_t pitch_t, const float* factor) {
+                                                      uint16_t* dst_t, int64_t pitch_t, const CeRows job) {
+  if (blockIdx.x * int64_t{kPackRows} >= rows) {             // the one behind the last tile
+    if (blockIdx.y == 0) ce_rows(job);
+    return;
+  }
   const int64_t cols_p = (static_cast<int64_t>(cols) + 63) / 64 * 64, rows_p = (static_cast<int64_t>(rows) + 63) / 64 * 64;
   __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];       // pairs of columns; odd rows of dwords: columns spread over the banks
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPackRows, c0 = static_cast<int64_t>(blockIdx.y) * kPackCols;
@@ -103,7 +116,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, 
     const u32x4v v = {pack_bf16x2(o[i].get(0), o[i].get(1)), pack_bf16x2(o[i].get(2), o[i].get(3)),
                       pack_bf16x2(o[i].get(4), o[i].get(5)), pack_bf16x2(o[i].get(6), o[i].get(7))};
     if (dst && r < rows && c0 + cl < cols_p) *reinterpret_cast<u32x4v*>(dst + r * pitch + c0 + cl) = v;
-    const bool out = factor && r < rows && factor[r] == 0.0f;
+    const bool out = job.targets && r < rows && (job.targets[r] < 0 || (job.g && job.g[r] == 0.0f));
 #pragma unroll
     for (int k = 0; k < 4; ++k) tile[rl + 16 * i][cl / 2 + k] = out ? 0u : v[k];
   }
@@ -118,11 +131,12 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, 
 }
 
 hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch, uint16_t* dst_t, int64_t pitch_t,
-                const float* factor, hipStream_t s) {
+                const CeRows& job, hipStream_t s) {
   // rows along the grid's long axis: up to 2^22 columns are 2^15 workgroups
-  const dim3 g(static_cast<uint32_t>((static_cast<int64_t>(rows) + kPackRows - 1) / kPackRows), static_cast<uint32_t>((cols + kPackCols - 1) / kPackCols));
-  if (dt == F32) ce_pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
-  else ce_pack_kernel<__bf16><<<g, 256, 0, s>>>(static_cast<const __bf16*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, factor);
+  const int64_t tiles = (static_cast<int64_t>(rows) + kPackRows - 1) / kPackRows + (job.targets ? 1 : 0);
+  const dim3 g(static_cast<uint32_t>(tiles), static_cast<uint32_t>((cols + kPackCols - 1) / kPackCols));
+  if (dt == F32) ce_pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, job);
+  else ce_pack_kernel<__bf16><<<g, 256, 0, s>>>(static_cast<const __bf16*>(src), ld, rows, cols, dst, pitch, dst_t, pitch_t, job);
   return hipGetLastError();
 }
 
@@ -622,7 +636,8 @@ hipError_t store(Tile tile, const ProductArgs& p, const StoreArgs<T>& e, hipStre
 }
 
 // ------------------------------------------------------------ the plan
-constexpr int64_t kDxRows = 64;
+constexpr int64_t kDxRows = 64;                             // at most, for ce_dx_rows_kernel
+
 // Pieces of the vocabulary, and the places of everything in the workspace.
 struct Plan {
   int64_t hp, tp;              // hidden size and rows, padded to whole pairs of stages
@@ -643,7 +658,6 @@ int64_t piece_of(int64_t vocab, int64_t most) {
   const int64_t n = (vocab + most - 1) / most;
   return std::min(up((vocab + n - 1) / n, 256), up(vocab, 256));
 }
-
 
 Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt, bool dx, bool dw) {
   Plan p{};
@@ -768,9 +782,9 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   const bool plain_x = plain(a.x, a.x_dt, a.ldx), plain_w = plain(a.w, a.w_dt, a.ldw);
   const int esz_w = a.w_dt == F32 ? 4 : 2, esz_dw = a.dw_dt == F32 ? 4 : 2;
 
-  if (grad) ce_rows_kernel<<<1, 1024, 0, s>>>(a.targets, a.grad_loss, a.rows, a.vocab, factor, scale);
-  MO_TRY(hipGetLastError());
-  if (!plain_x || want_dw) MO_TRY(pack(a.x_dt, a.x, a.ldx, a.rows, a.hidden, plain_x ? nullptr : xb, pl.ph, x_t, pl.pt, factor, s));
+  const CeRows job{grad ? a.targets : nullptr, a.grad_loss, factor, scale, a.rows, a.vocab};
+  if (!plain_x || want_dw) MO_TRY(pack(a.x_dt, a.x, a.ldx, a.rows, a.hidden, plain_x ? nullptr : xb, pl.ph, x_t, pl.pt, job, s));
+  else if (grad) MO_TRY(pack(a.x_dt, a.x, a.ldx, 0, 1, nullptr, 0, nullptr, 0, job, s));
 
   ProductArgs logits{};
   logits.a = static_cast<const uint8_t*>(plain_x ? a.x : xb);
@@ -791,7 +805,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     const int v = static_cast<int>(std::min<int64_t>(vf, a.vocab - v0));
     if (!plain_w || (once && w_t))
       MO_TRY(pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, plain_w ? nullptr : wb + (pl.keep_w ? v0 * pl.ph : 0), pl.ph, once ? w_t : nullptr,
-                  apart(up(v, 64)), nullptr, s));
+                  apart(up(v, 64)), {}, s));
     logits.b = operand(v0);
     logits.n = v;
     const CeStatsArgs e{a.targets, v0, part, zt, z, pl.pz, pl.keep && worth_streaming(z, pl.pz, a.rows, a.vocab)};
@@ -812,8 +826,8 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     const bool copied = !plain_w && pl.keep_w;                          // already there
     const bool need_w = (!pl.keep || pl.dx_rows) && !plain_w && !copied, need_w_t = w_t && !once;
     if (need_w || need_w_t)
-      MO_TRY(copied ? pack(BF16, operand(v0), pl.ph, v, a.hidden, nullptr, 0, w_t, pv, nullptr, s)
-                    : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.ph, need_w_t ? w_t : nullptr, pv, nullptr, s));
+      MO_TRY(copied ? pack(BF16, operand(v0), pl.ph, v, a.hidden, nullptr, 0, w_t, pv, {}, s)
+                    : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.ph, need_w_t ? w_t : nullptr, pv, {}, s));
     const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp),
                        apart(vp * pl.terms_x), apart(pl.tp * pl.terms_w)};
     if (pl.keep) {
