@@ -44,38 +44,37 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int64_t apart(int64_t elements) { return ((elements + 127) / 128 | 1) * 128; }
 
 // ------------------------------------------------------------ rows and packing
-// Per row: its factor in dz, relative to the largest |g| (so that equal g do
-// not add a rounding of their own to dz's): 0 for a row that takes no part, NaN
-// for a target that is no column.  scale[0] is that largest |g|, or 1.  One
-// workgroup, beside those that pack x.
+// Rows' weights in dz are relative to the largest |g| of those that take part (so
+// that equal g do not add a rounding of their own to dz's): scale[0], or 1.  One
+// workgroup finds it beside those that pack x.
 struct CeRows {
   const int64_t* targets;       // null: nothing to do
   const float* g;               // or null: 1
-  float *factor, *scale;
-  int rows, vocab;
+  float* scale;
+  int rows;
 };
-__device__ __forceinline__ void ce_rows(const CeRows& a) {
+__device__ __forceinline__ void ce_scale(const CeRows& a) {
+  constexpr int kAtOnce = 8;                                  // rows of a thread whose loads are in flight
   __shared__ float most[4];
   float m = 0.0f;
   if (a.g)
-#pragma unroll 8
-    for (int t = threadIdx.x; t < a.rows; t += 256) {
-      const int64_t y = a.targets[t];
-      const float r = fmaxf(m, fabsf(a.g[t]));                // NaN is left out
-      m = y >= 0 ? r : m;
+    for (int t0 = threadIdx.x; t0 < a.rows; t0 += 256 * kAtOnce) {
+      int64_t y[kAtOnce];
+      float r[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int t = min(t0 + 256 * i, a.rows - 1);          // some twice
+        y[i] = a.targets[t];
+        r[i] = a.g[t];
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) m = y[i] >= 0 ? fmaxf(m, fabsf(r[i])) : m;      // NaN is left out
     }
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
   __syncthreads();
   m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-  const float s = m > 0.0f && m < INFINITY ? m : 1.0f;
-  if (threadIdx.x == 0) *a.scale = s;
-#pragma unroll 8
-  for (int t = threadIdx.x; t < a.rows; t += 256) {
-    const int64_t y = a.targets[t];
-    const float r = a.g ? a.g[t] : 1.0f;
-    a.factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= a.vocab ? NAN : r / s;
-  }
+  if (threadIdx.x == 0) *a.scale = m > 0.0f && m < INFINITY ? m : 1.0f;
 }
 
 // bf16 copies of a [rows, cols] matrix: dst [rows][pitch] (columns past `cols`,
@@ -95,13 +94,14 @@ __device__ __forceinline__ u32x4v column8(const uint32_t (&tile)[kPackRows][kPac
 template <typename T>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t ld, int rows, int cols, uint16_t* dst, int64_t pitch,
                                                       uint16_t* dst_t, int64_t pitch_t, const CeRows job) {
-  if (blockIdx.x * int64_t{kPackRows} >= rows) {             // the one behind the last tile
-    if (blockIdx.y == 0) ce_rows(job);
+  const int64_t tile_r = static_cast<int64_t>(blockIdx.x) - (job.targets ? 1 : 0);
+  if (tile_r < 0) {                                          // the first one, as it takes longest
+    if (blockIdx.y == 0) ce_scale(job);
     return;
   }
   const int64_t cols_p = (static_cast<int64_t>(cols) + 63) / 64 * 64, rows_p = (static_cast<int64_t>(rows) + 63) / 64 * 64;
   __shared__ uint32_t tile[kPackRows][kPackCols / 2 + 1];       // pairs of columns; odd rows of dwords: columns spread over the banks
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPackRows, c0 = static_cast<int64_t>(blockIdx.y) * kPackCols;
+  const int64_t r0 = tile_r * kPackRows, c0 = static_cast<int64_t>(blockIdx.y) * kPackCols;
   const int cl = (threadIdx.x & 15) * 8, rl = threadIdx.x >> 4;
   const int left = static_cast<int>(min(int64_t{8}, cols - c0 - cl));
   Oct<T> o[4];
@@ -226,12 +226,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
 }
 
 // Joins a piece's statistics with those of the pieces before it, kLanes
-// threads per row; after the last piece the row's {m, 1 / sum} and its loss.
+// threads per row; after the last piece the row's {m, 1 / sum}, its loss and its
+// weight in dz: 0 where it takes no part, NaN for a target that is no column.
 // Latency bound: 3 rows of 500 tiles take 3.2 us with 256 threads to a row and 5.7
 // with 16, 1021 of 506 4.8 and 6.8, 8192 of 125 10.8 and 4.9.
 template <int kLanes>
 __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int cols, int rows, int vocab, int first, int last,
-                                                      const int64_t* targets, const float* target_logit, float2* stat, float* loss) {
+                                                      const int64_t* targets, const float* target_logit, float2* stat, float* loss,
+                                                      const float* g, const float* scale, float* factor) {
   __shared__ float2 waves[4];
   const int lane = threadIdx.x % kLanes;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
@@ -275,6 +277,10 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int co
   const bool none = m == -INFINITY;
   stat[t] = make_float2(m, none ? NAN : 1.0f / s);
   const int64_t y = targets[t];
+  if (factor) {
+    const float r = g ? g[t] : 1.0f;
+    factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= vocab ? NAN : r / *scale;
+  }
   loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + __builtin_fmaf(-target_logit[t], kLog2e, m) * kLn2;
 }
 
@@ -782,7 +788,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
   const bool plain_x = plain(a.x, a.x_dt, a.ldx), plain_w = plain(a.w, a.w_dt, a.ldw);
   const int esz_w = a.w_dt == F32 ? 4 : 2, esz_dw = a.dw_dt == F32 ? 4 : 2;
 
-  const CeRows job{grad ? a.targets : nullptr, a.grad_loss, factor, scale, a.rows, a.vocab};
+  const CeRows job{grad ? a.targets : nullptr, a.grad_loss, scale, a.rows};
   if (!plain_x || want_dw) MO_TRY(pack(a.x_dt, a.x, a.ldx, a.rows, a.hidden, plain_x ? nullptr : xb, pl.ph, x_t, pl.pt, job, s));
   else if (grad) MO_TRY(pack(a.x_dt, a.x, a.ldx, 0, 1, nullptr, 0, nullptr, 0, job, s));
 
@@ -815,7 +821,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     const auto join = wide ? ce_join_kernel<256> : ce_join_kernel<16>;
     const int per = wide ? 1 : 16;
     join<<<(a.rows + per - 1) / per, 256, 0, s>>>(part, cols, a.rows, a.vocab, v0 == 0,
-                                                    v0 + v >= a.vocab, a.targets, zt, stat, a.loss);
+                                                    v0 + v >= a.vocab, a.targets, zt, stat, a.loss, a.grad_loss, scale, grad ? factor : nullptr);
     MO_TRY(hipGetLastError());
   }
   if (!grad) return hipSuccess;
