@@ -38,9 +38,9 @@ __device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // Rows of the workspace's matrices lie an odd number of 256 bytes apart, so that
-// the rows of a tile spread over the memory's channels: 4096 x 4096 x 4096 takes
-// 139 us with rows 16384 bytes apart and 124 with 16640, 1024 x 2048 x 31744 in 8
-// splits 115 with 63488 and 172 with 65024 and shares of 8192 bytes.
+// the rows of a tile spread over the memory's channels: 1024 x 2048 x 31744 in 8
+// splits takes 118 us with rows 63744 bytes apart, 134 with 65024.  (Products whose
+// contraction is not split take the same with either.)
 int64_t apart(int64_t elements) { return ((elements + 127) / 128 | 1) * 128; }
 
 // ------------------------------------------------------------ rows and packing
@@ -145,8 +145,9 @@ hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_
 // of those products as rounded, sums are of 2^(z log2(e) - m), where a fused
 // multiply-add rounds the difference only.
 //
-// The product bounds it: 8192 x 32000 x 2048 takes 940 us without the logits and
-// 1000 to 1090 with them (1.05 GB), 838 stored in bf16 without statistics.  3 x
+// The product bounds it: 8192 x 28160 x 2048 takes 773 us without the logits (1.22
+// PFLOP/s), 8192 x 32000 x 2048 970 to 1090 with them (1.05 GB), 838 stored in bf16
+// without statistics.  3 x
 // 32000 x 2048 takes 21 us, the weights from the last-level cache.
 struct CeStatsArgs {
   const int64_t* targets;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int co
 
 // ------------------------------------------------------------ dz
 // Written as rows for dx and as columns for dw, both as whole lines.  From a
-// second product: 8192 x 8000 x 2048 302 us, of which the product is 210.
+// second product: 8192 x 28160 x 2048 996 us, of which the product is 740.
 struct CeGradArgs {
   const int64_t* targets;
   int64_t col0;

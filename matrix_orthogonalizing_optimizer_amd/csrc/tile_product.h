@@ -437,8 +437,9 @@ struct StoreArgs {
   int stream;                    // past the caches
 };
 // Outputs larger than the L2s whose rows are whole lines: 8192 x 32000 x 2048 in
-// bf16 (524 MB) 1034 to 958 us, 8192 x 8192 x 8192 843 to 822.  Rows that share
-// lines lose: dw of 129283 x 2045 in fp32 takes 12% longer past the caches.
+// bf16 (524 MB) 918 to 878 us, 8192 x 8192 x 8192 816 to 812.  Rows that share
+// lines gain nothing (129283 x 2045 x 1022 in three terms to fp32 1470 us both ways) and meet in
+// the caches.
 template <typename T>
 int worth_streaming(const T* out, int64_t ldo, int64_t m, int64_t n) {
   constexpr int kSize = sizeof(T);
