@@ -122,6 +122,7 @@ def test_strided_operands_and_accumulation(dwd):
     (50, 130, 1400001, F32, F32),         # weights copied for each product, logits computed twice
     (24, 20000, 27001, F32, BF16),        # the same with kept logits, several pieces of weights
     (40, 20000, 53000, BF16, F32),        # ones that are read in place
+    (8192, 256, 131000, BF16, BF16),      # kept logits of 4.3 GB
     (40, 4096, 33000, BF16, F32),         # kept logits
     (24, 4100, 33000, F32, BF16),
     (4500, 128, 15001, BF16, BF16),       # computed twice, odd columns
