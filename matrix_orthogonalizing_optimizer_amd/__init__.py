@@ -27,6 +27,7 @@ arithmetic step runs in the HIP library, and there is no fallback.
 from __future__ import annotations
 
 import contextlib
+import copy
 import ctypes
 import functools
 import threading
@@ -732,6 +733,19 @@ class Fp8Matrix:
             q._ptrs, q._image = (base + at, base + at + codes), None
             made.append(q)
         return made
+
+    # A copy's addresses are its own arrays': they are found again, not copied.
+    def __copy__(self) -> "Fp8Matrix":
+        return Fp8Matrix(self.codes, self.scales, self.cols)
+
+    def __deepcopy__(self, memo) -> "Fp8Matrix":
+        return Fp8Matrix(copy.deepcopy(self.codes, memo), copy.deepcopy(self.scales, memo), self.cols)
+
+    def __reduce__(self):
+        codes, scales = self.codes, self.scales
+        if self._at is not None:                # out of an allocation that would be stored whole
+            codes, scales = codes.clone(), scales.clone()
+        return Fp8Matrix, (codes, scales, self.cols)
 
     def _struct(self):                          # mo_fp8_image
         if self._image is None:
