@@ -23,7 +23,7 @@ namespace {
 
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 // dz enters its products as a sum of bf16 terms: one where the gradient is
 // bf16 itself (its rounding, 2^-9 of a value, is of the size of the result's
@@ -141,9 +141,10 @@ hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_
 }
 
 // ------------------------------------------------------------ statistics
-// Exponentials are powers of two of z log2(e): a row's reference m is the largest
-// of those products as rounded, sums are of 2^(z log2(e) - m), where a fused
-// multiply-add rounds the difference only.
+// A row's reference m is its largest logit, sums are of exp(z - m): the difference
+// first, as the rounding of a product z log2(e) passes every exponent from logits
+// of 2^31 on.  (z log2(e) - m' in one multiply-add saves nothing: 8192 x 32000 x 2048
+// 3075 us either way, logits multiplied again, x 128, 838 instead of 834.)
 //
 // The product bounds it: 8192 x 28160 x 2048 takes 773 us without the logits (1.22
 // PFLOP/s), 8192 x 32000 x 2048 970 to 1090 with them (1.05 GB), 838 stored in bf16
@@ -159,10 +160,13 @@ struct CeStatsArgs {
   int stream_z;
 };
 
+// exp(z - ref), where z is not above ref.
+__device__ __forceinline__ float exp_below(float z, float ref) { return __builtin_amdgcn_exp2f((z - ref) * kLog2e); }
+
 // Adds (m2, s2) to (m, s).  References of -inf stand for columns of -inf only.
 __device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
   const float n = fmaxf(m, m2), ref = n == -INFINITY ? 0.0f : n;
-  s = s * __builtin_amdgcn_exp2f(m - ref) + s2 * __builtin_amdgcn_exp2f(m2 - ref);
+  s = s * exp_below(m, ref) + s2 * exp_below(m2, ref);
   m = n;
 }
 
@@ -193,13 +197,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
-    m = fmaxf(m, __uint_as_float(lane_xor32(__float_as_uint(m)))) * kLog2e;
+    m = fmaxf(m, __uint_as_float(lane_xor32(__float_as_uint(m))));
     const float ref = m == -INFINITY ? 0.0f : m;            // columns of -inf alone: a sum of zero
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -ref));
+      for (int r = 0; r < 16; ++r) s += exp_below(acc[i][j][r], ref);
     s += __uint_as_float(lane_xor32(__float_as_uint(s)));
     const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
     const bool in = row <= q.mlast;
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int co
     const float r = g ? g[t] : 1.0f;
     factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= vocab ? NAN : r / *scale;
   }
-  loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + __builtin_fmaf(-target_logit[t], kLog2e, m) * kLn2;
+  loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + (m - target_logit[t]);
 }
 
 // ------------------------------------------------------------ dz
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
-        float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -st.x)) * st.y;
+        float v = exp_below(acc[i][j][r], st.x) * st.y;
         v = f * (c == hot ? v - 1.0f : v);
         acc[i][j][r] = f == 0.0f || c >= inside ? 0.0f : v;
       }
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
     const int64_t y = in ? e.targets[t] - e.col0 - c : -1;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float x = __builtin_amdgcn_exp2f(__builtin_fmaf(k < 4 ? lo[k] : hi[k - 4], kLog2e, -st.x)) * st.y;
+      float x = exp_below(k < 4 ? lo[k] : hi[k - 4], st.x) * st.y;
       x = f * (k == y ? x - 1.0f : x);
       v[i][k] = f == 0.0f || c + k >= cols ? 0.0f : x;
     }
