@@ -535,11 +535,14 @@ int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int o
  *   dz_tv   = g_t (exp(z_tv) / sum_v exp(z_tv) - [v = y_t]),
  *   dx = dz w,   dw = dz^T x  (+ dw when accumulate != 0).
  * The products take bf16 operands: x and w given in fp32 are rounded to bf16
- * on the way (values below 2^-126 count as zero).  Sums and the softmax's statistics are fp32.  dz enters the
- * products for a bf16 gradient rounded to bf16 (relative to the largest |g|),
- * for an fp32 gradient as a sum of three bf16 terms.  Each gradient is rounded
- * once to its type (after the accumulation).  Results do not depend on the run
- * (no atomics).
+ * on the way (values below 2^-126 count as zero).  Sums and the softmax's
+ * statistics are fp32; the target's share of them is made of the other columns,
+ * so that the loss and dz of a token of p near 1 keep the digits of 1 - p.  dz
+ * enters the products for a bf16 gradient rounded to bf16, for an fp32 gradient
+ * as a sum of three bf16 terms, in both cases relative to the largest |g| of the
+ * rows that take part: what is below 2^-126 of that counts as zero.  Each gradient
+ * is rounded once to its type (after the accumulation).  Results do not depend on
+ * the run (no atomics).
  *
  * A row with a negative target takes no part: loss 0, dx 0 and nothing in dw,
  * whatever its x holds.  g_t = 0 does the same to the row's gradients.  A

@@ -28,7 +28,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // dz enters its products as a sum of bf16 terms: one where the gradient is
 // bf16 itself (its rounding, 2^-9 of a value, is of the size of the result's
 // own), three where it is fp32 (2^-26: x and W are exact in bf16, so that the
-// fp32 sums are the only other error).
+// statistics and the fp32 sums are the only other errors).
 constexpr int terms_of(int dt) { return dt == F32 ? 3 : 1; }
 
 // LDS that only one wave uses: the hardware keeps the wave's accesses in order,
@@ -144,7 +144,10 @@ hipError_t pack(int dt, const void* src, int64_t ld, int rows, int cols, uint16_
 // A row's reference m is its largest logit, sums are of exp(z - m): the difference
 // first, as the rounding of a product z log2(e) passes every exponent from logits
 // of 2^31 on.  (z log2(e) - m' in one multiply-add saves nothing: 8192 x 32000 x 2048
-// 3075 us either way, logits multiplied again, x 128, 838 instead of 834.)
+// 3075 us either way, logits multiplied again, x 128, 838 instead of 834.)  The
+// target's column stays out of both and joins them last: a likely token's loss and
+// dz are made of the other columns' sum, as 1 - p of a rounded p has none of their
+// digits left.
 //
 // The product bounds it: 8192 x 28160 x 2048 takes 773 us without the logits (1.22
 // PFLOP/s), 8192 x 32000 x 2048 970 to 1090 with them (1.05 GB), 838 stored in bf16
@@ -154,7 +157,7 @@ struct CeStatsArgs {
   const int64_t* targets;
   int64_t col0;                 // the piece's first column
   float2* part;                 // [rows][tiles_n]: reference, sum
-  float* target_logit;          // written by the tile that holds the row's target
+  float* target;                // the target's logit, written by the tile that holds it
   float* z;                     // or null: the logits, rows `pitch_z` apart
   int64_t pitch_z;
   int stream_z;
@@ -192,6 +195,24 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
         for (int r = 0; r < 16; ++r)
           if (32 * j + 8 * (r / 4) + 4 * q.half + r % 4 >= inside) acc[i][j][r] = -INFINITY;
     }
+    const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
+    const bool in = row <= q.mlast;
+    const int64_t t = q.m0 + row;
+    // the target's logit, where these columns hold it, goes by itself
+    const int64_t y = in ? e.targets[t] - e.col0 - q.n0 - q.wn * W : -1;
+    const bool mine = y >= 0 && y < min(W, inside) && ((y >> 2) & 1) == q.half;
+    if (__any(mine)) {
+      float z = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (mine && y == 32 * j + 8 * (r / 4) + 4 * q.half + r % 4) {
+            z = acc[i][j][r];
+            acc[i][j][r] = -INFINITY;
+          }
+      if (mine) e.target[t] = z;
+    }
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
@@ -205,22 +226,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
 #pragma unroll
       for (int r = 0; r < 16; ++r) s += exp_below(acc[i][j][r], ref);
     s += __uint_as_float(lane_xor32(__float_as_uint(s)));
-    const int row = q.wm * (C::TM / C::WM) + 32 * i + q.r32;
-    const bool in = row <= q.mlast;
-    const int64_t t = q.m0 + row;
     if (q.half == 0) waves[row * C::WN + q.wn] = make_float2(m, s);
-    // the target's logit, where these columns hold it
-    const int64_t y = in ? e.targets[t] - e.col0 - q.n0 - q.wn * W : -1;
-    const bool mine = y >= 0 && y < min(W, inside) && ((y >> 2) & 1) == q.half;
-    if (__any(mine)) {
-      float z = 0.0f;
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (y == 32 * j + 8 * (r / 4) + 4 * q.half + r % 4) z = acc[i][j][r];
-      if (mine) e.target_logit[t] = z;
-    }
   }
   __syncthreads();
   for (int row = threadIdx.x; row <= q.mlast; row += C::kThreads) {
@@ -231,13 +237,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_stats_kernel(con
 }
 
 // Joins a piece's statistics with those of the pieces before it, kLanes
-// threads per row; after the last piece the row's {m, 1 / sum}, its loss and its
-// weight in dz: 0 where it takes no part, NaN for a target that is no column.
+// threads per row; after the last piece, with the target's logit, the row's {m, 1 /
+// sum}, p - 1 of its target (in the logit's place), its loss and its weight in dz: 0
+// where it takes no part, NaN for a target that is no column.
 // Latency bound: 3 rows of 500 tiles take 3.2 us with 256 threads to a row and 5.7
 // with 16, 1021 of 506 4.8 and 6.8, 8192 of 125 10.8 and 4.9.
 template <int kLanes>
 __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int cols, int rows, int vocab, int first, int last,
-                                                      const int64_t* targets, const float* target_logit, float2* stat, float* loss,
+                                                      const int64_t* targets, float* target, float2* stat, float* loss,
                                                       const float* g, const float* scale, float* factor) {
   __shared__ float2 waves[4];
   const int lane = threadIdx.x % kLanes;
@@ -279,14 +286,19 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* part, int co
     return;
   }
   // -inf alone, or a NaN or +inf anywhere, gives NaN
-  const bool none = m == -INFINITY;
-  stat[t] = make_float2(m, none ? NAN : 1.0f / s);
   const int64_t y = targets[t];
+  const bool column = y >= 0 && y < vocab;
+  const float z = column ? target[t] : -INFINITY, top = fmaxf(m, z);
+  const bool none = top == -INFINITY;
+  const float rest = s * exp_below(m, none ? 0.0f : top), own = column ? exp_below(z, none ? 0.0f : top) : 0.0f;
+  const float inv = none ? NAN : 1.0f / (rest + own);
+  stat[t] = make_float2(top, inv);
+  target[t] = -rest * inv;
   if (factor) {
     const float r = g ? g[t] : 1.0f;
     factor[t] = y < 0 || r == 0.0f ? 0.0f : y >= vocab ? NAN : r / *scale;
   }
-  loss[t] = y < 0 ? 0.0f : y >= vocab || none ? NAN : logf(s) + (m - target_logit[t]);
+  loss[t] = y < 0 ? 0.0f : !column || none ? NAN : (z == top ? log1pf(rest) : logf(rest + own)) + (top - z);
 }
 
 // ------------------------------------------------------------ dz
@@ -296,6 +308,7 @@ struct CeGradArgs {
   const int64_t* targets;
   int64_t col0;
   const float2* stat;
+  const float* target;          // p - 1 of the target's column
   const float* factor;
   uint16_t* dz;                 // [rows]: terms_x times vp, rows pitch_x apart
   uint16_t* dz_t;               // [columns]: terms_w times tp, pitch_w apart
@@ -329,6 +342,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
     const int64_t t = q.m0 + (in ? row : 0);
     const float f = in ? e.factor[t] : 0.0f;
     const float2 st = e.stat[t];
+    const float there = e.target[t];
     const int64_t y = e.targets[t] - e.col0 - q.n0 - q.wn * W;
     const int hot = y >= 0 && y < W ? static_cast<int>(y) : -1;
 #pragma unroll
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinWaves) ce_grad_kernel(cons
       for (int r = 0; r < 16; ++r) {
         const int c = 32 * j + 8 * (r / 4) + 4 * q.half + r % 4;
         float v = exp_below(acc[i][j][r], st.x) * st.y;
-        v = f * (c == hot ? v - 1.0f : v);
+        v = f * (c == hot ? there : v);
         acc[i][j][r] = f == 0.0f || c >= inside ? 0.0f : v;
       }
     for (int term = 0; term < terms; ++term) {
@@ -411,11 +425,12 @@ __global__ void __launch_bounds__(256) ce_kept_grad_kernel(const CeGradArgs e, c
     }
     const float f = in ? e.factor[t] : 0.0f;
     const float2 st = in ? e.stat[t] : make_float2(0.0f, 0.0f);
+    const float there = in ? e.target[t] : 0.0f;
     const int64_t y = in ? e.targets[t] - e.col0 - c : -1;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float x = exp_below(k < 4 ? lo[k] : hi[k - 4], st.x) * st.y;
-      x = f * (k == y ? x - 1.0f : x);
+      x = f * (k == y ? there : x);
       v[i][k] = f == 0.0f || c + k >= cols ? 0.0f : x;
     }
   }
@@ -839,7 +854,7 @@ hipError_t launch_linear_ce(const LinearCeArgs& a, void* ws, hipStream_t s) {
     if (need_w || need_w_t)
       MO_TRY(copied ? pack(BF16, operand(v0), pl.ph, v, a.hidden, nullptr, 0, w_t, pv, {}, s)
                     : pack(a.w_dt, weights(v0), a.ldw, v, a.hidden, need_w ? wb : nullptr, pl.ph, need_w_t ? w_t : nullptr, pv, {}, s));
-    const CeGradArgs e{a.targets, v0, stat, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp),
+    const CeGradArgs e{a.targets, v0, stat, zt, factor, dz, dz_t, pl.terms_x, pl.terms_w, static_cast<int>(vp), static_cast<int>(pl.tp),
                        apart(vp * pl.terms_x), apart(pl.tp * pl.terms_w)};
     if (pl.keep) {
       const dim3 g(static_cast<uint32_t>((v + kPackCols - 1) / kPackCols), static_cast<uint32_t>((a.rows + kPackRows - 1) / kPackRows));
