@@ -528,7 +528,8 @@ int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int o
                   int64_t ldo, int accumulate, void* stream);
 
 /* ------------------------------------------------------------------------
- * Cross entropy of a linear layer's logits, without logits of the caller's.
+ * Cross entropy of a linear layer's logits, which no caller holds: for the time of
+ * the call they may be in its workspace, as below.
  *
  * x [rows, hidden], w [vocab, hidden], z = x w^T.  Per row t with target y_t:
  *   loss[t] = log sum_v exp(z_tv) - z_{t, y_t},
@@ -554,9 +555,10 @@ int mo_fp8_matmul(const mo_fp8_image* a, const mo_fp8_image* b, void* out, int o
 
 /* Workspace of mo_linear_ce.  want_dx, want_dw: whether the call gives dx and
  * dw; dx has x's dtype.  With gradients it holds, beside copies of x and sums of
- * dx, up to 1 GiB each of the weights, their transpose and dz (1024 columns of it
- * at least), and up to 4 GiB of logits in fp32: all of them, or none, and then
- * they are computed twice.  Host-only. */
+ * dx, up to 1 GiB each of the weights, their transpose and dz (1024 columns at
+ * least; the padding of their rows comes on top), and up to 4 GiB of logits in
+ * fp32, the vocabulary rounded up to 64: all of them, or none, and then they are
+ * computed twice.  Host-only. */
 int mo_linear_ce_workspace_size(int64_t rows, int64_t hidden, int64_t vocab, int x_dtype,
                                 int dw_dtype, int want_dx, int want_dw, size_t* bytes);
 

@@ -701,14 +701,16 @@ Plan make_plan(int64_t rows, int64_t hidden, int64_t vocab, int x_dt, int dw_dt,
   // being multiplied again: 8192 x 32000 x 2048 4.04 to 3.36 ms, 8192 x 128256 x
   // 2048 15.8 to 13.1.  Where the product is quicker than that writing and
   // reading (x 256 1.12 and 1.08 ms, x 128 0.90 and 0.93), they stay only where
-  // the last-level cache holds them.
+  // the last-level cache holds them.  Their rows are not spread over the channels as
+  // the operands' are, which gains nothing here (8192 x 131072 x 256 4.47 ms either
+  // way, 8192 x 32768 x 2048 2.95) and would pass the 4 GiB.
   const int64_t r = std::max<int64_t>(rows, 1), vocab_p = up(vocab, 64);
   const int64_t held = int64_t{1} << (hidden >= 256 ? 30 : 26);
   p.keep = (dx || dw) && vocab_p <= held && r <= held / vocab_p;
   const int64_t terms = std::max(p.terms_x + p.terms_w, 2);
   const int64_t by_w = (int64_t{1} << 29) / p.hp, by_z = (int64_t{1} << 29) / (terms * r);
   p.vb = piece_of(vocab, std::min(std::max(std::min(by_w, by_z) / 256 * 256, int64_t{1024}), int64_t{1} << 20));
-  p.pz = (vocab_p / 64 | 1) * 64;
+  p.pz = vocab_p;
   // with gradients a copy of up to 1 GiB is made once, not once for each product
   p.keep_w = (dx || dw) && vocab <= (int64_t{1} << 29) / p.ph;
   p.vf = piece_of(vocab, std::max((int64_t{1} << 28) / std::max<int64_t>(rows, 1) / 256 * 256, int64_t{4096}));

@@ -45,3 +45,14 @@ def test_gradients_past_the_caches(t, h, v, dwd, accumulate):
     add = dw.clone() if accumulate else None
     loss, dx, _ = mo.linear_cross_entropy(x, w, y, grad_loss=g, dw=dw, accumulate=accumulate)
     _check(x, w, y, g, loss, dx, dw, add)
+
+
+def test_the_largest_logits_that_are_kept():
+    """4 GiB of them, to the last byte: the last row's target is the last column."""
+    x, w, y, g = _inputs(8192, 256, 131072, 25)
+    y[-1], y[-2], y[0] = 131071, 131070, 131071
+    loss, dx, dw = mo.linear_cross_entropy(x, w, y, grad_loss=g)
+    _check(x, w, y, g, loss, dx, dw)
+    # its loss alone, from no kept logits
+    one = mo.linear_cross_entropy(x[-1:], w, y[-1:], grad=False)[0]
+    _check(x[-1:], w, y[-1:], None, one, None, None)
