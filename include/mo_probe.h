@@ -46,6 +46,11 @@ int mo_probe_mfma_bf16_random(int iters, int reps, double* tflops);
  * *tflops = 131072 flop x MFMAs / seconds; best of `reps` launches. */
 int mo_probe_mfma_fp4(int random_codes, int iters, int reps, double* tflops);
 
+/* The same for 8-bit (e4m3) operands, as in the products of FP8 images: codes that
+ * are all zero (codes = 0), random ones (1), or those of normal values under a
+ * block's scale (2), four operands per side cycled.  Same units and outputs. */
+int mo_probe_mfma_fp8(int codes, int iters, int reps, double* tflops);
+
 /* HBM rates over a buffer of `bytes` (rounded down to 64 KiB):
  * *read_gbs: a read-only reduction of the whole buffer (16-byte loads);
  * *copy_gbs: a copy into a second buffer, counted as read + write bytes.

@@ -1,5 +1,5 @@
-// Roofline probes (declared in include/mo_probe.h): the bf16 and 4-bit matrix-core
-// rates and the HBM streaming rates the chip sustains on their own.
+// Roofline probes (declared in include/mo_probe.h): the bf16, 4-bit and 8-bit
+// matrix-core rates and the HBM streaming rates the chip sustains on their own.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -132,6 +132,58 @@ __global__ __launch_bounds__(256) void mfma_fp4_probe_kernel(float* out, int ite
   out[blockIdx.x * blockDim.x + threadIdx.x] = s;
 }
 
+// The same instruction on 8-bit (e4m3) operands: codes that are all zero, random
+// ones (no NaN), or those of normal values scaled as a block of 128 is, whose
+// largest, 2.7 standard deviations on average, lies between 224 and 448.
+typedef short i16x2_t __attribute__((ext_vector_type(2)));
+enum Fp8Codes { kZeroCodes, kRandomCodes, kNormalCodes };
+__device__ inline float probe_normal(unsigned h) {        // Box and Muller's transform of two uniform numbers
+  const float u = (static_cast<float>(h >> 16) + 0.5f) / 65536.0f, v = static_cast<float>(h & 0xffffu) / 65536.0f;
+  return sqrtf(-2.0f * logf(u)) * cosf(6.2831853f * v);
+}
+template <Fp8Codes kCodes>
+__device__ inline int probe_fp8_quad(unsigned h) {
+  if constexpr (kCodes == kZeroCodes) return 0;
+  if constexpr (kCodes == kRandomCodes) {
+    unsigned v = probe_hash(h);
+    for (int i = 0; i < 4; ++i)
+      if (((v >> (8 * i)) & 0x7fu) == 0x7fu) v ^= 1u << (8 * i);
+    return static_cast<int>(v);
+  }
+  float f[4];
+  for (int i = 0; i < 4; ++i) f[i] = fminf(fmaxf(130.0f * probe_normal(probe_hash(4u * h + i)), -448.0f), 448.0f);
+  i16x2_t r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, f[0], f[1], 1.0f, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, f[2], f[3], 1.0f, true);
+  return __builtin_bit_cast(int, r);
+}
+template <Fp8Codes kCodes>
+__global__ __launch_bounds__(256) void mfma_fp8_probe_kernel(float* out, int iters) {
+  const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
+  constexpr int kFp8Ops = 4;                              // of 8 registers each
+  i32x8_t a[kFp8Ops], b[kFp8Ops];
+#pragma unroll
+  for (int o = 0; o < kFp8Ops; ++o)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      a[o][k] = probe_fp8_quad<kCodes>(t * 64u + o * 16u + k);
+      b[o][k] = probe_fp8_quad<kCodes>((t * 64u + o * 16u + 8u + k) ^ 0x9e3779b9u);
+    }
+  f32x16_t acc[kChains];
+  for (int c = 0; c < kChains; ++c)
+    for (int r = 0; r < 16; ++r) acc[c][r] = 0.0f;
+  for (int i = 0; i < iters; ++i) {
+#pragma unroll
+    for (int k = 0; k < kPerIter; ++k)
+      acc[k % kChains] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          a[k % kFp8Ops], b[(k + k / kFp8Ops + 1) % kFp8Ops], acc[k % kChains], 0, 0, 0, kUnitScale, 0, kUnitScale);
+  }
+  float s = 0.0f;
+  for (int c = 0; c < kChains; ++c)
+    for (int r = 0; r < 16; ++r) s += acc[c][r];
+  out[blockIdx.x * blockDim.x + threadIdx.x] = s;
+}
+
 // Streaming kernels: each pass of the grid covers gridDim.x * 256 * U
 // consecutive 16-byte words, thread t of a block taking words t, t + 256,
 // .. t + 256 (U - 1) of its block's span (coalesced), U loads in flight
@@ -257,6 +309,17 @@ int mo_probe_mfma_bf16_random(int iters, int reps, double* tflops) {
 
 int mo_probe_mfma_fp4(int random_codes, int iters, int reps, double* tflops) {
   return mfma_probe(random_codes ? mfma_fp4_probe_kernel<true> : mfma_fp4_probe_kernel<false>, 131072.0, iters, reps, tflops);
+}
+
+int mo_probe_mfma_fp8(int codes, int iters, int reps, double* tflops) {
+  if (codes < kZeroCodes || codes > kNormalCodes) {
+    g_probe_err = "codes must be 0, 1 or 2";
+    return -2;
+  }
+  return mfma_probe(codes == kZeroCodes     ? mfma_fp8_probe_kernel<kZeroCodes>
+                    : codes == kRandomCodes ? mfma_fp8_probe_kernel<kRandomCodes>
+                                            : mfma_fp8_probe_kernel<kNormalCodes>,
+                    131072.0, iters, reps, tflops);
 }
 
 int mo_probe_hbm(size_t bytes, int reps, double* read_gbs, double* copy_gbs) {
