@@ -609,7 +609,7 @@ def mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, *, out_dtype: torch.dtype = torch.bfl
 
 
 def _flat2(x: torch.Tensor) -> torch.Tensor:
-    return x if x.dim() == 2 else x.view(-1, x.shape[-1])
+    return x if x.dim() == 2 else x.view(x.shape[:-1].numel(), x.shape[-1])
 
 
 def mx4_linear(x: torch.Tensor, w: Mx4Matrix, *, out_dtype: torch.dtype = torch.bfloat16,
