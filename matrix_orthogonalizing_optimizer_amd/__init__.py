@@ -11,8 +11,8 @@ weights needs: microscaled 4-bit images of matrices and their products
 (``mx4_*``), token log probabilities with the top alternatives, and the
 distillation loss with its gradient.  For training in 8 bits: 8-bit floating
 point images with a scale per block of 128 and their products (``fp8_*``), the
-cross entropy of an LM head without its logits, and a router's balance loss
-with its experts' counts.
+cross entropy of an LM head from its input and weights, which leaves no logits
+behind, and a router's balance loss with its experts' counts.
 
 No function here takes part in autograd: results carry no graph, also where
 an argument requires a gradient.  The backward passes are calls of their own
@@ -861,7 +861,8 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, *, out_dtype: torch.dtype = torch.bfl
     """``a b^T`` over the values of two images with equal columns
     (``mo_fp8_matmul``): a [M, K], b [N, K] give [M, N], fp32 sums rounded
     once; fp32 results from exact products, bf16 ones from the 8-bit matrix
-    instruction.  ``out``: written instead of a new tensor (its dtype counts,
+    instruction, which cuts small products beside large ones (``include/muon.h``
+    says where).  ``out``: written instead of a new tensor (its dtype counts,
     rows may be strided); with ``accumulate`` the product is added to it."""
     if not isinstance(a, Fp8Matrix) or not isinstance(b, Fp8Matrix):
         raise TypeError("a and b must be Fp8Matrix")
@@ -1054,7 +1055,9 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     ``accumulate`` adds to ``dw``.  Not seen by autograd: pass the gradients on
     yourself.  For the time of the call, gradients take a workspace: copies of
     the operands, up to 1 GiB of the logits' gradient, and the logits in fp32
-    where 4 GiB hold them (computed twice where not)."""
+    where 4 GiB hold them (computed twice where not): 2.5 GB for 8192 rows of
+    2048 and a vocabulary of 32000, more than the logits alone in bf16 (0.5 GB).
+    The gradients are formed relative to the largest ``|grad_loss|``."""
     if grad not in _GRADS:
         raise ValueError(f"grad must be one of {_GRADS}")
     x2 = _flat2(x)
